@@ -17,6 +17,14 @@ this package is its Python binding.  Entry points (same names as the C functions
   fp8q_dequant_w_128x128(q, s)                 E4M3 [N, K] + fp32 [N/128, K/128] -> bf16 [N, K]
   fp8q_moe_route_topk(logits, k)               top-k experts and the expert-sorted, 128-padded row layout
   fp8q_moe_gather_fp8(q, s, row_of, row_token, offsets)   quantized token rows in that layout (FP8 dispatch)
+  fp8q_moe_gate_topk(logits, k, score, bias, n_group, ...)   scores, group-limited top-k, weights and that layout
+  fp8q_moe_gate_backward(logits, topk_idx, grad_weight)      gradient of the weights -> of the logits
+  fp8q_moe_combine(c, row_of, weight, add)     expert rows weighted and added up per token
+  fp8q_moe_combine_backward(grad_y, c, row_of, weight, row_token, offsets)   its gradient: expert rows, weights
+  fp8q_quant_int8(x)                           bf16 [M, K] -> (INT8 [M, K], one fp32 scale per row [M])
+  fp8q_gemm_int8(qa, sa, qw, sw)               INT8 product with scales per token and channel, bf16 or fp32 [M, N]
+  fp8q_grouped_gemm_int8(qa, sa, qw, sw, offsets)            the same per expert segment
+  fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets)   the same, reading token rows directly
 """
 from ._binding import (  # noqa: F401
     OUT_BF16,
@@ -26,6 +34,13 @@ from ._binding import (  # noqa: F401
     fp8q_gemm_blockscaled,
     fp8q_grouped_gemm_blockscaled,
     fp8q_grouped_gemm_blockscaled_gather,
+    fp8q_gemm_int8,
+    fp8q_grouped_gemm_int8,
+    fp8q_grouped_gemm_int8_gather,
+    fp8q_moe_combine,
+    fp8q_moe_combine_backward,
+    fp8q_moe_gate_backward,
+    fp8q_moe_gate_topk,
     fp8q_moe_gather_fp8,
     fp8q_moe_route_capacity,
     fp8q_moe_route_topk,
@@ -34,6 +49,7 @@ from ._binding import (  # noqa: F401
     fp8q_quant_act_dual,
     fp8q_quant_act_e5m6_1x128,
     fp8q_quant_act_fp4_1x128,
+    fp8q_quant_int8,
     fp8q_quant_w_128x128,
     fp8q_quant_w_fp4_128x128,
     fp8q_quant_w_per_channel,

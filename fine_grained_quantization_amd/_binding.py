@@ -49,6 +49,22 @@ def load_library(path: str = LIB_PATH):
         lib.fp8q_moe_route_topk.argtypes = [P, I64, I64, I64, P, P, P, P, I64, P, I64, P]
         lib.fp8q_moe_gather_fp8.argtypes = [P, P, I64, I64, I64, P, P, P, I64, I64, P, P, P]
         lib.fp8q_moe_route_topk_noalloc.argtypes = [P, I64, I64, I64, P, P, P, P, I64, P]
+        F = ctypes.c_float
+        lib.fp8q_moe_gate_topk.argtypes = [P, I, I64, I64, I64, I64, I, P, I64, I64, I64, I, F, P, P, P, P, P, I64, P,
+                                           P, I64, P]
+        lib.fp8q_moe_gate_backward.argtypes = [P, I, I64, I64, I64, I64, I, I, F, P, P, P, P]
+        lib.fp8q_moe_combine.argtypes = [P, I, I64, I64, P, P, I64, I64, P, P, P]
+        lib.fp8q_moe_combine_backward.argtypes = [P, P, I, I64, I64, P, P, I64, I64, P, P, I64, P, P, P]
+        lib.fp8q_quant_int8.argtypes = [P, I64, I64, I64, P, P, P]
+        lib.fp8q_gemm_int8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
+        lib.fp8q_grouped_gemm_int8.argtypes = [P, P, P, P, P, I, P, I64, I64, I64, I64, P]
+        lib.fp8q_grouped_gemm_int8_gather.argtypes = [P, P, I64, P, P, P, P, I, P, I64, I64, I64, I64, P]
+        for f in (lib.fp8q_moe_gate_topk, lib.fp8q_moe_gate_backward, lib.fp8q_moe_combine,
+                  lib.fp8q_moe_combine_backward, lib.fp8q_quant_int8, lib.fp8q_gemm_int8, lib.fp8q_grouped_gemm_int8,
+                  lib.fp8q_grouped_gemm_int8_gather):
+            f.restype = ctypes.c_int
+        lib.fp8q_moe_gate_workspace_bytes.argtypes = [I64, I64]
+        lib.fp8q_moe_gate_workspace_bytes.restype = I64
         for f in (lib.fp8q_quant_act_1x128, lib.fp8q_quant_w_128x128, lib.fp8q_swiglu_quant_act_1x128,
                   lib.fp8q_swiglu_bf16, lib.fp8q_quant_act_dual, lib.fp8q_quant_act_fp4_1x128,
                   lib.fp8q_quant_w_fp4_128x128, lib.fp8q_quant_w_per_channel, lib.fp8q_quant_act_e5m6_1x128,
@@ -282,7 +298,7 @@ def _need_rows(t, name):
     """A bf16 [M, K] device view whose rows are contiguous (any row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _BF16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 device tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
 
 
@@ -508,3 +524,232 @@ def fp8q_moe_gather_fp8(q, s, row_of, row_token, offsets, qa=None, sa=None, stre
                                               _ptr(offsets), E, rows, _ptr(qa), _ptr(sa), _stream_ptr(stream)),
            "fp8q_moe_gather_fp8")
     return qa, sa
+
+
+_FLOAT = (torch.bfloat16, torch.float32)
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _score_code(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return _SCORES[score]
+
+
+def _need_out(t, name, dtype, size):
+    """A contiguous device tensor of one dtype and element count (an output, or an input of known size)."""
+    _need(t, name, (dtype,))
+    if t.numel() != size:
+        raise ValueError(f"{name} has {t.numel()} elements; expected {size}")
+
+
+def _need_logits(x):
+    """fp32 or bf16 logits [T, E] whose rows are contiguous (any row stride >= E); returns that stride."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in _FLOAT or x.dim() != 2:
+        raise ValueError("logits must be a 2-D float32 or bfloat16 device tensor")
+    T, E = x.shape
+    if T > 0 and E > 1 and x.stride(1) != 1:
+        raise ValueError("logits must have contiguous rows")
+    ld = x.stride(0) if T > 1 else E
+    if ld < E:
+        raise ValueError("logits must not overlap between rows")
+    return ld
+
+
+def fp8q_moe_gate_topk(logits, k: int, score: str = "sigmoid", bias=None, n_group: int = 1, topk_group: int = 1,
+                       group_top: int = 2, renormalize: bool = True, scale: float = 1.0, rows: int | None = None,
+                       workspace=None, out=None, stream=None):
+    """Gating with scores, bias, groups and weights, and the expert-sorted layout.  ``logits`` float32 or bf16
+    [T, E] (rows may be strided), ``bias`` float32 [E] or None -> ``(topk_idx int32 [T, k], topk_weight float32
+    [T, k], offsets int32 [E+1], row_of int32 [T, k], row_token int32 [rows], load int32 [E])``.
+
+    ``score`` is "sigmoid" or "softmax"; the choice goes by score + bias within the ``topk_group`` best of
+    ``n_group`` groups (a group's value is the sum of its ``group_top`` largest keys), the weights are the chosen
+    scores, divided by their sum if ``renormalize``, times ``scale``.  Experts whose logit is -inf or NaN are never
+    chosen; slots without an expert get expert -1, weight 0 and row -1.  ``rows`` defaults to
+    :func:`fp8q_moe_route_capacity`; ``workspace`` (``fp8q_moe_gate_workspace_bytes(T, E)`` bytes) and ``out`` (the
+    six outputs) are allocated when not given."""
+    ld = _need_logits(logits)
+    T, E = logits.shape
+    lib = load_library()
+    code = _score_code(score)
+    if group_top not in (1, 2):
+        raise ValueError(f"group_top must be 1 or 2, got {group_top}")
+    if bias is not None:
+        _need_out(bias, "bias", torch.float32, E)
+    if rows is None:
+        rows = fp8q_moe_route_capacity(T, E, k)
+    wbytes = lib.fp8q_moe_gate_workspace_bytes(T, E)
+    if wbytes < 0:
+        raise ValueError(f"invalid gating sizes T={T} E={E}")
+    if workspace is None:
+        workspace = torch.empty(max(wbytes, 4), dtype=torch.uint8, device=logits.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=logits.device)
+        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=logits.device),
+               torch.empty(E + 1, **i32), torch.empty((T, k), **i32), torch.empty(rows, **i32), torch.empty(E, **i32))
+    topk_idx, topk_weight, offsets, row_of, row_token, load = out
+    _need_out(topk_idx, "topk_idx", torch.int32, T * k)
+    _need_out(topk_weight, "topk_weight", torch.float32, T * k)
+    _need_out(offsets, "offsets", torch.int32, E + 1)
+    _need_out(row_of, "row_of", torch.int32, T * k)
+    _need_out(row_token, "row_token", torch.int32, rows)
+    _need_out(load, "load", torch.int32, E)
+    _check(lib.fp8q_moe_gate_topk(_ptr(logits), _out_code(logits.dtype), ld, T, E, k, code, _ptr(bias), n_group,
+                                  topk_group, group_top, 1 if renormalize else 0, scale, _ptr(topk_idx),
+                                  _ptr(topk_weight), _ptr(offsets), _ptr(row_of), _ptr(row_token), rows, _ptr(load),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream_ptr(stream)), "fp8q_moe_gate_topk")
+    return topk_idx, topk_weight, offsets, row_of, row_token, load
+
+
+def fp8q_moe_gate_backward(logits, topk_idx, grad_weight, score: str = "sigmoid", renormalize: bool = True,
+                           scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of :func:`fp8q_moe_gate_topk`'s weights with respect to the logits, the choice held fixed.
+    ``logits`` [T, E] float32 or bf16, ``topk_idx`` int32 [T, k], ``grad_weight`` float32 [T, k] -> ``grad_logits``
+    [T, E] in the logits' dtype.  ``score``, ``renormalize`` and ``scale`` as in the forward call."""
+    ld = _need_logits(logits)
+    T, E = logits.shape
+    code = _score_code(score)
+    _need(topk_idx, "topk_idx", (torch.int32,), 2)
+    if topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must have one row per token")
+    k = topk_idx.shape[1]
+    _need_out(grad_weight, "grad_weight", torch.float32, T * k)
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need_out(grad_logits, "grad_logits", logits.dtype, T * E)
+    _check(load_library().fp8q_moe_gate_backward(
+        _ptr(logits), _out_code(logits.dtype), ld, T, E, k, code, 1 if renormalize else 0, scale, _ptr(topk_idx),
+        _ptr(grad_weight), _ptr(grad_logits), _stream_ptr(stream)), "fp8q_moe_gate_backward")
+    return grad_logits
+
+
+def fp8q_moe_combine(c, row_of, weight, add=None, y=None, stream=None):
+    """Expert rows back to tokens: ``y[t] = add[t] + sum_j weight[t, j] * c[row_of[t, j]]``.  ``c`` bf16 or float32
+    [rows, H], ``row_of`` int32 [T, k] (outside [0, rows): an empty slot), ``weight`` float32 [T, k], ``add`` [T, H]
+    in ``c``'s dtype or None -> ``y`` [T, H] in ``c``'s dtype."""
+    _need(c, "c", _FLOAT, 2)
+    _need(row_of, "row_of", (torch.int32,), 2)
+    rows, H = c.shape
+    T, k = row_of.shape
+    _need_out(weight, "weight", torch.float32, T * k)
+    if add is not None:
+        _need_out(add, "add", c.dtype, T * H)
+    if y is None:
+        y = torch.empty((T, H), dtype=c.dtype, device=c.device)
+    _need_out(y, "y", c.dtype, T * H)
+    _check(load_library().fp8q_moe_combine(_ptr(c), _out_code(c.dtype), rows, H, _ptr(row_of), _ptr(weight), T, k,
+                                           _ptr(add), _ptr(y), _stream_ptr(stream)), "fp8q_moe_combine")
+    return y
+
+
+def fp8q_moe_combine_backward(grad_y, c, row_of, weight, row_token, offsets, grad_c=None, grad_weight=None,
+                              stream=None):
+    """Gradient of :func:`fp8q_moe_combine` -> ``(grad_c [rows, H], grad_weight float32 [T, k])``.  ``row_token`` int32
+    [rows] and ``offsets`` int32 [E+1] are the layout ``row_of`` belongs to: rows below ``offsets[E]`` without a
+    token get zeros, rows from there on are left as they were (uninitialized when ``grad_c`` is not given)."""
+    _need(c, "c", _FLOAT, 2)
+    _need(row_of, "row_of", (torch.int32,), 2)
+    _need(offsets, "offsets", (torch.int32,), 1)
+    rows, H = c.shape
+    T, k = row_of.shape
+    _need_out(grad_y, "grad_y", c.dtype, T * H)
+    _need_out(weight, "weight", torch.float32, T * k)
+    _need_out(row_token, "row_token", torch.int32, rows)
+    if grad_c is None:
+        grad_c = torch.empty_like(c)
+    if grad_weight is None:
+        grad_weight = torch.empty((T, k), dtype=torch.float32, device=c.device)
+    _need_out(grad_c, "grad_c", c.dtype, rows * H)
+    _need_out(grad_weight, "grad_weight", torch.float32, T * k)
+    _check(load_library().fp8q_moe_combine_backward(
+        _ptr(grad_y), _ptr(c), _out_code(c.dtype), rows, H, _ptr(row_of), _ptr(weight), T, k, _ptr(row_token),
+        _ptr(offsets), offsets.numel() - 1, _ptr(grad_c), _ptr(grad_weight), _stream_ptr(stream)),
+        "fp8q_moe_combine_backward")
+    return grad_c, grad_weight
+
+
+def fp8q_quant_int8(x, q=None, s=None, stream=None):
+    """INT8 quantization with one scale per row (tokens, or a weight's output channels).  ``x`` bf16 [M, K] (rows
+    may be strided; an expert stack is passed as [E * N, K]) -> ``(q int8 [M, K], s float32 [M])``."""
+    _need_rows(x, "x")
+    M, K = x.shape
+    ld = x.stride(0) if M > 1 and K > 0 else (K + 7) // 8 * 8
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if s is None:
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need_out(q, "q", torch.int8, M * K)
+    _need_out(s, "s", torch.float32, M)
+    _check(load_library().fp8q_quant_int8(_ptr(x), ld, M, K, _ptr(q), _ptr(s), _stream_ptr(stream)),
+           "fp8q_quant_int8")
+    return q, s
+
+
+def fp8q_gemm_int8(qa, sa, qw, sw, out_dtype=torch.bfloat16, c=None, stream=None):
+    """INT8 product with scales per token and channel: ``C[m, n] = sa[m] sw[n] sum_k qa[m, k] qw[n, k]``.  ``qa`` int8
+    [M, K], ``sa`` float32 [M], ``qw`` int8 [N, K], ``sw`` float32 [N] -> ``c`` [M, N] in ``out_dtype``."""
+    _need(qa, "qa", (torch.int8,), 2)
+    _need(qw, "qw", (torch.int8,), 2)
+    M, K = qa.shape
+    N = qw.shape[0]
+    if qw.shape[1] != K:
+        raise ValueError("inconsistent GEMM operand shapes")
+    _need_out(sa, "sa", torch.float32, M)
+    _need_out(sw, "sw", torch.float32, N)
+    code = _out_code(out_dtype)
+    if c is None:
+        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+    _need_out(c, "c", out_dtype, M * N)
+    _check(load_library().fp8q_gemm_int8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(c), code, M, N, K,
+                                         _stream_ptr(stream)), "fp8q_gemm_int8")
+    return c
+
+
+def fp8q_grouped_gemm_int8(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, c=None, stream=None):
+    """INT8 product per expert segment.  ``qa`` int8 [M_total, K], ``sa`` float32 [M_total], ``qw`` int8 [E, N, K],
+    ``sw`` float32 [E, N], ``offsets`` int32 device [E+1] -> ``c`` [M_total, N]."""
+    _need(qa, "qa", (torch.int8,), 2)
+    _need(qw, "qw", (torch.int8,), 3)
+    _need(offsets, "offsets", (torch.int32,), 1)
+    M, K = qa.shape
+    E, N, K2 = qw.shape
+    if K2 != K or offsets.numel() != E + 1:
+        raise ValueError("inconsistent grouped GEMM operand shapes")
+    _need_out(sa, "sa", torch.float32, M)
+    _need_out(sw, "sw", torch.float32, E * N)
+    code = _out_code(out_dtype)
+    if c is None:
+        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+    _need_out(c, "c", out_dtype, M * N)
+    _check(load_library().fp8q_grouped_gemm_int8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(c), code, _ptr(offsets),
+                                                 E, M, N, K, _stream_ptr(stream)), "fp8q_grouped_gemm_int8")
+    return c
+
+
+def fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets, out_dtype=torch.bfloat16, c=None, stream=None):
+    """:func:`fp8q_grouped_gemm_int8` reading each row's token through ``row_token``.  ``q`` int8 [T, K] token codes,
+    ``s`` float32 [T], ``row_token`` int32 device [M_total] (outside [0, T): an empty row, output 0), ``qw`` int8
+    [E, N, K], ``sw`` float32 [E, N], ``offsets`` int32 device [E+1] -> ``c`` [M_total, N]."""
+    _need(q, "q", (torch.int8,), 2)
+    _need(qw, "qw", (torch.int8,), 3)
+    _need(row_token, "row_token", (torch.int32,), 1)
+    _need(offsets, "offsets", (torch.int32,), 1)
+    T, K = q.shape
+    E, N, K2 = qw.shape
+    M = row_token.numel()
+    if K2 != K or offsets.numel() != E + 1:
+        raise ValueError("inconsistent grouped GEMM operand shapes")
+    _need_out(s, "s", torch.float32, T)
+    _need_out(sw, "sw", torch.float32, E * N)
+    code = _out_code(out_dtype)
+    if c is None:
+        c = torch.empty((M, N), dtype=out_dtype, device=qw.device)
+    _need_out(c, "c", out_dtype, M * N)
+    _check(load_library().fp8q_grouped_gemm_int8_gather(
+        _ptr(q), _ptr(s), T, _ptr(row_token), _ptr(qw), _ptr(sw), _ptr(c), code, _ptr(offsets), E, M, N, K,
+        _stream_ptr(stream)), "fp8q_grouped_gemm_int8_gather")
+    return c

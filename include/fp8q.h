@@ -59,7 +59,8 @@ typedef enum {
     FP8Q_ERR_NO_DEVICE = -5,          /* no HIP device is available */
     FP8Q_ERR_UNSUPPORTED_DEVICE = -6, /* the current device is not gfx950 */
     FP8Q_ERR_HIP = -7,                /* the HIP runtime reported an error at launch */
-    FP8Q_ERR_WORKSPACE = -8           /* the workspace is smaller than the call needs */
+    FP8Q_ERR_WORKSPACE = -8,          /* the workspace is smaller than the call needs */
+    FP8Q_ERR_OPTION = -9              /* an option argument has an unknown value */
 } fp8q_status;
 
 typedef enum { FP8Q_OUT_BF16 = 0, FP8Q_OUT_F32 = 1 } fp8q_out_dtype;
@@ -331,6 +332,122 @@ int fp8q_moe_route_topk_noalloc(const float *logits, int64_t T, int64_t E, int64
 int fp8q_moe_gather_fp8(const uint8_t *q, const float *s, int64_t T, int64_t K, int64_t k, const int32_t *row_of,
                         const int32_t *row_token, const int32_t *offsets, int64_t E, int64_t rows, uint8_t *qa,
                         float *sa, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * MoE gating with weights, the way back from expert rows to tokens, and their
+ * gradients (page "DeepSeek starts updating frequently", the list of TileKernels
+ * features: MoE gating and routing).  Element types are the FP8Q_OUT_* values.
+ * ------------------------------------------------------------------------- */
+typedef enum { FP8Q_SCORE_SIGMOID = 0, FP8Q_SCORE_SOFTMAX = 1 } fp8q_score;
+
+/* Bytes of device workspace fp8q_moe_gate_topk needs (0 up to 32 tokens, then
+ * E rounded up to 4 for every 32 tokens).  Returns -1 for invalid sizes. */
+int64_t fp8q_moe_gate_workspace_bytes(int64_t T, int64_t E);
+
+/* Scores, group-limited top-k, weights and the expert-sorted layout.  For token t
+ * with logits x_e (values above the largest finite fp32 count as that value):
+ *   s_e   = 1 / (1 + exp(-x_e))  or  softmax over e, in fp32;
+ *   key_e = s_e + bias[e] (no bias: s_e).  An expert whose logit is -inf or NaN
+ *           is masked: its score is 0 and it is never chosen;
+ *   the E experts form n_group groups of E / n_group consecutive experts; a
+ *           group's value is the sum of its group_top (1 or 2) largest keys, or
+ *           of the one it has; the topk_group groups of largest value stay;
+ *   the k largest keys of the experts that stay are chosen, best first; equal
+ *           keys and equal groups go to the lower index.  Slots for which no
+ *           expert is left get topk_idx -1, topk_weight 0 and row_of -1;
+ *   topk_weight = scale * s_j / (sum of the chosen s + 1e-20) when renormalize is
+ *           1, scale * s_j when it is 0 (the score, without the bias).
+ *   logits      : [T] rows of E elements (fp32 or bf16, dtype), ld elements apart
+ *   bias        : fp32 [E], finite, or NULL
+ *   topk_idx    : int32 [T][k],  topk_weight : fp32 [T][k]           (outputs)
+ *   offsets, row_of, row_token, rows : the layout, as fp8q_moe_route_topk
+ *   load        : int32 [E] (output, or NULL) tokens that chose the expert
+ *   workspace   : device memory of workspace_bytes bytes, 4-byte aligned, its
+ *                 contents on entry do not matter (calls that share one must not
+ *                 overlap); NULL will do when 0 bytes are needed
+ * Requires the sizes of fp8q_moe_route_topk, T <= 2^31 - 1, ld >= E, 1 <=
+ * topk_group <= n_group <= 64, E % n_group == 0, k <= topk_group * E / n_group,
+ * rows >= fp8q_moe_route_capacity(T, E, k); pointers aligned to their elements.
+ * One launch up to 32 tokens, two above; deterministic. */
+int fp8q_moe_gate_topk(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, int score,
+                       const float *bias, int64_t n_group, int64_t topk_group, int64_t group_top, int renormalize,
+                       float scale, int32_t *topk_idx, float *topk_weight, int32_t *offsets, int32_t *row_of,
+                       int32_t *row_token, int64_t rows, int32_t *load, void *workspace, int64_t workspace_bytes,
+                       void *stream);
+
+/* The gradient of fp8q_moe_gate_topk's weights with respect to the logits, the
+ * choice held fixed (the bias has no gradient):
+ *   topk_idx    : int32 [T][k] as the forward call gave it (-1: an empty slot;
+ *                 a token's experts are distinct)
+ *   grad_weight : fp32 [T][k] gradient of topk_weight
+ *   grad_logits : [T][E] contiguous, in dtype (output; 0 for masked experts)
+ * The other arguments are the forward call's.  fp32 arithmetic. */
+int fp8q_moe_gate_backward(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, int score,
+                           int renormalize, float scale, const int32_t *topk_idx, const float *grad_weight,
+                           void *grad_logits, void *stream);
+
+/* Expert rows back to tokens:
+ *   y[t] = add[t] + sum_j weight[t][j] * c[row_of[t][j]]
+ *   c   : [rows][H] fp32 or bf16 (dtype), the grouped products' output
+ *   row_of : int32 [T][k]; a value outside [0, rows) is an empty slot, which adds
+ *         nothing and reads nothing
+ *   weight : fp32 [T][k];  add : [T][H] in dtype (shared expert, residual) or NULL
+ *   y   : [T][H] in dtype (output)
+ * fp32 sums, slots in order, rounded once.  Requires H % 8 == 0, 1 <= k <= 16,
+ * T, rows, H <= 2^31 - 1, 16-byte aligned c, add and y. */
+int fp8q_moe_combine(const void *c, int dtype, int64_t rows, int64_t H, const int32_t *row_of, const float *weight,
+                     int64_t T, int64_t k, const void *add, void *y, void *stream);
+
+/* Its gradient (that of add is grad_y itself):
+ *   grad_c[row_of[t][j]] = weight[t][j] * grad_y[t],  grad_weight[t][j] = <grad_y[t], c[row_of[t][j]]>
+ *   row_token, offsets, E : the layout that row_of belongs to
+ *   grad_c : [rows][H] in dtype (output): rows below offsets[E] that carry no
+ *            token become zeros, rows from offsets[E] on are not written
+ *   grad_weight : fp32 [T][k] (output; 0 for an empty slot)
+ * Requires what fp8q_moe_combine requires, and rows of different slots to be
+ * different.  fp32 sums in a fixed order. */
+int fp8q_moe_combine_backward(const void *grad_y, const void *c, int dtype, int64_t rows, int64_t H,
+                              const int32_t *row_of, const float *weight, int64_t T, int64_t k,
+                              const int32_t *row_token, const int32_t *offsets, int64_t E, void *grad_c,
+                              float *grad_weight, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * INT8 with one scale per token and per output channel (the per-token and
+ * per-channel modes of the same list, in 8-bit integers).
+ * ------------------------------------------------------------------------- */
+
+/* Rows of bf16 to INT8, one scale per row: tokens and weights alike.
+ *   x : bf16 [M][K], rows ld elements apart
+ *   s : fp32 [M] (output) = fl32(max_k |x| / 127)
+ *   q : int8 [M][K] contiguous (output) = fl32(x / s) rounded to nearest even, in
+ *       [-127, 127]; 0 where s is 0
+ * Requires K % 16 == 0, ld >= K, ld % 8 == 0, 16-byte aligned x and q, 4-byte
+ * aligned s; with K == 0, x and q may be null and s is set to 0. */
+int fp8q_quant_int8(const uint16_t *x, int64_t ld, int64_t M, int64_t K, int8_t *q, float *s, void *stream);
+
+/* C[m,n] = fl32(sum_k qa[m,k] * qw[n,k]) * (sa[m] * sw[n]), the sum exact in 32-bit integers:
+ *   qa : int8 [M][K], sa : fp32 [M];  qw : int8 [N][K], sw : fp32 [N]
+ *   c  : [M][N] bf16 or fp32 (out_dtype)
+ * Requires M >= 0, N % 8 == 0, K % 16 == 0, 16 <= K <= 131056; qa, qw and c
+ * 16-byte aligned, sa and sw 4-byte aligned. */
+int fp8q_gemm_int8(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw, void *c, int out_dtype,
+                   int64_t M, int64_t N, int64_t K, void *stream);
+
+/* The same per expert segment: rows [off[e], off[e+1]) of qa [M_total][K] and sa
+ * [M_total] times expert e's qw [E][N][K], sw [E][N].  The offsets' rules and
+ * guarantees are those of fp8q_grouped_gemm_blockscaled (segments multiples of
+ * 128 rows, rows from off[E] on not written), the sizes' those of
+ * fp8q_gemm_int8 with E >= 1 and M_total % 128 == 0. */
+int fp8q_grouped_gemm_int8(const int8_t *qa, const float *sa, const int8_t *qw, const float *sw, void *c,
+                           int out_dtype, const int32_t *off, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                           void *stream);
+
+/* The same with row r's token read in place: q [T][K], s [T], row_token[r] int32
+ * [M_total]; a token outside [0, T) is an empty row, whose output is 0.  Requires
+ * T * K < 2^31 besides; q and s may be null when T == 0. */
+int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, const int32_t *row_token,
+                                  const int8_t *qw, const float *sw, void *c, int out_dtype, const int32_t *off,
+                                  int64_t E, int64_t M_total, int64_t N, int64_t K, void *stream);
 
 #ifdef __cplusplus
 }
