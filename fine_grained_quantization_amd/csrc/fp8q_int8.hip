@@ -66,11 +66,14 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restr
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Matrix product.  A workgroup of 4 waves computes 128 rows x 128 channels, a wave 64 x 64 of them, K in blocks
-// of 128 codes through one LDS stage.
+// Matrix product.  A workgroup of 4 waves, WM along the rows x WN along the channels, computes a tile of
+// BM = 32 TM WM rows x BN = 32 TN WN channels, a wave 32 TM x 32 TN of it with 32 x 32 x 32 MFMAs (weights as the
+// row operand, so that a lane's 4 consecutive result registers are 4 consecutive channels of one row).  Both tiles
+// travel in blocks of 128 codes from global memory straight into a ring of 5 LDS slots, each for one operand's block
+// (A0 W0 A1 W1 A2 W2 ...): while block kb is multiplied, kb + 1 and A's kb + 2 are on the way or there.
 // ---------------------------------------------------------------------------------------------------------
 
-constexpr int kTile = 128;
+typedef int v16i __attribute__((ext_vector_type(16)));
 
 struct Int8Args {
     const uint8_t *qa;
@@ -84,107 +87,255 @@ struct Int8Args {
     int64_t n_mtiles, n_ntiles;
 };
 
-template <bool OUT_BF16, bool GROUPED, bool GATHER>
-__global__ __launch_bounds__(256) void gemm_int8_kernel(Int8Args p) {
-    __shared__ __attribute__((aligned(1024))) uint8_t tA[kTile * 128], tW[kTile * 128];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int64_t m0, mend = p.M, n0, e = 0;
-    if constexpr (GROUPED) {
-        if (!grouped_tile<kTile>(blockIdx.x, p.off, p.E, p.M, p.n_mtiles, p.n_ntiles, kTile, lane, m0, mend, n0, e))
-            return;
+// Waits for this wave's LDS reads and for all but its last N copies into LDS, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void copies_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int TM, int TN, int WM, int WN>
+struct TileShape {
+    static_assert(WM * WN == 4, "4 waves");
+    static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
+    static constexpr int kSlots = 5, kSlot = (BM > BN ? BM : BN) * 128, kLds = kSlots * kSlot;
+    static constexpr int kRowsA = BM / 4, kRowsW = BN / 4;  // rows that a wave copies per block
+    static constexpr int kCopyA = kRowsA / 8, kCopyW = kRowsW / 8;
+};
+
+// The order of one step's instructions.  Left alone, the compiler reads each fragment right before its MFMAs and waits
+// for it.  These put the LDS reads (0x100) first, two before each MFMA (0x008), and the copies (0x010) after them,
+// spread between the MFMAs that are left.
+template <int READS, int MFMAS, int COPIES, int I = 0>
+__device__ __forceinline__ void schedule_step() {
+    constexpr int kRest = MFMAS - READS / 2;
+    if constexpr (I < READS / 2) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     } else {
-        int64_t mt, nt;
-        if (!dense_tile_at(xcd_order(blockIdx.x), p.n_mtiles, p.n_ntiles, mt, nt)) return;
-        m0 = mt * kTile;
-        n0 = nt * kTile;
+        constexpr int i = I - READS / 2, n = (i + 1) * COPIES / kRest - i * COPIES / kRest;
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x010, n, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
     }
-    const uint8_t *W = p.qw + e * p.N * p.K;
-    const float *SW = p.sw + e * p.N;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    // Copies: thread t moves chunk t % 8 of rows t / 8, t / 8 + 32, ... of both tiles.
-    const int cr = tid >> 3, cc = tid & 7;
-    int64_t arow[4];
+    if constexpr (I + 1 < MFMAS) schedule_step<READS, MFMAS, COPIES, I + 1>();
+}
+
+// One tile at (m0, n0): rows [m0, mend) of c, W / SW the weights and their scales.  With GATHER row r's codes are
+// those of token rtok[r].
+template <bool OUT_BF16, int TM, int TN, int WM, int WN, bool GATHER>
+__device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const uint8_t *W, const float *SW,
+                                          int64_t m0, int64_t mend, int64_t n0) {
+    using S = TileShape<TM, TN, WM, WN>;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) & 3;
+    const int wm = (wave % WM) * 32 * TM, wn = (wave / WM) * 32 * TN;
+    const int64_t K = p.K;
+    const int KB = (int)((K + 127) >> 7);
+    const int64_t nrow = mend - m0 < S::BM ? mend - m0 : S::BM;
+    const int64_t ncol = p.N - n0 < S::BN ? p.N - n0 : S::BN;
+
+    // Copies: one instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, physical chunk l % 8, which
+    // holds logical chunk (l % 8) ^ swzf(row).  Rows past the operand are given an offset past its resource.
+    const i32x4 ra = GATHER ? make_rsrc(p.qa, (uint64_t)p.T * (uint64_t)K) : make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
+    const i32x4 rw = make_rsrc(W + n0 * K, (uint64_t)(ncol * K));
+    const int c0 = (lane & 7) ^ (lane >> 3);  // logical chunk in the copies of even j; c0 ^ 1 in the odd ones
+    int avoff[S::kCopyA], wvoff[S::kCopyW];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const int64_t r = m0 + cr + 32 * j;
-        int64_t src = r < mend ? r : -1;
+    for (int j = 0; j < S::kCopyA; j++) {
+        const int r = wave * S::kRowsA + 8 * j + (lane >> 3);
+        const int ch = (lane & 7) ^ swzf(r);
+        if constexpr (GATHER) {
+            const int64_t tok = r < nrow ? p.rtok[m0 + r] : -1;
+            avoff[j] = tok >= 0 && tok < p.T ? (int)(tok * K) + ch * 16 : kOutOfRange;
+        } else {
+            avoff[j] = r < nrow ? (int)(r * K) + ch * 16 : kOutOfRange;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < S::kCopyW; j++) {
+        const int r = wave * S::kRowsW + 8 * j + (lane >> 3);
+        wvoff[j] = r < ncol ? (int)(r * K) + (((lane & 7) ^ swzf(r)) << 4) : kOutOfRange;
+    }
+    // Half h of block kb's A or W rows into its slot; past the last block the resources are empty and nothing is
+    // read.  In a block that K ends in, chunks past K read zeros.  (The scalar offset of the block is not
+    // range-checked, the others are.)
+    auto copy = [&](i32x4 rsrc, const int *voff, int per_wave, int h, int kb, int slot) {
+        const bool in = kb < KB;
+        const i32x4 rs = in ? rsrc : empty_rsrc(rsrc);
+        const int so = in ? kb * 128 : 0;
+        const int left = in ? (int)(K - (int64_t)kb * 128) : 128;
+        const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
+#pragma unroll
+        for (int j = h * per_wave / 2; j < (h + 1) * per_wave / 2; j++)
+            fp8q_raw_buffer_load_lds(rs, (lds_ptr)(lds + slot * S::kSlot + (wave * per_wave + j) * 1024), 16,
+                                     (j & 1 ? ok1 : ok0) ? voff[j] : kOutOfRange, so, 0, 0);
+    };
+    auto copy_a = [&](int h, int kb, int slot) { copy(ra, avoff, S::kCopyA, h, kb, slot); };
+    auto copy_w = [&](int h, int kb, int slot) { copy(rw, wvoff, S::kCopyW, h, kb, slot); };
+    // Operand fragments of step ks (32 codes): lane l takes row l % 32 and chunk 2 ks + l / 32.
+    auto frag = [&](const uint8_t *tile, int row0, int ks) {
+        return *reinterpret_cast<const v4i *>(tile + swz(row0 + (lane & 31), 2 * ks + (lane >> 5)));
+    };
+
+    v16i acc[TN][TM];
+#pragma unroll
+    for (int ni = 0; ni < TN; ni++)
+#pragma unroll
+        for (int mi = 0; mi < TM; mi++)
+#pragma unroll
+            for (int r = 0; r < 16; r++) acc[ni][mi][r] = 0;
+
+    copy_a(0, 0, 0);
+    copy_a(1, 0, 0);
+    copy_w(0, 0, 1);
+    copy_w(1, 0, 1);
+    copy_a(0, 1, 2);
+    copy_a(1, 1, 2);
+    copy_w(0, 1, 3);
+    copies_barrier<S::kCopyA + S::kCopyW / 2>();  // block 0 is there
+    v4i fa[2][TM], fw[2][TN];
+#pragma unroll
+    for (int i = 0; i < TM; i++) fa[0][i] = frag(lds, wm + 32 * i, 0);
+#pragma unroll
+    for (int i = 0; i < TN; i++) fw[0][i] = frag(lds + S::kSlot, wn + 32 * i, 0);
+    // Slot of A's block kb (W's is the next one).  The fragments of a step are read while the MFMAs of the step
+    // before it run, and a quarter of the copies of a block is issued in each step.  The last step's fragments are
+    // in registers before the barrier that frees the block's slots.
+    int slot = 0;
+    for (int kb = 0; kb < KB; kb++) {
+        const int s1 = slot + 1 < S::kSlots ? slot + 1 : slot + 1 - S::kSlots;
+        const int s2 = slot + 2 < S::kSlots ? slot + 2 : slot + 2 - S::kSlots;
+        const int s3 = slot + 3 < S::kSlots ? slot + 3 : slot + 3 - S::kSlots;
+        const int s4 = slot + 4 < S::kSlots ? slot + 4 : slot + 4 - S::kSlots;
+#pragma unroll
+        for (int ks = 0; ks < 4; ks++) {
+            if (ks == 3) {
+                copies_barrier<S::kCopyA>();  // block kb + 1 is there; A's kb + 2 may still be on the way
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const uint8_t *tA = lds + (ks < 3 ? slot : s2) * S::kSlot, *tW = lds + (ks < 3 ? s1 : s3) * S::kSlot;
+#pragma unroll
+            for (int i = 0; i < TM; i++) fa[(ks + 1) & 1][i] = frag(tA, wm + 32 * i, (ks + 1) & 3);
+#pragma unroll
+            for (int i = 0; i < TN; i++) fw[(ks + 1) & 1][i] = frag(tW, wn + 32 * i, (ks + 1) & 3);
+            if (ks == 0) copy_w(1, kb + 1, s3);
+            if (ks == 1) copy_a(0, kb + 2, s4);
+            if (ks == 2) copy_a(1, kb + 2, s4);
+            if (ks == 3) copy_w(0, kb + 2, slot);  // the slot that A's block kb leaves
+#pragma unroll
+            for (int ni = 0; ni < TN; ni++)
+#pragma unroll
+                for (int mi = 0; mi < TM; mi++)
+                    acc[ni][mi] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[ks & 1][ni], fa[ks & 1][mi], acc[ni][mi],
+                                                                        0, 0, 0);
+            if (ks == 0 || ks == 3)
+                schedule_step<TM + TN, TM * TN, S::kCopyW / 2>();
+            else
+                schedule_step<TM + TN, TM * TN, S::kCopyA / 2>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        slot = s2;
+    }
+
+    // Register 4 g + i of a lane is channel 8 g + 4 (lane / 32) + i of row lane % 32.  Results pass through LDS so
+    // that whole row segments are stored: a wave's block of 32 TM rows x 256 bytes at a time, the 16-byte chunks
+    // of row r at chunk ^ (r % 16).
+    float sa[TM];
+#pragma unroll
+    for (int mi = 0; mi < TM; mi++) {
+        const int64_t m = m0 + wm + 32 * mi + (lane & 31);
+        int64_t src = m < mend ? m : -1;
         if constexpr (GATHER) {
             src = src >= 0 ? p.rtok[src] : -1;
             if (src >= p.T) src = -1;
         }
-        arow[j] = src;
+        sa[mi] = src >= 0 ? p.sa[src] : 0.0f;
     }
-    v4i acc[4][4];
+    constexpr int kEl = OUT_BF16 ? 2 : 4;
+    constexpr int kSubs = TN * 32 * kEl > 256 ? 256 / (32 * kEl) : TN;  // channel subtiles per pass
+    constexpr int kRowBytes = kSubs * 32 * kEl, kChunks = kRowBytes / 16;
+    static_assert(4 * 32 * TM * kRowBytes <= S::kLds && (kChunks & (kChunks - 1)) == 0, "staging");
+    copies_barrier<0>();
+    uint8_t *blk = lds + wave * 32 * TM * kRowBytes;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int n1 = 0; n1 < TN; n1 += kSubs) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = (v4i){0, 0, 0, 0};
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    for (int64_t k0 = 0; k0 < p.K; k0 += 128) {
-        u32x4 va[4], vw[4];
-        const int64_t k = k0 + cc * 16;
+        for (int ni = n1; ni < n1 + kSubs; ni++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int64_t n = n0 + cr + 32 * j;
-            va[j] = k < p.K && arow[j] >= 0 ? *reinterpret_cast<const u32x4 *>(p.qa + arow[j] * p.K + k) : zero;
-            vw[j] = k < p.K && n < p.N ? *reinterpret_cast<const u32x4 *>(W + n * p.K + k) : zero;
-        }
-        __syncthreads();
+            for (int g = 0; g < 4; g++) {
+                const int nl = 32 * ni + 8 * g + 4 * (lane >> 5);
+                const int64_t n = n0 + wn + nl;
+                float4 sw = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (n < p.N) {
+                    sw.x = SW[n];
+                    sw.y = SW[n + 1];
+                    sw.z = SW[n + 2];
+                    sw.w = SW[n + 3];
+                }
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            *reinterpret_cast<u32x4 *>(tA + swz(cr + 32 * j, cc)) = va[j];
-            *reinterpret_cast<u32x4 *>(tW + swz(cr + 32 * j, cc)) = vw[j];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            v4i fa[4], fw[4];
-            const int ch = 4 * h + (lane >> 4);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                fa[i] = *reinterpret_cast<const v4i *>(tA + swz(wm + 16 * i + (lane & 15), ch));
-                fw[i] = *reinterpret_cast<const v4i *>(tW + swz(wn + 16 * i + (lane & 15), ch));
+                for (int mi = 0; mi < TM; mi++) {
+                    const int r = 32 * mi + (lane & 31);
+                    v4f v;
+                    v[0] = (float)acc[ni][mi][4 * g] * (sa[mi] * sw.x);
+                    v[1] = (float)acc[ni][mi][4 * g + 1] * (sa[mi] * sw.y);
+                    v[2] = (float)acc[ni][mi][4 * g + 2] * (sa[mi] * sw.z);
+                    v[3] = (float)acc[ni][mi][4 * g + 3] * (sa[mi] * sw.w);
+                    const int byte = (nl - 32 * n1) * kEl;
+                    store4<OUT_BF16>(blk + r * kRowBytes + ((((byte >> 4) ^ r) & (kChunks - 1)) << 4) + (byte & 15), 0, v);
+                }
             }
+        // (the block is the wave's own: its LDS operations are in order)
 #pragma unroll
-            for (int ni = 0; ni < 4; ni++)
-#pragma unroll
-                for (int mi = 0; mi < 4; mi++)
-                    acc[ni][mi] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ni], fa[mi], acc[ni][mi], 0, 0, 0);
-        }
-    }
-    // A lane holds channels n .. n + 3 of one row.
-#pragma unroll
-    for (int mi = 0; mi < 4; mi++) {
-        const int64_t m = m0 + wm + 16 * mi + (lane & 15);
-        if (m >= mend) continue;
-        int64_t src = m;
-        if constexpr (GATHER) {
-            src = p.rtok[m];
-            if (src >= p.T) src = -1;
-        }
-        const float sa = src >= 0 ? p.sa[src] : 0.0f;
-#pragma unroll
-        for (int ni = 0; ni < 4; ni++) {
-            const int64_t n = n0 + wn + 16 * ni + 4 * (lane >> 4);
-            if (n >= p.N) continue;
-            v4f v;
-#pragma unroll
-            for (int r = 0; r < 4; r++) v[r] = (float)acc[ni][mi][r] * (sa * SW[n + r]);
-            store4<OUT_BF16>(p.c, m * p.N + n, v);
+        for (int j = 0; j < 32 * TM * kChunks / 64; j++) {
+            const int idx = j * 64 + lane, r = idx / kChunks, ch = idx % kChunks;
+            const int64_t m = m0 + wm + r, n = n0 + wn + 32 * n1 + ch * (16 / kEl);
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(blk + r * kRowBytes + (((ch ^ r) & (kChunks - 1)) << 4));
+            if (m < mend && n < p.N)
+                *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(p.c) + (m * p.N + n) * kEl) = v;
         }
     }
 }
 
-template <bool GROUPED, bool GATHER>
-hipError_t launch_int8(Int8Args p, bool out_bf16, hipStream_t stream) {
-    p.n_mtiles = GROUPED ? p.M / kTile + p.E : (p.M + kTile - 1) / kTile;
-    p.n_ntiles = (p.N + kTile - 1) / kTile;
+template <bool OUT_BF16, bool GROUPED, bool GATHER, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(256, 1) void gemm_int8_kernel(Int8Args p) {
+    using S = TileShape<TM, TN, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+    int64_t m0, mend = p.M, n0, e = 0;
+    if constexpr (GROUPED) {
+        if (!grouped_tile<S::BM>(blockIdx.x, p.off, p.E, p.M, p.n_mtiles, p.n_ntiles, S::BN, threadIdx.x & 63, m0, mend,
+                                 n0, e))
+            return;
+        // The same in every lane, but the compiler cannot see that: they come out of lane shuffles.
+        e = __builtin_amdgcn_readfirstlane((int)e);
+        m0 = __builtin_amdgcn_readfirstlane((int)m0);
+        mend = __builtin_amdgcn_readfirstlane((int)mend);
+    } else {
+        int64_t mt, nt;
+        if (!dense_tile_at(xcd_order(blockIdx.x), p.n_mtiles, p.n_ntiles, mt, nt)) return;
+        m0 = mt * S::BM;
+        n0 = nt * S::BN;
+    }
+    int8_tile<OUT_BF16, TM, TN, WM, WN, GATHER>(lds, p, p.qw + e * p.N * p.K, p.sw + e * p.N, m0, mend, n0);
+}
+
+constexpr int kTile = 128;  // the smallest tile's rows and channels
+
+template <bool GROUPED, bool GATHER, int TM, int TN, int WM, int WN>
+hipError_t launch_int8_tile(Int8Args p, bool out_bf16, hipStream_t stream) {
+    using S = TileShape<TM, TN, WM, WN>;
+    p.n_mtiles = GROUPED ? p.M / S::BM + p.E : (p.M + S::BM - 1) / S::BM;
+    p.n_ntiles = (p.N + S::BN - 1) / S::BN;
     const dim3 grid((unsigned)((p.n_mtiles * p.n_ntiles + 255) / 256 * 256));
     if (out_bf16)
-        gemm_int8_kernel<true, GROUPED, GATHER><<<grid, 256, 0, stream>>>(p);
+        gemm_int8_kernel<true, GROUPED, GATHER, TM, TN, WM, WN><<<grid, 256, 0, stream>>>(p);
     else
-        gemm_int8_kernel<false, GROUPED, GATHER><<<grid, 256, 0, stream>>>(p);
+        gemm_int8_kernel<false, GROUPED, GATHER, TM, TN, WM, WN><<<grid, 256, 0, stream>>>(p);
     return hipGetLastError();
+}
+
+template <bool GROUPED, bool GATHER>
+hipError_t launch_int8(Int8Args p, bool out_bf16, hipStream_t stream) {
+    if (p.M >= 2048) return launch_int8_tile<GROUPED, GATHER, 4, 4, 2, 2>(p, out_bf16, stream);
+    return launch_int8_tile<GROUPED, GATHER, 2, 2, 2, 2>(p, out_bf16, stream);
 }
 
 }  // namespace
