@@ -66,14 +66,12 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restr
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Matrix product.  A workgroup of 4 waves, WM along the rows x WN along the channels, computes a tile of
-// BM = 32 TM WM rows x BN = 32 TN WN channels, a wave 32 TM x 32 TN of it with 32 x 32 x 32 MFMAs (weights as the
-// row operand, so that a lane's 4 consecutive result registers are 4 consecutive channels of one row).  Both tiles
+// Matrix product.  A workgroup of WM waves along the rows x WN along the channels (4 or 8) computes a tile of
+// BM = 16 TM WM rows x BN = 16 TN WN channels, a wave 16 TM x 16 TN of it with 16 x 16 x 64 MFMAs (weights as the
+// row operand, so that a lane's 4 result registers are 4 consecutive channels of one row).  Both tiles
 // travel in blocks of 128 codes from global memory straight into a ring of 5 LDS slots, each for one operand's block
 // (A0 W0 A1 W1 A2 W2 ...): while block kb is multiplied, kb + 1 and A's kb + 2 are on the way or there.
 // ---------------------------------------------------------------------------------------------------------
-
-typedef int v16i __attribute__((ext_vector_type(16)));
 
 struct Int8Args {
     const uint8_t *qa;
@@ -93,30 +91,32 @@ __device__ __forceinline__ void copies_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+constexpr int kBack = 4096;
+// An offset past every resource here (they end below 2^31 + kBack), also with an instruction's offset on top.
+constexpr int kFar = (int)0xFFFFF000u;
+
 template <int TM, int TN, int WM, int WN>
 struct TileShape {
-    static_assert(WM * WN == 4, "4 waves");
-    static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
+    static constexpr int kWaves = WM * WN;
+    static_assert(kWaves == 4 || kWaves == 8, "waves");
+    static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
     static constexpr int kSlots = 5, kSlot = (BM > BN ? BM : BN) * 128, kLds = kSlots * kSlot;
-    static constexpr int kRowsA = BM / 4, kRowsW = BN / 4;  // rows that a wave copies per block
+    static constexpr int kRowsA = BM / kWaves, kRowsW = BN / kWaves;  // rows that a wave copies per block
     static constexpr int kCopyA = kRowsA / 8, kCopyW = kRowsW / 8;
+    static_assert(kCopyA % 2 == 0 && kCopyW % 2 == 0, "copies go out in halves");
 };
 
-// The order of one step's instructions.  Left alone, the compiler reads each fragment right before its MFMAs and waits
-// for it.  These put the LDS reads (0x100) first, two before each MFMA (0x008), and the copies (0x010) after them,
-// spread between the MFMAs that are left.
-template <int READS, int MFMAS, int COPIES, int I = 0>
-__device__ __forceinline__ void schedule_step() {
-    constexpr int kRest = MFMAS - READS / 2;
-    if constexpr (I < READS / 2) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    } else {
-        constexpr int i = I - READS / 2, n = (i + 1) * COPIES / kRest - i * COPIES / kRest;
-        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x010, n, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+// f(0), f(1), ... f(N - 1) with the index as a compile-time constant.
+template <int I>
+struct Index {
+    static constexpr int value = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void static_for(const F &f) {
+    if constexpr (I < N) {
+        f(Index<I>{});
+        static_for<N, I + 1>(f);
     }
-    if constexpr (I + 1 < MFMAS) schedule_step<READS, MFMAS, COPIES, I + 1>();
 }
 
 // One tile at (m0, n0): rows [m0, mend) of c, W / SW the weights and their scales.  With GATHER row r's codes are
@@ -126,17 +126,21 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
                                           int64_t m0, int64_t mend, int64_t n0) {
     using S = TileShape<TM, TN, WM, WN>;
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) & 3;
-    const int wm = (wave % WM) * 32 * TM, wn = (wave / WM) * 32 * TN;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) & (S::kWaves - 1);
+    const int wm = (wave % WM) * 16 * TM, wn = (wave / WM) * 16 * TN;
     const int64_t K = p.K;
-    const int KB = (int)((K + 127) >> 7);
+    const int KB = __builtin_amdgcn_readfirstlane((int)((K + 127) >> 7));
     const int64_t nrow = mend - m0 < S::BM ? mend - m0 : S::BM;
     const int64_t ncol = p.N - n0 < S::BN ? p.N - n0 : S::BN;
 
     // Copies: one instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, physical chunk l % 8, which
     // holds logical chunk (l % 8) ^ swzf(row).  Rows past the operand are given an offset past its resource.
-    const i32x4 ra = GATHER ? make_rsrc(p.qa, (uint64_t)p.T * (uint64_t)K) : make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
-    const i32x4 rw = make_rsrc(W + n0 * K, (uint64_t)(ncol * K));
+    // The LDS address of a copy is a base register plus the instruction's offset, which counts for the memory address
+    // too: four copies share one base, and the memory offsets of copy j are kBack - 1024 (j % 4) with resources that
+    // start kBack bytes early.  (Writing the base register for every copy makes each wait for the one before it.)
+    const i32x4 ra = GATHER ? make_rsrc(p.qa - kBack, (uint64_t)p.T * (uint64_t)K + kBack)
+                            : make_rsrc(p.qa + m0 * K - kBack, (uint64_t)(nrow * K) + kBack);
+    const i32x4 rw = make_rsrc(W + n0 * K - kBack, (uint64_t)(ncol * K) + kBack);
     const int c0 = (lane & 7) ^ (lane >> 3);  // logical chunk in the copies of even j; c0 ^ 1 in the odd ones
     int avoff[S::kCopyA], wvoff[S::kCopyW];
 #pragma unroll
@@ -145,104 +149,132 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         const int ch = (lane & 7) ^ swzf(r);
         if constexpr (GATHER) {
             const int64_t tok = r < nrow ? p.rtok[m0 + r] : -1;
-            avoff[j] = tok >= 0 && tok < p.T ? (int)(tok * K) + ch * 16 : kOutOfRange;
+            avoff[j] = tok >= 0 && tok < p.T ? (int)(tok * K) + ch * 16 + kBack - 1024 * (j & 3) : kFar;
         } else {
-            avoff[j] = r < nrow ? (int)(r * K) + ch * 16 : kOutOfRange;
+            avoff[j] = r < nrow ? (int)(r * K) + ch * 16 + kBack - 1024 * (j & 3) : kFar;
         }
     }
 #pragma unroll
     for (int j = 0; j < S::kCopyW; j++) {
         const int r = wave * S::kRowsW + 8 * j + (lane >> 3);
-        wvoff[j] = r < ncol ? (int)(r * K) + (((lane & 7) ^ swzf(r)) << 4) : kOutOfRange;
+        wvoff[j] = r < ncol ? (int)(r * K) + (((lane & 7) ^ swzf(r)) << 4) + kBack - 1024 * (j & 3) : kFar;
     }
-    // Half h of block kb's A or W rows into its slot; past the last block the resources are empty and nothing is
-    // read.  In a block that K ends in, chunks past K read zeros.  (The scalar offset of the block is not
-    // range-checked, the others are.)
-    auto copy = [&](i32x4 rsrc, const int *voff, int per_wave, int h, int kb, int slot) {
-        const bool in = kb < KB;
-        const i32x4 rs = in ? rsrc : empty_rsrc(rsrc);
-        const int so = in ? kb * 128 : 0;
-        const int left = in ? (int)(K - (int64_t)kb * 128) : 128;
-        const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
-#pragma unroll
-        for (int j = h * per_wave / 2; j < (h + 1) * per_wave / 2; j++)
-            fp8q_raw_buffer_load_lds(rs, (lds_ptr)(lds + slot * S::kSlot + (wave * per_wave + j) * 1024), 16,
-                                     (j & 1 ? ok1 : ok0) ? voff[j] : kOutOfRange, so, 0, 0);
+    // Copies [j0, j1) of block kb's A or W rows into its slot; past the last block the resources are empty and nothing
+    // is read.  K may end inside a block: that one goes first (the integer sums do not depend on the order), with the
+    // chunks past K masked, so that the loop below copies whole blocks only.  Block kb > 0 starts at code
+    // (kb - 1) * 128.  (The scalar offset of the block is not range-checked, the others are.)
+    auto copy_one = [&](auto index, i32x4 rs, int voff, int so, int per_wave, int slot) __attribute__((always_inline)) {
+        constexpr int j = decltype(index)::value;
+        fp8q_raw_buffer_load_lds(rs, (lds_ptr)(lds + slot * S::kSlot + (wave * per_wave + (j & ~3)) * 1024), 16, voff, so,
+                                 (j & 3) * 1024, 0);
     };
-    auto copy_a = [&](int h, int kb, int slot) { copy(ra, avoff, S::kCopyA, h, kb, slot); };
-    auto copy_w = [&](int h, int kb, int slot) { copy(rw, wvoff, S::kCopyW, h, kb, slot); };
-    // Operand fragments of step ks (32 codes): lane l takes row l % 32 and chunk 2 ks + l / 32.
+    auto copy_a = [&](auto index, int kb, int slot) __attribute__((always_inline)) {
+        i32x4 rs = ra;
+        rs[2] = __builtin_amdgcn_readfirstlane(kb < KB ? rs[2] : 0);
+        copy_one(index, rs, avoff[decltype(index)::value], __builtin_amdgcn_readfirstlane(kb - 1) * 128, S::kCopyA, slot);
+    };
+    auto copy_w = [&](auto index, int kb, int slot) __attribute__((always_inline)) {
+        i32x4 rs = rw;
+        rs[2] = __builtin_amdgcn_readfirstlane(kb < KB ? rs[2] : 0);
+        copy_one(index, rs, wvoff[decltype(index)::value], __builtin_amdgcn_readfirstlane(kb - 1) * 128, S::kCopyW, slot);
+    };
+    // Operand fragments of step ks (64 codes): lane l takes row l % 16 and chunk 4 ks + l / 16.
     auto frag = [&](const uint8_t *tile, int row0, int ks) {
-        return *reinterpret_cast<const v4i *>(tile + swz(row0 + (lane & 31), 2 * ks + (lane >> 5)));
+        return *reinterpret_cast<const v4i *>(tile + swz(row0 + (lane & 15), 4 * ks + (lane >> 4)));
     };
 
-    v16i acc[TN][TM];
+    v4i acc[TN][TM];
 #pragma unroll
     for (int ni = 0; ni < TN; ni++)
 #pragma unroll
-        for (int mi = 0; mi < TM; mi++)
-#pragma unroll
-            for (int r = 0; r < 16; r++) acc[ni][mi][r] = 0;
+        for (int mi = 0; mi < TM; mi++) acc[ni][mi] = (v4i){0, 0, 0, 0};
 
-    copy_a(0, 0, 0);
-    copy_a(1, 0, 0);
-    copy_w(0, 0, 1);
-    copy_w(1, 0, 1);
-    copy_a(0, 1, 2);
-    copy_a(1, 1, 2);
-    copy_w(0, 1, 3);
-    copies_barrier<S::kCopyA + S::kCopyW / 2>();  // block 0 is there
-    v4i fa[2][TM], fw[2][TN];
+    const int left = (int)(K - (int64_t)(KB - 1) * 128);
+    const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
+    static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) {
+        copy_one(j, ra, (j.value & 1 ? ok1 : ok0) ? avoff[j.value] : kFar, (KB - 1) * 128, S::kCopyA, 0);
+    });
+    static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) {
+        copy_one(j, rw, (j.value & 1 ? ok1 : ok0) ? wvoff[j.value] : kFar, (KB - 1) * 128, S::kCopyW, 1);
+    });
+    static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, 1, 2); });
+    static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, 1, 3); });
+    copies_barrier<S::kCopyA + S::kCopyW>();  // block 0 is there
+    // A block is 2 TN phases: phase g multiplies channel subtile g % TN by all row subtiles, for the 64 codes of step
+    // g / TN.  Channel fragments are read kAhead phases before their use, row fragments a step before.  The last of
+    // the block's fragments is read kAhead phases before the end; the barrier after that phase frees the block's slots,
+    // and the next block's first fragments and the copies into A's slot follow it.
+    constexpr int kAhead = 3, kPhases = 2 * TN, kBarrier = kPhases - kAhead;
+    static_assert(kPhases % (kAhead + 1) == 0 && kBarrier > TN && TM % 2 == 0, "phases");
+    v4i fa[2][TM], fw[kAhead + 1];
 #pragma unroll
-    for (int i = 0; i < TM; i++) fa[0][i] = frag(lds, wm + 32 * i, 0);
+    for (int i = 0; i < TM; i++) fa[0][i] = frag(lds, wm + 16 * i, 0);
 #pragma unroll
-    for (int i = 0; i < TN; i++) fw[0][i] = frag(lds + S::kSlot, wn + 32 * i, 0);
-    // Slot of A's block kb (W's is the next one).  The fragments of a step are read while the MFMAs of the step
-    // before it run, and a quarter of the copies of a block is issued in each step.  The last step's fragments are
-    // in registers before the barrier that frees the block's slots.
-    int slot = 0;
-    for (int kb = 0; kb < KB; kb++) {
-        const int s1 = slot + 1 < S::kSlots ? slot + 1 : slot + 1 - S::kSlots;
-        const int s2 = slot + 2 < S::kSlots ? slot + 2 : slot + 2 - S::kSlots;
-        const int s3 = slot + 3 < S::kSlots ? slot + 3 : slot + 3 - S::kSlots;
-        const int s4 = slot + 4 < S::kSlots ? slot + 4 : slot + 4 - S::kSlots;
-#pragma unroll
-        for (int ks = 0; ks < 4; ks++) {
-            if (ks == 3) {
+    for (int i = 0; i < kAhead; i++) fw[i] = frag(lds + S::kSlot, wn + 16 * i, 0);
+    // Block kb with A in slot `slot` and W in the next.
+    auto block = [&](auto index, int kb) __attribute__((always_inline)) {
+        constexpr int slot = decltype(index)::value;
+        constexpr int s1 = (slot + 1) % S::kSlots, s2 = (slot + 2) % S::kSlots, s3 = (slot + 3) % S::kSlots,
+                      s4 = (slot + 4) % S::kSlots;
+        const uint8_t *tA = lds + slot * S::kSlot, *tW = lds + s1 * S::kSlot;
+        const uint8_t *nA = lds + s2 * S::kSlot, *nW = lds + s3 * S::kSlot;
+        static_for<kPhases>([&](auto phase) __attribute__((always_inline)) {
+            constexpr int g = decltype(phase)::value, ks = g / TN, ni = g % TN, gw = (g + kAhead) % kPhases;
+            constexpr int after = g - kBarrier;  // phases since the barrier
+            // Row fragments [r0, r1) and copies [a0, a1) of A, [w0, w1) of W that this phase issues.
+            constexpr int r0 = ks == 0 ? ni * TM / TN : (after == 1 ? TM / 2 : 0);
+            constexpr int r1 = ks == 0 ? (ni + 1) * TM / TN : (after == 0 ? TM / 2 : (after == 1 ? TM : 0));
+            constexpr int a0 = ks == 0 ? ni * S::kCopyA / TN : 0, a1 = ks == 0 ? (ni + 1) * S::kCopyA / TN : 0;
+            constexpr int w0 = after < 0 ? 0 : after * S::kCopyW / kAhead;
+            constexpr int w1 = after < 0 ? 0 : (after + 1) * S::kCopyW / kAhead;
+            if constexpr (after == 0) {
                 copies_barrier<S::kCopyA>();  // block kb + 1 is there; A's kb + 2 may still be on the way
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const uint8_t *tA = lds + (ks < 3 ? slot : s2) * S::kSlot, *tW = lds + (ks < 3 ? s1 : s3) * S::kSlot;
+            fw[gw % (kAhead + 1)] = frag(after < 0 ? tW : nW, wn + 16 * (gw % TN), gw / TN);
 #pragma unroll
-            for (int i = 0; i < TM; i++) fa[(ks + 1) & 1][i] = frag(tA, wm + 32 * i, (ks + 1) & 3);
+            for (int i = r0; i < r1; i++) fa[ks ^ 1][i] = frag(ks == 0 ? tA : nA, wm + 16 * i, ks ^ 1);
+            static_for<a1 - a0>([&](auto j) __attribute__((always_inline)) {
+                copy_a(Index<a0 + decltype(j)::value>{}, kb + 2, s4);
+            });
+            static_for<w1 - w0>([&](auto j) __attribute__((always_inline)) {
+                copy_w(Index<w0 + decltype(j)::value>{}, kb + 2, slot);  // the slot that A's block kb leaves
+            });
+            // (every other phase takes the rows backwards, so that one operand changes from MFMA to MFMA, not two)
 #pragma unroll
-            for (int i = 0; i < TN; i++) fw[(ks + 1) & 1][i] = frag(tW, wn + 32 * i, (ks + 1) & 3);
-            if (ks == 0) copy_w(1, kb + 1, s3);
-            if (ks == 1) copy_a(0, kb + 2, s4);
-            if (ks == 2) copy_a(1, kb + 2, s4);
-            if (ks == 3) copy_w(0, kb + 2, slot);  // the slot that A's block kb leaves
-#pragma unroll
-            for (int ni = 0; ni < TN; ni++)
-#pragma unroll
-                for (int mi = 0; mi < TM; mi++)
-                    acc[ni][mi] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[ks & 1][ni], fa[ks & 1][mi], acc[ni][mi],
-                                                                        0, 0, 0);
-            if (ks == 0 || ks == 3)
-                schedule_step<TM + TN, TM * TN, S::kCopyW / 2>();
-            else
-                schedule_step<TM + TN, TM * TN, S::kCopyA / 2>();
+            for (int i = 0; i < TM; i++) {
+                const int mi = g & 1 ? TM - 1 - i : i;
+                acc[ni][mi] =
+                    __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[g % (kAhead + 1)], fa[ks][mi], acc[ni][mi], 0, 0, 0);
+            }
+            // Left alone, the compiler reads each fragment right before its MFMAs and waits for it.
+            if constexpr (1 + r1 - r0 > 0) __builtin_amdgcn_sched_group_barrier(0x100, 1 + r1 - r0, 0);  // LDS reads
+            if constexpr (a1 - a0 + w1 - w0 > 0) __builtin_amdgcn_sched_group_barrier(0x010, a1 - a0 + w1 - w0, 0);  // copies
+            __builtin_amdgcn_sched_group_barrier(0x008, TM, 0);  // MFMAs
             __builtin_amdgcn_sched_barrier(0);
-        }
-        slot = s2;
+        });
+    };
+    // Five blocks at a time, so that the slots are constants: block kb's A is in slot 2 kb % 5.
+    for (int kb = 0;; kb += 5) {
+        block(Index<0>{}, kb);
+        if (kb + 1 >= KB) break;
+        block(Index<2>{}, kb + 1);
+        if (kb + 2 >= KB) break;
+        block(Index<4>{}, kb + 2);
+        if (kb + 3 >= KB) break;
+        block(Index<1>{}, kb + 3);
+        if (kb + 4 >= KB) break;
+        block(Index<3>{}, kb + 4);
+        if (kb + 5 >= KB) break;
     }
 
-    // Register 4 g + i of a lane is channel 8 g + 4 (lane / 32) + i of row lane % 32.  Results pass through LDS so
-    // that whole row segments are stored: a wave's block of 32 TM rows x 256 bytes at a time, the 16-byte chunks
-    // of row r at chunk ^ (r % 16).
+    // A lane holds channels 4 (lane / 16) .. + 3 of row lane % 16 of each subtile.  Results pass through LDS so that
+    // whole row segments are stored: a wave's block of 16 TM rows x at most 256 bytes at a time, the 16-byte chunks of row r
+    // at chunk ^ (r % 16).
     float sa[TM];
 #pragma unroll
     for (int mi = 0; mi < TM; mi++) {
-        const int64_t m = m0 + wm + 32 * mi + (lane & 31);
+        const int64_t m = m0 + wm + 16 * mi + (lane & 15);
         int64_t src = m < mend ? m : -1;
         if constexpr (GATHER) {
             src = src >= 0 ? p.rtok[src] : -1;
@@ -251,43 +283,38 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         sa[mi] = src >= 0 ? p.sa[src] : 0.0f;
     }
     constexpr int kEl = OUT_BF16 ? 2 : 4;
-    constexpr int kSubs = TN * 32 * kEl > 256 ? 256 / (32 * kEl) : TN;  // channel subtiles per pass
-    constexpr int kRowBytes = kSubs * 32 * kEl, kChunks = kRowBytes / 16;
-    static_assert(4 * 32 * TM * kRowBytes <= S::kLds && (kChunks & (kChunks - 1)) == 0, "staging");
+    constexpr int kMaxRow = S::kWaves * 16 * TM * 256 <= S::kLds ? 256 : 128;
+    constexpr int kSubs = TN * 16 * kEl > kMaxRow ? kMaxRow / (16 * kEl) : TN;  // channel subtiles per pass
+    constexpr int kRowBytes = kSubs * 16 * kEl, kChunks = kRowBytes / 16;
+    static_assert(S::kWaves * 16 * TM * kRowBytes <= S::kLds && (kChunks & (kChunks - 1)) == 0, "staging");
     copies_barrier<0>();
-    uint8_t *blk = lds + wave * 32 * TM * kRowBytes;
+    uint8_t *blk = lds + wave * 16 * TM * kRowBytes;
 #pragma unroll
     for (int n1 = 0; n1 < TN; n1 += kSubs) {
 #pragma unroll
-        for (int ni = n1; ni < n1 + kSubs; ni++)
+        for (int ni = n1; ni < n1 + kSubs; ni++) {
+            const int nl = 16 * ni + 4 * (lane >> 4);
+            const int64_t n = n0 + wn + nl;
+            float sw[4] = {0.f, 0.f, 0.f, 0.f};
+            if (n < p.N) {
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const int nl = 32 * ni + 8 * g + 4 * (lane >> 5);
-                const int64_t n = n0 + wn + nl;
-                float4 sw = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (n < p.N) {
-                    sw.x = SW[n];
-                    sw.y = SW[n + 1];
-                    sw.z = SW[n + 2];
-                    sw.w = SW[n + 3];
-                }
-#pragma unroll
-                for (int mi = 0; mi < TM; mi++) {
-                    const int r = 32 * mi + (lane & 31);
-                    v4f v;
-                    v[0] = (float)acc[ni][mi][4 * g] * (sa[mi] * sw.x);
-                    v[1] = (float)acc[ni][mi][4 * g + 1] * (sa[mi] * sw.y);
-                    v[2] = (float)acc[ni][mi][4 * g + 2] * (sa[mi] * sw.z);
-                    v[3] = (float)acc[ni][mi][4 * g + 3] * (sa[mi] * sw.w);
-                    const int byte = (nl - 32 * n1) * kEl;
-                    store4<OUT_BF16>(blk + r * kRowBytes + ((((byte >> 4) ^ r) & (kChunks - 1)) << 4) + (byte & 15), 0, v);
-                }
+                for (int r = 0; r < 4; r++) sw[r] = SW[n + r];
             }
+#pragma unroll
+            for (int mi = 0; mi < TM; mi++) {
+                const int r = 16 * mi + (lane & 15);
+                v4f v;
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] = (float)acc[ni][mi][i] * (sa[mi] * sw[i]);
+                const int byte = (nl - 16 * n1) * kEl;
+                store4<OUT_BF16>(blk + r * kRowBytes + ((((byte >> 4) ^ r) & (kChunks - 1)) << 4) + (byte & 15), 0, v);
+            }
+        }
         // (the block is the wave's own: its LDS operations are in order)
 #pragma unroll
-        for (int j = 0; j < 32 * TM * kChunks / 64; j++) {
+        for (int j = 0; j < 16 * TM * kChunks / 64; j++) {
             const int idx = j * 64 + lane, r = idx / kChunks, ch = idx % kChunks;
-            const int64_t m = m0 + wm + r, n = n0 + wn + 32 * n1 + ch * (16 / kEl);
+            const int64_t m = m0 + wm + r, n = n0 + wn + 16 * n1 + ch * (16 / kEl);
             const u32x4 v = *reinterpret_cast<const u32x4 *>(blk + r * kRowBytes + (((ch ^ r) & (kChunks - 1)) << 4));
             if (m < mend && n < p.N)
                 *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(p.c) + (m * p.N + n) * kEl) = v;
@@ -296,7 +323,7 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
 }
 
 template <bool OUT_BF16, bool GROUPED, bool GATHER, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(256, 1) void gemm_int8_kernel(Int8Args p) {
+__global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(Int8Args p) {
     using S = TileShape<TM, TN, WM, WN>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
     int64_t m0, mend = p.M, n0, e = 0;
@@ -326,16 +353,16 @@ hipError_t launch_int8_tile(Int8Args p, bool out_bf16, hipStream_t stream) {
     p.n_ntiles = (p.N + S::BN - 1) / S::BN;
     const dim3 grid((unsigned)((p.n_mtiles * p.n_ntiles + 255) / 256 * 256));
     if (out_bf16)
-        gemm_int8_kernel<true, GROUPED, GATHER, TM, TN, WM, WN><<<grid, 256, 0, stream>>>(p);
+        gemm_int8_kernel<true, GROUPED, GATHER, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
     else
-        gemm_int8_kernel<false, GROUPED, GATHER, TM, TN, WM, WN><<<grid, 256, 0, stream>>>(p);
+        gemm_int8_kernel<false, GROUPED, GATHER, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 template <bool GROUPED, bool GATHER>
 hipError_t launch_int8(Int8Args p, bool out_bf16, hipStream_t stream) {
-    if (p.M >= 2048) return launch_int8_tile<GROUPED, GATHER, 4, 4, 2, 2>(p, out_bf16, stream);
-    return launch_int8_tile<GROUPED, GATHER, 2, 2, 2, 2>(p, out_bf16, stream);
+    if (p.M >= 2048) return launch_int8_tile<GROUPED, GATHER, 4, 8, 4, 2>(p, out_bf16, stream);
+    return launch_int8_tile<GROUPED, GATHER, 4, 4, 2, 2>(p, out_bf16, stream);
 }
 
 }  // namespace
