@@ -83,6 +83,7 @@ struct Int8Args {
     const int32_t *off, *rtok;
     int64_t E, T;     // T: rows of qa when rtok picks them
     int64_t n_mtiles, n_ntiles;
+    int64_t n_tail, n_ntiles_tail;  // dense: columns from n_tail on are covered by tiles of half the width
 };
 
 // Waits for this wave's LDS reads and for all but its last N copies into LDS, then for the workgroup.
@@ -127,7 +128,10 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     using S = TileShape<TM, TN, WM, WN>;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) & (S::kWaves - 1);
-    const int wm = (wave % WM) * 16 * TM, wn = (wave / WM) * 16 * TN;
+    // With 8 waves, waves w and w + 4 share a SIMD; they take different rows, so that absent rows idle half of every SIMD
+    // and not both waves of some.
+    static_assert(WM <= 4, "waves along the rows");
+    const int wn = (wave / WM) * 16 * TN, wm = (S::kWaves == 8 && wave >= 4 ? (wave % WM) ^ (WM - 1) : wave % WM) * 16 * TM;
     const int64_t K = p.K;
     const int KB = __builtin_amdgcn_readfirstlane((int)((K + 127) >> 7));
     const int64_t nrow = mend - m0 < S::BM ? mend - m0 : S::BM;
@@ -254,6 +258,37 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
             __builtin_amdgcn_sched_barrier(0);
         });
     };
+    // A wave whose rows are all absent (past the tile's last, or rows of no token) copies for the others and stores zeros
+    // in the rows below mend.
+    constexpr int kEl = OUT_BF16 ? 2 : 4;
+    uint64_t rows_here = 0;
+#pragma unroll
+    for (int i = 0; i < 16 * TM; i += 64) {
+        const int r = wm + i + lane;
+        bool here = i + lane < 16 * TM && r < nrow;
+        if constexpr (GATHER) {
+            const int64_t tok = here ? p.rtok[m0 + r] : -1;
+            here = tok >= 0 && tok < p.T;
+        }
+        rows_here |= __ballot(here);
+    }
+    if (__builtin_amdgcn_readfirstlane((int)(rows_here != 0)) == 0) {
+        for (int kb = 0, slot = 0; kb < KB; kb++) {
+            const int s4 = slot + 4 < S::kSlots ? slot + 4 : slot + 4 - S::kSlots;
+            static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, kb + 2, s4); });
+            copies_barrier<S::kCopyA>();
+            static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, kb + 2, slot); });
+            slot = slot + 2 < S::kSlots ? slot + 2 : slot + 2 - S::kSlots;
+        }
+        copies_barrier<0>();
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        constexpr int kChunks = TN * kEl;  // 16-byte chunks of a row's 16 TN channels
+        for (int idx = lane; idx < 16 * TM * kChunks; idx += 64) {
+            const int64_t m = m0 + wm + idx / kChunks, n = n0 + wn + idx % kChunks * (16 / kEl);
+            if (m < mend && n < p.N) *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(p.c) + (m * p.N + n) * kEl) = zero;
+        }
+        return;
+    }
     // Five blocks at a time, so that the slots are constants: block kb's A is in slot 2 kb % 5.
     for (int kb = 0;; kb += 5) {
         block(Index<0>{}, kb);
@@ -282,7 +317,6 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         }
         sa[mi] = src >= 0 ? p.sa[src] : 0.0f;
     }
-    constexpr int kEl = OUT_BF16 ? 2 : 4;
     constexpr int kMaxRow = S::kWaves * 16 * TM * 256 <= S::kLds ? 256 : 128;
     constexpr int kSubs = TN * 16 * kEl > kMaxRow ? kMaxRow / (16 * kEl) : TN;  // channel subtiles per pass
     constexpr int kRowBytes = kSubs * 16 * kEl, kChunks = kRowBytes / 16;
@@ -322,7 +356,9 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     }
 }
 
-template <bool OUT_BF16, bool GROUPED, bool GATHER, int TM, int TN, int WM, int WN>
+// One tile per workgroup.  GROUPED: tiles of an expert-sorted layout.  TAIL (dense): the tiles of columns [0, n_tail), then
+// tiles of half the width over the other columns, which fill what would be a last round of few whole tiles.
+template <bool OUT_BF16, bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(Int8Args p) {
     using S = TileShape<TM, TN, WM, WN>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
@@ -336,39 +372,237 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(
         m0 = __builtin_amdgcn_readfirstlane((int)m0);
         mend = __builtin_amdgcn_readfirstlane((int)mend);
     } else {
+        const int64_t i = xcd_order(blockIdx.x);
         int64_t mt, nt;
-        if (!dense_tile_at(xcd_order(blockIdx.x), p.n_mtiles, p.n_ntiles, mt, nt)) return;
+        if (!dense_tile_at(i, p.n_mtiles, p.n_ntiles, mt, nt)) {
+            if constexpr (TAIL) {
+                if (dense_tile_at(i - p.n_mtiles * p.n_ntiles, p.n_mtiles, p.n_ntiles_tail, mt, nt))
+                    int8_tile<OUT_BF16, TM, TN / 2, WM, WN, false>(lds, p, p.qw, p.sw, mt * S::BM, p.M,
+                                                                   p.n_tail + nt * (S::BN / 2));
+            }
+            return;
+        }
         m0 = mt * S::BM;
         n0 = nt * S::BN;
     }
     int8_tile<OUT_BF16, TM, TN, WM, WN, GATHER>(lds, p, p.qw + e * p.N * p.K, p.sw + e * p.N, m0, mend, n0);
 }
 
-constexpr int kTile = 128;  // the smallest tile's rows and channels
+// ---------------------------------------------------------------------------------------------------------
+// Few rows: a workgroup of 8 waves computes 16 TM rows x up to 16 NS channels, and the waves split K: wave w takes
+// blocks w, w + 8, ... of 128 codes, copies the block's rows of both operands into an LDS slot of its own, reads its
+// fragments, starts the copies of its next block and multiplies, with no barrier between the waves.  The 8 partial
+// sums meet in LDS by integer adds, whose order does not matter.
+// ---------------------------------------------------------------------------------------------------------
 
-template <bool GROUPED, bool GATHER, int TM, int TN, int WM, int WN>
-hipError_t launch_int8_tile(Int8Args p, bool out_bf16, hipStream_t stream) {
-    using S = TileShape<TM, TN, WM, WN>;
-    p.n_mtiles = GROUPED ? p.M / S::BM + p.E : (p.M + S::BM - 1) / S::BM;
-    p.n_ntiles = (p.N + S::BN - 1) / S::BN;
-    const dim3 grid((unsigned)((p.n_mtiles * p.n_ntiles + 255) / 256 * 256));
+constexpr int kSplitWaves = 8;
+
+template <bool OUT_BF16, int TM, int NS>
+__global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(Int8Args p, int64_t cols_per_wg) {
+    constexpr int kA = TM * 2048, kSlot = (TM + NS) * 2048, kSum = TM * NS * 1024;
+    constexpr int kLds = kSplitWaves * kSlot > kSum ? kSplitWaves * kSlot : kSum;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & (kSplitWaves - 1);
+    const int64_t K = p.K;
+    const int KB = (int)((K + 127) >> 7);
+    // Row tiles of one slice of channels are neighbours, so that the slice's weights are read by them together.
+    const int64_t nt = blockIdx.x / p.n_mtiles, mt = blockIdx.x - nt * p.n_mtiles;
+    const int64_t m0 = mt * 16 * TM, n0 = nt * cols_per_wg;
+    const int64_t nrow = p.M - m0 < 16 * TM ? p.M - m0 : 16 * TM;
+    const int64_t ncol = p.N - n0 < cols_per_wg ? p.N - n0 : cols_per_wg;
+    const i32x4 ra = make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
+    const i32x4 rw = make_rsrc(p.qw + n0 * K, (uint64_t)(ncol * K));
+    uint8_t *slot = lds + wave * kSlot;
+    const int c0 = (lane & 7) ^ (lane >> 3);
+    // Rows 8 j + lane / 8 of either operand, as in the tile kernel.
+    int voff[2 * (TM > NS ? TM : NS)];
+#pragma unroll
+    for (int j = 0; j < 2 * (TM > NS ? TM : NS); j++) voff[j] = (8 * j + (lane >> 3)) * (int)K + (j & 1 ? c0 ^ 1 : c0) * 16;
+    auto issue = [&](int kb) {
+        const bool in = kb < KB;
+        i32x4 ta = ra, tw = rw;
+        ta[2] = in ? ta[2] : 0;
+        tw[2] = in ? tw[2] : 0;
+        const int so = in ? kb * 128 : 0;
+        const int left = in ? (int)(K - (int64_t)kb * 128) : 128;
+        const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
+#pragma unroll
+        for (int j = 0; j < 2 * NS; j++)
+            fp8q_raw_buffer_load_lds(tw, (lds_ptr)(slot + kA + j * 1024), 16, (j & 1 ? ok1 : ok0) ? voff[j] : kFar, so, 0,
+                                     0);
+#pragma unroll
+        for (int j = 0; j < 2 * TM; j++)
+            fp8q_raw_buffer_load_lds(ta, (lds_ptr)(slot + j * 1024), 16, (j & 1 ? ok1 : ok0) ? voff[j] : kFar, so, 0, 0);
+    };
+    v4i acc[NS][TM];
+#pragma unroll
+    for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+        for (int mi = 0; mi < TM; mi++) acc[ni][mi] = (v4i){0, 0, 0, 0};
+    issue(wave);
+    for (int kb = wave; kb < KB; kb += kSplitWaves) {
+        __builtin_amdgcn_s_waitcnt(0);  // the block is there
+        asm volatile("" ::: "memory");
+        v4i fa[2][TM], fw[2][NS];
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+            const int ch = 4 * ks + (lane >> 4);
+#pragma unroll
+            for (int i = 0; i < TM; i++) fa[ks][i] = *reinterpret_cast<const v4i *>(slot + swz(16 * i + (lane & 15), ch));
+#pragma unroll
+            for (int i = 0; i < NS; i++)
+                fw[ks][i] = *reinterpret_cast<const v4i *>(slot + kA + swz(16 * i + (lane & 15), ch));
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the fragments are in registers: the slot may be overwritten
+        asm volatile("" ::: "memory");
+        issue(kb + kSplitWaves);
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+            for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+                for (int mi = 0; mi < TM; mi++)
+                    acc[ni][mi] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ks][ni], fa[ks][mi], acc[ni][mi], 0, 0, 0);
+    }
+    // The last copies (of no bytes) have retired and every wave is done with its slot before the sums take its place.
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    int *sum = reinterpret_cast<int *>(lds);
+    for (int i = tid; i < kSum / 4; i += 64 * kSplitWaves) sum[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+        for (int mi = 0; mi < TM; mi++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) atomicAdd(&sum[((ni * TM + mi) * 4 + r) * 64 + lane], acc[ni][mi][r]);
+    __syncthreads();
+    for (int q = wave; q < NS * TM; q += kSplitWaves) {
+        const int ni = q / TM, mi = q % TM;
+        const int64_t m = m0 + 16 * mi + (lane & 15);
+        const int nl = 16 * ni + 4 * (lane >> 4);  // channels nl .. nl + 3 of the slice: all in or all out
+        if (m >= p.M || nl >= ncol) continue;
+        const float sa = p.sa[m];
+        v4f v;
+#pragma unroll
+        for (int r = 0; r < 4; r++) v[r] = (float)sum[(q * 4 + r) * 64 + lane] * (sa * p.sw[n0 + nl + r]);
+        store4<OUT_BF16>(p.c, m * p.N + n0 + nl, v);
+    }
+}
+
+template <int TM, int NS>
+hipError_t launch_int8_split(Int8Args p, int64_t cols, bool out_bf16, hipStream_t stream) {
+    p.n_mtiles = (p.M + 16 * TM - 1) / (16 * TM);
+    p.n_ntiles = (p.N + cols - 1) / cols;
+    const dim3 grid((unsigned)(p.n_mtiles * p.n_ntiles));
     if (out_bf16)
-        gemm_int8_kernel<true, GROUPED, GATHER, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+        gemm_int8_split_kernel<true, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     else
-        gemm_int8_kernel<false, GROUPED, GATHER, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+        gemm_int8_split_kernel<false, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     return hipGetLastError();
 }
 
-template <bool GROUPED, bool GATHER>
-hipError_t launch_int8(Int8Args p, bool out_bf16, hipStream_t stream) {
-    if (p.M >= 2048) return launch_int8_tile<GROUPED, GATHER, 4, 8, 4, 2>(p, out_bf16, stream);
-    return launch_int8_tile<GROUPED, GATHER, 4, 4, 2, 2>(p, out_bf16, stream);
+template <int TM>
+hipError_t launch_int8_split(const Int8Args &p, int64_t cols, bool out_bf16, hipStream_t stream) {
+    switch ((cols + 15) / 16) {
+        case 1: return launch_int8_split<TM, 1>(p, cols, out_bf16, stream);
+        case 2: return launch_int8_split<TM, 2>(p, cols, out_bf16, stream);
+        case 3: return launch_int8_split<TM, 3>(p, cols, out_bf16, stream);
+        case 4: return launch_int8_split<TM, 4>(p, cols, out_bf16, stream);
+        default: return launch_int8_split<TM, 5>(p, cols, out_bf16, stream);
+    }
+}
+
+constexpr int kTile = 128;  // the smallest tile's rows and channels
+
+template <bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN>
+hipError_t launch_int8_tile(Int8Args p, int64_t n_tail, bool out_bf16, hipStream_t stream) {
+    using S = TileShape<TM, TN, WM, WN>;
+    p.n_mtiles = GROUPED ? p.M / S::BM + p.E : (p.M + S::BM - 1) / S::BM;
+    p.n_ntiles = (n_tail + S::BN - 1) / S::BN;
+    p.n_tail = n_tail;
+    p.n_ntiles_tail = (p.N - n_tail + S::BN / 2 - 1) / (S::BN / 2);
+    const dim3 grid((unsigned)((p.n_mtiles * (p.n_ntiles + p.n_ntiles_tail) + 255) / 256 * 256));
+    if (out_bf16)
+        gemm_int8_kernel<true, GROUPED, GATHER, TAIL, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+    else
+        gemm_int8_kernel<false, GROUPED, GATHER, TAIL, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+// The dense product's kernel and its shape, by estimated time in us.  The estimates were fitted to measurements on
+// shapes from 64 x 1024 x 16384 to 4096 x 16384 x 7168; they matter by their ratios, at the crossings.
+struct Int8Plan {
+    enum Kind { kSplitK, kSmall, kWide, kLarge } kind;
+    int tm;          // kSplitK: 16-row subtiles of a workgroup
+    int64_t cols;    // kSplitK: channels of a workgroup
+    int64_t n_tail;  // kLarge: columns covered by whole tiles
+};
+
+Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
+    const double ncu = cu_count();
+    const double KB = (double)((K + 127) / 128);
+    auto tiles = [](int64_t n, int64_t t) { return (double)((n + t - 1) / t); };
+    auto rounds = [](double n, double d) { return (double)(int64_t)((n + d - 1) / d); };
+    // 128 x 128 tiles, two to a CU: 0.42 us a block for a few tiles, 0.60 with one on every CU, 0.92 with two.
+    const double ts = tiles(M, 128) * tiles(N, 128);
+    Int8Plan best{Int8Plan::kSmall, 0, 0, N};
+    double cost = 5.0 + (ts <= ncu       ? KB * (0.42 + 0.18 * ts / ncu)
+                         : ts <= 2 * ncu ? KB * (0.28 + 0.32 * ts / ncu) + 3.0
+                                         : rounds(ts, 2 * ncu) * (KB * 0.92 + 3.0));
+    // 256 x 128 tiles, one to a CU: 0.88 us a block.
+    const double tw = tiles(M, 256) * tiles(N, 128), wide = KB * 0.88 + 3.0;
+    if (5.0 + rounds(tw, ncu) * wide < cost) {
+        cost = 5.0 + rounds(tw, ncu) * wide;
+        best = {Int8Plan::kWide, 0, 0, N};
+    }
+    // 256 x 256 tiles, one to a CU: 1.48 us a block; all of them, or whole rounds and then 256 x 128 tiles.
+    const double mt = tiles(M, 256), nt = tiles(N, 256), large = KB * 1.48 + 5.0;
+    if (5.0 + rounds(mt * nt, ncu) * large < cost) {
+        cost = 5.0 + rounds(mt * nt, ncu) * large;
+        best = {Int8Plan::kLarge, 0, 0, N};
+    }
+    const int64_t full = (int64_t)(mt * nt / ncu), cols = (int64_t)((double)full * ncu / mt);
+    if (full >= 1 && cols >= 1 && cols * 256 < N) {
+        const double tail = mt * tiles(N - cols * 256, 128);
+        const double c = 5.0 + (double)full * large + rounds(tail, ncu) * wide;
+        if (c < cost) {
+            cost = c;
+            best = {Int8Plan::kLarge, 0, 0, cols * 256};
+        }
+    }
+    // Waves that split K: a workgroup takes 8 blocks a round, whose copies come at up to 116 bytes a ns per CU and
+    // 14000 a ns over the chip; then the partial sums.
+    for (int tm = 1; tm <= 4; tm *= 2) {
+        if (tm > 1 && M <= 8 * tm) break;  // half of the rows would be absent
+        for (int64_t c = 8; c <= 80; c += 8) {
+            const double w = tiles(M, 16 * tm) * tiles(N, c), ns = (double)((c + 15) / 16);
+            if (w > 16 * ncu) continue;
+            const double act = w < ncu ? w : ncu, rate = 14000.0 / act < 116.0 ? 14000.0 / act : 116.0;
+            const double round = (16.0 * tm + (double)c) * 1.024 / rate;
+            const double t = 2.0 + rounds(w, ncu) * (rounds(KB, 8.0) * round + 0.165 * tm * ns);
+            if (t < cost) {
+                cost = t;
+                best = {Int8Plan::kSplitK, tm, c, N};
+            }
+            if (c >= N) break;
+        }
+    }
+    return best;
+}
+
+template <bool GATHER>
+hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t stream) {
+    if (p.M >= 2048) return launch_int8_tile<true, GATHER, false, 4, 8, 4, 2>(p, p.N, out_bf16, stream);
+    return launch_int8_tile<true, GATHER, false, 4, 4, 2, 2>(p, p.N, out_bf16, stream);
 }
 
 }  // namespace
 
 int64_t gemm_int8_blocks(int64_t M, int64_t N, int64_t E) {
-    // an upper bound: 128 x 128 tiles; -1 past 2^40
+    // An upper bound over the kernels: 128 x 128 tiles (the others launch fewer workgroups, or at most 16 for each CU);
+    // -1 past 2^40.
     const int64_t mt = M / kTile + (E > 0 ? E : 1), nt = (N + kTile - 1) / kTile;
     if (nt > 0 && mt > (int64_t(1) << 40) / nt) return -1;
     return mt * nt + 256;
@@ -386,16 +620,27 @@ hipError_t launch_quant_int8(const uint16_t *x, int64_t ld, int64_t M, int64_t K
 
 hipError_t launch_gemm_int8(const uint8_t *qa, const float *sa, const uint8_t *qw, const float *sw, void *c,
                             bool out_bf16, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-    const Int8Args p = {qa, sa, qw, sw, c, M, N, K, nullptr, nullptr, 0, M, 0, 0};
-    return launch_int8<false, false>(p, out_bf16, stream);
+    const Int8Args p = {qa, sa, qw, sw, c, M, N, K, nullptr, nullptr, 0, M, 0, 0, 0, 0};
+    const Int8Plan plan = plan_int8(M, N, K);
+    switch (plan.kind) {
+        case Int8Plan::kSplitK:
+            if (plan.tm == 1) return launch_int8_split<1>(p, plan.cols, out_bf16, stream);
+            if (plan.tm == 2) return launch_int8_split<2>(p, plan.cols, out_bf16, stream);
+            return launch_int8_split<4>(p, plan.cols, out_bf16, stream);
+        case Int8Plan::kSmall: return launch_int8_tile<false, false, false, 4, 4, 2, 2>(p, N, out_bf16, stream);
+        case Int8Plan::kWide: return launch_int8_tile<false, false, false, 4, 4, 4, 2>(p, N, out_bf16, stream);
+        default: break;
+    }
+    if (plan.n_tail < N) return launch_int8_tile<false, false, true, 4, 8, 4, 2>(p, plan.n_tail, out_bf16, stream);
+    return launch_int8_tile<false, false, false, 4, 8, 4, 2>(p, N, out_bf16, stream);
 }
 
 hipError_t launch_grouped_gemm_int8(const uint8_t *qa, const float *sa, int64_t T, const int32_t *row_token,
                                     const uint8_t *qw, const float *sw, void *c, bool out_bf16, const int32_t *off,
                                     int64_t E, int64_t M_total, int64_t N, int64_t K, hipStream_t stream) {
-    const Int8Args p = {qa, sa, qw, sw, c, M_total, N, K, off, row_token, E, T, 0, 0};
-    return row_token != nullptr ? launch_int8<true, true>(p, out_bf16, stream)
-                                : launch_int8<true, false>(p, out_bf16, stream);
+    const Int8Args p = {qa, sa, qw, sw, c, M_total, N, K, off, row_token, E, T, 0, 0, 0, 0};
+    return row_token != nullptr ? launch_int8_grouped<true>(p, out_bf16, stream)
+                                : launch_int8_grouped<false>(p, out_bf16, stream);
 }
 
 }  // namespace fp8q
