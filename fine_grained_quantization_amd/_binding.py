@@ -25,6 +25,8 @@ _lib = None
 def load_library(path: str = LIB_PATH):
     """Load libfp8q.so and declare the C signatures.  Raises if it has not been built."""
     global _lib
+    if _lib is not None and path == LIB_PATH:
+        return _lib
     with _lock:
         if _lib is not None and path == LIB_PATH:
             return _lib
@@ -98,17 +100,19 @@ def _check(rc: int, name: str):
 # The current stream's handle without building a Stream object (that costs ~3 us a call, a third of a
 # call's host time); torch.cuda.current_stream() where this accessor does not exist.
 _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+# Addresses go to ctypes as plain integers (the declared argument types make pointers of them).
 def _stream_ptr(stream):
     if stream is None and _RAW_STREAM is not None:
-        return ctypes.c_void_p(_RAW_STREAM(torch.cuda.current_device()))
+        return _RAW_STREAM(_GET_DEVICE())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _need(t: torch.Tensor, name: str, dtypes, ndim=None):
@@ -538,6 +542,8 @@ def _score_code(score):
 
 def _need_out(t, name, dtype, size):
     """A contiguous device tensor of one dtype and element count (an output, or an input of known size)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() == size:
+        return
     _need(t, name, (dtype,))
     if t.numel() != size:
         raise ValueError(f"{name} has {t.numel()} elements; expected {size}")
