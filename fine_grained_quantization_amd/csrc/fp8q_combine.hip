@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const void *__restrict
             const int64_t r = j0 + u < k ? row_of[t * k + j0 + u] : -1;  // the same in every lane
             const bool in = r >= 0 && r < rows;
             w[u] = in ? weight[t * k + j0 + u] : 0.0f;
-            v[u] = in ? src[r * chunks] : zero;
+            v[u] = in ? load_stream16(src + r * chunks) : zero;
         }
 #pragma unroll
         for (int u = 0; u < kSlots; u++) {
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
             u32x4 v[kSlots];
 #pragma unroll
             for (int u = 0; u < kSlots; u++)
-                v[u] = row[u] >= 0 ? static_cast<const u32x4 *>(c)[row[u] * chunks + ch] : zero;
+                v[u] = row[u] >= 0 ? load_stream16(static_cast<const u32x4 *>(c) + row[u] * chunks + ch) : zero;
 #pragma unroll
             for (int u = 0; u < kSlots; u++) {
                 if (row[u] < 0) continue;  // the same in every lane
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
                     dot[u] = __builtin_fmaf(x.f[i], dy.f[i], dot[u]);
                     dc.f[i] = w[u] * dy.f[i];
                 }
-                static_cast<u32x4 *>(grad_c)[row[u] * chunks + ch] = dc.pack();
+                __builtin_nontemporal_store(dc.pack(), static_cast<u32x4 *>(grad_c) + row[u] * chunks + ch);
             }
         }
 #pragma unroll
