@@ -258,14 +258,14 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // A wave whose rows are all absent (past the tile's last, or rows of no token) copies for the others and stores zeros
-    // in the rows below mend.
+    // A wave whose rows are all absent (past the tile's last, or rows of no token), or whose channels are, copies for the
+    // others and stores zeros where rows and channels are its own.
     constexpr int kEl = OUT_BF16 ? 2 : 4;
     uint64_t rows_here = 0;
 #pragma unroll
     for (int i = 0; i < 16 * TM; i += 64) {
         const int r = wm + i + lane;
-        bool here = i + lane < 16 * TM && r < nrow;
+        bool here = i + lane < 16 * TM && r < nrow && wn < ncol;
         if constexpr (GATHER) {
             const int64_t tok = here ? p.rtok[m0 + r] : -1;
             here = tok >= 0 && tok < p.T;
