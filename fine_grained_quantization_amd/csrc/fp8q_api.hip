@@ -395,7 +395,7 @@ int fp8q_moe_combine_backward(const void *grad_y, const void *c, int dtype, int6
     if (!aligned16(grad_y) || !aligned16(c) || !aligned16(grad_c) || !aligned4(row_of) || !aligned4(weight) ||
         !aligned4(grad_weight) || !aligned4(row_token) || !aligned4(offsets))
         return FP8Q_ERR_ALIGN;
-    if (T + rows / 64 + 1 > kMaxGrid) return FP8Q_ERR_SHAPE;
+    if (T + rows / 16 + 1 > kMaxGrid) return FP8Q_ERR_SHAPE;  // a workgroup per token and per 16 rows
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_moe_combine_backward(grad_y, c, dtype == FP8Q_OUT_BF16, rows, H, row_of, weight, T,

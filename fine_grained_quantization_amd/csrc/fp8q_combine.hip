@@ -42,6 +42,7 @@ struct Chunk {
 };
 
 constexpr int kSlots = 8;  // expert rows in flight per lane
+constexpr int kZeroRows = 16;
 
 // One workgroup of 256 lanes per (token, 256 chunks of its row): a lane owns one 16-byte chunk of y.
 template <bool BF16>
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const void *__restrict
 
 // The first T workgroups take one token each: a lane walks the row in 16-byte chunks, keeps one partial sum per
 // slot, and the workgroup adds the partials up in a fixed order.  The workgroups after them write zeros into the
-// rows below offsets[E] that no token has, 64 rows each.
+// rows below offsets[E] that no token has, kZeroRows rows each.
 template <bool BF16>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const void *__restrict__ grad_y, const void *__restrict__ c, int64_t rows, int64_t chunks,
@@ -90,8 +91,8 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const u32x4 zero = {0u, 0u, 0u, 0u};
     if ((int64_t)blockIdx.x >= T) {
         const int64_t used = offsets[E] < rows ? offsets[E] : rows;
-        const int64_t r0 = ((int64_t)blockIdx.x - T) * 64;
-        for (int i = wave; i < 64; i += 4) {
+        const int64_t r0 = ((int64_t)blockIdx.x - T) * kZeroRows;
+        for (int i = wave; i < kZeroRows; i += 4) {
             const int64_t r = r0 + i;
             if (r >= used) break;
             const int64_t t = __builtin_amdgcn_readfirstlane(row_token[r]);
@@ -169,7 +170,7 @@ hipError_t launch_moe_combine_backward(const void *grad_y, const void *c, bool b
                                        const int32_t *row_token, const int32_t *offsets, int64_t E, void *grad_c,
                                        float *grad_weight, hipStream_t stream) {
     const int64_t chunks = H / (bf16 ? 8 : 4);
-    const dim3 grid((unsigned)(T + (rows + 63) / 64));
+    const dim3 grid((unsigned)(T + (rows + kZeroRows - 1) / kZeroRows));
     if (bf16)
         moe_combine_backward_kernel<true><<<grid, 256, 0, stream>>>(grad_y, c, rows, chunks, row_of, weight, T, k,
                                                                     row_token, offsets, E, grad_c, grad_weight);

@@ -18,7 +18,7 @@
 namespace fp8q {
 namespace {
 
-constexpr int kGateChunk = 32;      // tokens per workgroup of the gating kernel
+constexpr int kGateChunk = 32;      // tokens per workgroup of the gating kernel, at most (a bit each in 32-bit masks)
 constexpr int kGateThreads = 1024;  // of the kernels that build the layout
 constexpr int kGateWaves = kGateThreads / 64;
 constexpr float kWeightEps = 1e-20f;
@@ -365,11 +365,11 @@ __device__ __forceinline__ void fill_empty(const LayoutArgs &o, const int32_t *s
 // order in which the bits arrived.
 // ONE: all tokens fit in one chunk.  Every workgroup then gates all of them (which costs less than a second
 // launch), workgroup 0 writes the outputs, and all of them share the filling of the empty rows.
-template <int LT, int R, bool ONE, int THREADS>
+template <int LT, int R, bool ONE, int THREADS, int CHUNK>
 __global__ __launch_bounds__(THREADS) void moe_gate_kernel(GateArgs a, LayoutArgs o) {
     constexpr int kAtOnce = THREADS / LT;  // tokens
-    constexpr int kPasses = kGateChunk / kAtOnce;
-    static_assert(kPasses * kAtOnce == kGateChunk && (!ONE || THREADS == kGateThreads), "tokens");
+    constexpr int kPasses = CHUNK / kAtOnce;
+    static_assert(kPasses * kAtOnce == CHUNK && (!ONE || THREADS == kGateThreads), "tokens");
     __shared__ uint32_t mask[kMoeMaxExperts];
     __shared__ int32_t total[ONE ? kMoeMaxExperts : 1];
     __shared__ int32_t seg[ONE ? kMoeMaxExperts + 1 : 1];
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(THREADS) void moe_gate_kernel(GateArgs a, LayoutArg
 #pragma unroll
     for (int i = 0; i < kPasses; i++) {
         const int tl = i * kAtOnce + tid / LT;
-        const int64_t t = c * kGateChunk + tl;
+        const int64_t t = c * CHUNK + tl;
         const bool valid = t < a.T;
         idx[i] = -1;
         if (__ballot(valid) == 0) continue;
@@ -421,7 +421,7 @@ __global__ __launch_bounds__(THREADS) void moe_gate_kernel(GateArgs a, LayoutArg
 #pragma unroll
     for (int i = 0; i < kPasses; i++) {
         const int tl = i * kAtOnce + tid / LT;
-        const int64_t t = c * kGateChunk + tl;
+        const int64_t t = c * CHUNK + tl;
         if (t >= a.T || in >= a.k) continue;
         int32_t r = idx[i] >= 0 ? __popc(mask[idx[i]] & ((1u << tl) - 1u)) : -1;
         if constexpr (ONE) {
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(THREADS) void moe_gate_kernel(GateArgs a, LayoutArg
 // its threads share), which gives the totals, the segment starts and the counts before its own chunks; it then
 // places the tokens of its chunks [c0, c1) and does its share of the empty rows.
 __global__ __launch_bounds__(kGateThreads) void moe_gate_layout_kernel(LayoutArgs o, int64_t T, int64_t C, int E,
-                                                                       int k, int64_t chunks_per_wg) {
+                                                                       int k, int chunk, int64_t chunks_per_wg) {
     __shared__ int32_t part_all[4096], part_before[4096];
     __shared__ int32_t total[kMoeMaxExperts], base[kMoeMaxExperts];
     __shared__ int32_t seg[kMoeMaxExperts + 1];
@@ -451,8 +451,8 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_layout_kernel(LayoutArg
     const uint32_t *counts = reinterpret_cast<const uint32_t *>(o.counts);
     const int col = tid % cols, p = tid / cols;
     // The first chunk's slots (at most 512), loaded here so that their latency passes beside the counts'.
-    const int64_t first = c0 * kGateChunk * k + tid;
-    const bool has = first < T * k && tid < kGateChunk * k;
+    const int64_t first = c0 * chunk * k + tid;
+    const bool has = first < T * k && tid < chunk * k;
     const int first_e = has ? o.topk_idx[first] : -1, first_r = has ? o.row_of[first] : 0;
     if (p < P) {
         int32_t all[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
@@ -501,8 +501,8 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_layout_kernel(LayoutArg
     fill_empty(o, seg, total, E, blockIdx.x, gridDim.x);
     __syncthreads();
     for (int64_t c = c0; c < c1; c++) {
-        const int64_t t0 = c * kGateChunk;
-        const int n = (int)((T - t0 < kGateChunk ? T - t0 : kGateChunk) * k);
+        const int64_t t0 = c * chunk;
+        const int n = (int)((T - t0 < chunk ? T - t0 : chunk) * k);
         for (int i = tid; i < n; i += kGateThreads) {
             const int64_t at = t0 * k + i;
             const int e = c == c0 ? first_e : o.topk_idx[at];
@@ -661,8 +661,16 @@ bool lanes_aligned(const void *p, int64_t ld, int n, int R, bool bf16) {
 
 }  // namespace
 
+namespace {
+// Tokens per workgroup: 16 while that gives every CU at most one workgroup, if the counts' rows need no padding (so that
+// the workspace stays within the other routing's), else 32.
+int chunk_tokens(int64_t T, int64_t E) { return T <= 4096 && E % 4 == 0 ? 16 : kGateChunk; }
+}  // namespace
+
 int64_t moe_gate_workspace_bytes(int64_t T, int64_t E) {
-    return T <= kGateChunk ? 0 : (T + kGateChunk - 1) / kGateChunk * ((E + 3) / 4 * 4);
+    if (T <= kGateChunk) return 0;
+    const int64_t chunk = chunk_tokens(T, E);
+    return (T + chunk - 1) / chunk * ((E + 3) / 4 * 4);
 }
 
 hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *topk_weight, int32_t *offsets,
@@ -670,12 +678,14 @@ hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *to
                                 hipStream_t stream) {
     const LayoutArgs o = {topk_idx, topk_weight, offsets, row_of, row_token, load, static_cast<uint8_t *>(workspace),
                           rows};
-    const int64_t C = (g.T + kGateChunk - 1) / kGateChunk;
-    const bool one = C <= 1;
+    const bool one = g.T <= kGateChunk;
+    const int chunk = one ? kGateChunk : chunk_tokens(g.T, g.E);
+    const int64_t C = (g.T + chunk - 1) / chunk;
     // A few tokens: 64 lanes each, the shortest way to an answer.  Many: 16 lanes each, which takes half the instructions
-    // (8192 tokens, 256 experts: MEASURED), where a lane then holds at most 32 experts.
+    // (8192 tokens, 256 experts: 15.4 us by 64 lanes, 11.0 by 16), where a lane then holds at most 32 experts.
     GateArgs a = gate_args(g, 16);
-    const bool narrow = !one && a.lanes_per_group >= 1 && regs_for(g.E / g.n_group, a.lanes_per_group) <= 32;
+    const bool narrow = chunk == kGateChunk && !one && a.lanes_per_group >= 1 &&
+                        regs_for(g.E / g.n_group, a.lanes_per_group) <= 32;
     if (!narrow) a = gate_args(g, 64);
     const int R = regs_for(g.E / g.n_group, a.lanes_per_group);
     a.vec = lanes_aligned(g.logits, g.ld, g.E / g.n_group, R, g.bf16);
@@ -684,14 +694,16 @@ hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *to
     const int64_t blocks = one ? (rows / 2048 < 1 ? 1 : (rows / 2048 > 32 ? 32 : rows / 2048)) : C;
     const dim3 grid((unsigned)blocks);
     switch (R) {
-#define FP8Q_GATE_CASE(N)                                                                      \
-    case N:                                                                                    \
-        if (one)                                                                               \
-            moe_gate_kernel<64, N, true, kGateThreads><<<grid, kGateThreads, 0, stream>>>(a, o); \
-        else if (narrow)                                                                       \
-            moe_gate_kernel<16, N, false, 512><<<grid, 512, 0, stream>>>(a, o);                \
-        else                                                                                   \
-            moe_gate_kernel<64, N, false, 512><<<grid, 512, 0, stream>>>(a, o);                \
+#define FP8Q_GATE_CASE(N)                                                                          \
+    case N:                                                                                        \
+        if (one)                                                                                   \
+            moe_gate_kernel<64, N, true, kGateThreads, 32><<<grid, kGateThreads, 0, stream>>>(a, o); \
+        else if (narrow)                                                                           \
+            moe_gate_kernel<16, N, false, 512, 32><<<grid, 512, 0, stream>>>(a, o);                \
+        else if (chunk == 16)                                                                      \
+            moe_gate_kernel<64, N, false, 1024, 16><<<grid, 1024, 0, stream>>>(a, o);              \
+        else                                                                                       \
+            moe_gate_kernel<64, N, false, 1024, 32><<<grid, 1024, 0, stream>>>(a, o);              \
         break;
         FP8Q_GATE_CASE(1)
         FP8Q_GATE_CASE(2)
@@ -705,7 +717,7 @@ hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *to
     if (!one) {
         const int64_t per = (C + 255) / 256;  // at most 256 workgroups: each reads all counts
         moe_gate_layout_kernel<<<dim3((unsigned)((C + per - 1) / per)), kGateThreads, 0, stream>>>(o, g.T, C, g.E, g.k,
-                                                                                                   per);
+                                                                                                   chunk, per);
     }
     return hipGetLastError();
 }

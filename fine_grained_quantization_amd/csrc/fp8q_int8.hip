@@ -397,7 +397,10 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(
 
 constexpr int kSplitWaves = 8;
 
-template <bool OUT_BF16, int TM, int NS>
+// MODE 0: dense.  1: expert segments; a workgroup takes one slice of one expert's channels and walks the segment's rows
+// 16 TM at a time.  2: the same with row r's codes those of token rtok[r]; where none of the rows has a token it only
+// stores zeros.
+template <bool OUT_BF16, int MODE, int TM, int NS>
 __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(Int8Args p, int64_t cols_per_wg) {
     constexpr int kA = TM * 2048, kSlot = (TM + NS) * 2048, kSum = TM * NS * 1024;
     constexpr int kLds = kSplitWaves * kSlot > kSum ? kSplitWaves * kSlot : kSum;
@@ -406,111 +409,157 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & (kSplitWaves - 1);
     const int64_t K = p.K;
     const int KB = (int)((K + 127) >> 7);
-    // Row tiles of one slice of channels are neighbours, so that the slice's weights are read by them together.
-    const int64_t nt = blockIdx.x / p.n_mtiles, mt = blockIdx.x - nt * p.n_mtiles;
-    const int64_t m0 = mt * 16 * TM, n0 = nt * cols_per_wg;
-    const int64_t nrow = p.M - m0 < 16 * TM ? p.M - m0 : 16 * TM;
+    int64_t m0, mend, n0, e = 0;
+    if constexpr (MODE == 0) {
+        // Row tiles of one slice of channels are neighbours, so that the slice's weights are read by them together.
+        const int64_t nt = blockIdx.x / p.n_mtiles;
+        m0 = (blockIdx.x - nt * p.n_mtiles) * 16 * TM;
+        mend = p.M - m0 < 16 * TM ? p.M : m0 + 16 * TM;
+        n0 = nt * cols_per_wg;
+    } else {
+        e = blockIdx.x / p.n_ntiles;
+        n0 = (blockIdx.x - e * p.n_ntiles) * cols_per_wg;
+        // the segment, cut to [0, M)
+        const int64_t lo = p.off[e], hi = p.off[e + 1];
+        m0 = lo < 0 ? 0 : (lo > p.M ? p.M : lo);
+        mend = hi < m0 ? m0 : (hi > p.M ? p.M : hi);
+    }
     const int64_t ncol = p.N - n0 < cols_per_wg ? p.N - n0 : cols_per_wg;
-    const i32x4 ra = make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
-    const i32x4 rw = make_rsrc(p.qw + n0 * K, (uint64_t)(ncol * K));
+    const i32x4 rw = make_rsrc(p.qw + (e * p.N + n0) * K, (uint64_t)(ncol * K));
+    const float *SW = p.sw + e * p.N + n0;
     uint8_t *slot = lds + wave * kSlot;
     const int c0 = (lane & 7) ^ (lane >> 3);
     // Rows 8 j + lane / 8 of either operand, as in the tile kernel.
-    int voff[2 * (TM > NS ? TM : NS)];
+    int wvoff[2 * NS], avoff[2 * TM];
 #pragma unroll
-    for (int j = 0; j < 2 * (TM > NS ? TM : NS); j++) voff[j] = (8 * j + (lane >> 3)) * (int)K + (j & 1 ? c0 ^ 1 : c0) * 16;
-    auto issue = [&](int kb) {
-        const bool in = kb < KB;
-        i32x4 ta = ra, tw = rw;
-        ta[2] = in ? ta[2] : 0;
-        tw[2] = in ? tw[2] : 0;
-        const int so = in ? kb * 128 : 0;
-        const int left = in ? (int)(K - (int64_t)kb * 128) : 128;
-        const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
-#pragma unroll
-        for (int j = 0; j < 2 * NS; j++)
-            fp8q_raw_buffer_load_lds(tw, (lds_ptr)(slot + kA + j * 1024), 16, (j & 1 ? ok1 : ok0) ? voff[j] : kFar, so, 0,
-                                     0);
-#pragma unroll
-        for (int j = 0; j < 2 * TM; j++)
-            fp8q_raw_buffer_load_lds(ta, (lds_ptr)(slot + j * 1024), 16, (j & 1 ? ok1 : ok0) ? voff[j] : kFar, so, 0, 0);
-    };
-    v4i acc[NS][TM];
-#pragma unroll
-    for (int ni = 0; ni < NS; ni++)
-#pragma unroll
-        for (int mi = 0; mi < TM; mi++) acc[ni][mi] = (v4i){0, 0, 0, 0};
-    issue(wave);
-    for (int kb = wave; kb < KB; kb += kSplitWaves) {
-        __builtin_amdgcn_s_waitcnt(0);  // the block is there
-        asm volatile("" ::: "memory");
-        v4i fa[2][TM], fw[2][NS];
-#pragma unroll
-        for (int ks = 0; ks < 2; ks++) {
-            const int ch = 4 * ks + (lane >> 4);
-#pragma unroll
-            for (int i = 0; i < TM; i++) fa[ks][i] = *reinterpret_cast<const v4i *>(slot + swz(16 * i + (lane & 15), ch));
-#pragma unroll
-            for (int i = 0; i < NS; i++)
-                fw[ks][i] = *reinterpret_cast<const v4i *>(slot + kA + swz(16 * i + (lane & 15), ch));
-        }
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // the fragments are in registers: the slot may be overwritten
-        asm volatile("" ::: "memory");
-        issue(kb + kSplitWaves);
-#pragma unroll
-        for (int ks = 0; ks < 2; ks++)
-#pragma unroll
-            for (int ni = 0; ni < NS; ni++)
-#pragma unroll
-                for (int mi = 0; mi < TM; mi++)
-                    acc[ni][mi] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ks][ni], fa[ks][mi], acc[ni][mi], 0, 0, 0);
+    for (int j = 0; j < 2 * NS; j++) {
+        const int r = 8 * j + (lane >> 3);
+        wvoff[j] = r < ncol ? r * (int)K + (j & 1 ? c0 ^ 1 : c0) * 16 : kFar;
     }
-    // The last copies (of no bytes) have retired and every wave is done with its slot before the sums take its place.
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
     int *sum = reinterpret_cast<int *>(lds);
-    for (int i = tid; i < kSum / 4; i += 64 * kSplitWaves) sum[i] = 0;
-    __syncthreads();
+    for (; m0 < mend; m0 += 16 * TM) {
+        const int64_t nrow = mend - m0 < 16 * TM ? mend - m0 : 16 * TM;
+        if constexpr (MODE == 2) {
+            int64_t tok = lane < nrow ? p.rtok[m0 + lane] : -1;
+            static_assert(16 * TM <= 64, "a lane per row");
+            if (__ballot(tok >= 0 && tok < p.T) == 0) {  // the same in every wave
+                constexpr int kEl = OUT_BF16 ? 2 : 4;
+                const u32x4 zero = {0u, 0u, 0u, 0u};
+                const int chunks = (int)(ncol * kEl / 16);  // channels come in multiples of 8
+                for (int i = tid; i < nrow * chunks; i += 64 * kSplitWaves)
+                    *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(p.c) + ((m0 + i / chunks) * p.N + n0) * kEl +
+                                               i % chunks * 16) = zero;
+                continue;
+            }
+        }
+        const i32x4 ra = MODE == 2 ? make_rsrc(p.qa, (uint64_t)(p.T * K)) : make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
 #pragma unroll
-    for (int ni = 0; ni < NS; ni++)
+        for (int j = 0; j < 2 * TM; j++) {
+            const int r = 8 * j + (lane >> 3);
+            int64_t row = r < nrow ? r : -1;
+            if constexpr (MODE == 2) row = row >= 0 ? p.rtok[m0 + row] : -1;
+            avoff[j] = row >= 0 && (MODE != 2 || row < p.T) ? (int)(row * K) + (j & 1 ? c0 ^ 1 : c0) * 16 : kFar;
+        }
+        auto issue = [&](int kb) {
+            const bool in = kb < KB;
+            i32x4 ta = ra, tw = rw;
+            ta[2] = in ? ta[2] : 0;
+            tw[2] = in ? tw[2] : 0;
+            const int so = in ? kb * 128 : 0;
+            const int left = in ? (int)(K - (int64_t)kb * 128) : 128;
+            const bool ok0 = c0 * 16 < left, ok1 = (c0 ^ 1) * 16 < left;
 #pragma unroll
-        for (int mi = 0; mi < TM; mi++)
+            for (int j = 0; j < 2 * NS; j++)
+                fp8q_raw_buffer_load_lds(tw, (lds_ptr)(slot + kA + j * 1024), 16, (j & 1 ? ok1 : ok0) ? wvoff[j] : kFar, so,
+                                         0, 0);
 #pragma unroll
-            for (int r = 0; r < 4; r++) atomicAdd(&sum[((ni * TM + mi) * 4 + r) * 64 + lane], acc[ni][mi][r]);
-    __syncthreads();
-    for (int q = wave; q < NS * TM; q += kSplitWaves) {
-        const int ni = q / TM, mi = q % TM;
-        const int64_t m = m0 + 16 * mi + (lane & 15);
-        const int nl = 16 * ni + 4 * (lane >> 4);  // channels nl .. nl + 3 of the slice: all in or all out
-        if (m >= p.M || nl >= ncol) continue;
-        const float sa = p.sa[m];
-        v4f v;
+            for (int j = 0; j < 2 * TM; j++)
+                fp8q_raw_buffer_load_lds(ta, (lds_ptr)(slot + j * 1024), 16, (j & 1 ? ok1 : ok0) ? avoff[j] : kFar, so, 0,
+                                         0);
+        };
+        v4i acc[NS][TM];
 #pragma unroll
-        for (int r = 0; r < 4; r++) v[r] = (float)sum[(q * 4 + r) * 64 + lane] * (sa * p.sw[n0 + nl + r]);
-        store4<OUT_BF16>(p.c, m * p.N + n0 + nl, v);
+        for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+            for (int mi = 0; mi < TM; mi++) acc[ni][mi] = (v4i){0, 0, 0, 0};
+        issue(wave);
+        for (int kb = wave; kb < KB; kb += kSplitWaves) {
+            __builtin_amdgcn_s_waitcnt(0);  // the block is there
+            asm volatile("" ::: "memory");
+            v4i fa[2][TM], fw[2][NS];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                const int ch = 4 * ks + (lane >> 4);
+#pragma unroll
+                for (int i = 0; i < TM; i++)
+                    fa[ks][i] = *reinterpret_cast<const v4i *>(slot + swz(16 * i + (lane & 15), ch));
+#pragma unroll
+                for (int i = 0; i < NS; i++)
+                    fw[ks][i] = *reinterpret_cast<const v4i *>(slot + kA + swz(16 * i + (lane & 15), ch));
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // the fragments are in registers: the slot may be overwritten
+            asm volatile("" ::: "memory");
+            issue(kb + kSplitWaves);
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+                    for (int mi = 0; mi < TM; mi++)
+                        acc[ni][mi] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[ks][ni], fa[ks][mi], acc[ni][mi], 0, 0, 0);
+        }
+        // The last copies (of no bytes) have retired and every wave is done with its slot before the sums take its place.
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        for (int i = tid; i < kSum / 4; i += 64 * kSplitWaves) sum[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int ni = 0; ni < NS; ni++)
+#pragma unroll
+            for (int mi = 0; mi < TM; mi++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) atomicAdd(&sum[((ni * TM + mi) * 4 + r) * 64 + lane], acc[ni][mi][r]);
+        __syncthreads();
+        for (int q = wave; q < NS * TM; q += kSplitWaves) {
+            const int ni = q / TM, mi = q % TM;
+            const int64_t m = m0 + 16 * mi + (lane & 15);
+            const int nl = 16 * ni + 4 * (lane >> 4);  // channels nl .. nl + 3 of the slice: all in or all out
+            if (m >= mend || nl >= ncol) continue;
+            int64_t src = m;
+            if constexpr (MODE == 2) {
+                src = p.rtok[m];
+                if (src >= p.T) src = -1;
+            }
+            const float sa = src >= 0 ? p.sa[src] : 0.0f;
+            v4f v;
+#pragma unroll
+            for (int r = 0; r < 4; r++) v[r] = (float)sum[(q * 4 + r) * 64 + lane] * (sa * SW[nl + r]);
+            store4<OUT_BF16>(p.c, m * p.N + n0 + nl, v);
+        }
+        __syncthreads();  // the sums have been read before the next rows' copies overwrite them
     }
 }
 
-template <int TM, int NS>
+template <int MODE, int TM, int NS>
 hipError_t launch_int8_split(Int8Args p, int64_t cols, bool out_bf16, hipStream_t stream) {
-    p.n_mtiles = (p.M + 16 * TM - 1) / (16 * TM);
+    p.n_mtiles = MODE == 0 ? (p.M + 16 * TM - 1) / (16 * TM) : p.E;
     p.n_ntiles = (p.N + cols - 1) / cols;
     const dim3 grid((unsigned)(p.n_mtiles * p.n_ntiles));
     if (out_bf16)
-        gemm_int8_split_kernel<true, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
+        gemm_int8_split_kernel<true, MODE, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     else
-        gemm_int8_split_kernel<false, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
+        gemm_int8_split_kernel<false, MODE, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     return hipGetLastError();
 }
 
-template <int TM>
-hipError_t launch_int8_split(const Int8Args &p, int64_t cols, bool out_bf16, hipStream_t stream) {
+template <int TM, int MODE>
+hipError_t launch_int8_split_cols(const Int8Args &p, int64_t cols, bool out_bf16, hipStream_t stream) {
     switch ((cols + 15) / 16) {
-        case 1: return launch_int8_split<TM, 1>(p, cols, out_bf16, stream);
-        case 2: return launch_int8_split<TM, 2>(p, cols, out_bf16, stream);
-        case 3: return launch_int8_split<TM, 3>(p, cols, out_bf16, stream);
-        case 4: return launch_int8_split<TM, 4>(p, cols, out_bf16, stream);
-        default: return launch_int8_split<TM, 5>(p, cols, out_bf16, stream);
+        case 1: return launch_int8_split<MODE, TM, 1>(p, cols, out_bf16, stream);
+        case 2: return launch_int8_split<MODE, TM, 2>(p, cols, out_bf16, stream);
+        case 3: return launch_int8_split<MODE, TM, 3>(p, cols, out_bf16, stream);
+        case 4: return launch_int8_split<MODE, TM, 4>(p, cols, out_bf16, stream);
+        default: return launch_int8_split<MODE, TM, 5>(p, cols, out_bf16, stream);
     }
 }
 
@@ -534,7 +583,7 @@ hipError_t launch_int8_tile(Int8Args p, int64_t n_tail, bool out_bf16, hipStream
 // The dense product's kernel and its shape, by estimated time in us.  The estimates were fitted to measurements on
 // shapes from 64 x 1024 x 16384 to 4096 x 16384 x 7168; they matter by their ratios, at the crossings.
 struct Int8Plan {
-    enum Kind { kSplitK, kSmall, kWide, kLarge } kind;
+    enum Kind { kSplitK, kSmall, kTall, kWide, kLarge } kind;
     int tm;          // kSplitK: 16-row subtiles of a workgroup
     int64_t cols;    // kSplitK: channels of a workgroup
     int64_t n_tail;  // kLarge: columns covered by whole tiles
@@ -545,16 +594,21 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
     const double KB = (double)((K + 127) / 128);
     auto tiles = [](int64_t n, int64_t t) { return (double)((n + t - 1) / t); };
     auto rounds = [](double n, double d) { return (double)(int64_t)((n + d - 1) / d); };
-    // 128 x 128 tiles, two to a CU: 0.42 us a block for a few tiles, 0.60 with one on every CU, 0.92 with two.
+    // 128 x 128 tiles, two to a CU: 0.42 us a block for a few tiles, 0.60 with one on every CU, 0.92 with two, 1.05 over
+    // many rounds.
     const double ts = tiles(M, 128) * tiles(N, 128);
     Int8Plan best{Int8Plan::kSmall, 0, 0, N};
     double cost = 5.0 + (ts <= ncu       ? KB * (0.42 + 0.18 * ts / ncu)
                          : ts <= 2 * ncu ? KB * (0.28 + 0.32 * ts / ncu) + 3.0
-                                         : rounds(ts, 2 * ncu) * (KB * 0.92 + 3.0));
-    // 256 x 128 tiles, one to a CU: 0.88 us a block.
-    const double tw = tiles(M, 256) * tiles(N, 128), wide = KB * 0.88 + 3.0;
-    if (5.0 + rounds(tw, ncu) * wide < cost) {
-        cost = 5.0 + rounds(tw, ncu) * wide;
+                                         : rounds(ts, 2 * ncu) * (KB * 1.05 + 3.0));
+    // 256 x 128 or 128 x 256 tiles, one to a CU: 0.88 us a block.
+    const double half = KB * 0.88 + 3.0, tt = tiles(M, 256) * tiles(N, 128), tw = tiles(M, 128) * tiles(N, 256);
+    if (5.0 + rounds(tt, ncu) * half < cost) {
+        cost = 5.0 + rounds(tt, ncu) * half;
+        best = {Int8Plan::kTall, 0, 0, N};
+    }
+    if (5.0 + rounds(tw, ncu) * half < cost) {
+        cost = 5.0 + rounds(tw, ncu) * half;
         best = {Int8Plan::kWide, 0, 0, N};
     }
     // 256 x 256 tiles, one to a CU: 1.48 us a block; all of them, or whole rounds and then 256 x 128 tiles.
@@ -566,7 +620,7 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
     const int64_t full = (int64_t)(mt * nt / ncu), cols = (int64_t)((double)full * ncu / mt);
     if (full >= 1 && cols >= 1 && cols * 256 < N) {
         const double tail = mt * tiles(N - cols * 256, 128);
-        const double c = 5.0 + (double)full * large + rounds(tail, ncu) * wide;
+        const double c = 5.0 + (double)full * large + rounds(tail, ncu) * half;
         if (c < cost) {
             cost = c;
             best = {Int8Plan::kLarge, 0, 0, cols * 256};
@@ -592,15 +646,31 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-// The host sees the layout's capacity (T k + 127 E rows and a little) and not the segments.  256 x 256 tiles, unless the
-// experts have few rows on average or those tiles would not fill the CUs: then 128 x 128 tiles, two to a CU.  Measured
-// with 64 experts of 2048 x 7168 (256 / 128): 4 rows on average 204 / 180 us, 16 rows 207 / 186, 64 rows 212 / 231, 256
-// rows 300 / 359, 1024 rows 876 / 1098; 16 experts of 1024 x 1024 with 500 rows (190 large tiles): 24.9 / 23.5.
+// The host sees the layout's capacity (T k + 127 E rows, rounded up to 128) and not the segments.
+//  - Up to 2 rows an expert on average, or up to 16 and so few 128 x 128 tiles that they leave CUs idle: the waves split K
+//    (one token, 8 of 64 experts of 2048 x 7168: 26 us, by 128 x 128 tiles 39; 32 tokens: 195 and 180).
+//  - Up to 32 rows, or where the estimated time is less: 128 x 128 tiles, two to a CU.  Measured with 64 experts of 2048 x
+//    7168 (256 x 256 tiles / 128 x 128): 4 rows on average 204 / 180 us, 16 rows 207 / 186, 64 rows 212 / 231, 256 rows 300
+//    / 359, 1024 rows 876 / 1098.
+//  - Else 256 x 256 tiles.
 template <bool GATHER>
 hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t stream) {
-    const int64_t rows = p.M > 127 * p.E ? p.M - 127 * p.E : 0;
-    const int64_t large = (rows / 256 + p.E / 2) * ((p.N + 255) / 256);
-    if (rows <= 32 * p.E || large < cu_count())
+    const int64_t rows = p.M > 127 * p.E + 64 ? p.M - 127 * p.E - 64 : 0;
+    const int64_t ncu = cu_count(), KB = (p.K + 127) / 128;
+    auto tiles = [](int64_t n, int64_t t) { return (n + t - 1) / t; };
+    if (rows <= 2 * p.E || (rows <= 16 * p.E && p.E * tiles(p.N, 128) <= ncu)) {
+        // A slice of channels per workgroup and expert: as few slices as put a workgroup on every CU, at most 80 channels.
+        const int64_t want = (ncu + p.E - 1) / p.E;
+        int64_t cols = 8 * ((p.N / 8 + want - 1) / want);
+        cols = cols < 80 ? cols : 80;
+        return launch_int8_split_cols<1, GATHER ? 2 : 1>(p, cols, out_bf16, stream);
+    }
+    const int64_t small = (rows + 64 * p.E) / 128 * tiles(p.N, 128);
+    const int64_t large = ((rows + 64 * p.E) / 256 + p.E / 4) * tiles(p.N, 256);
+    const double t_small = small <= ncu ? KB * 0.60 + 5.0 : (double)tiles(small, 2 * ncu) * (KB * 1.05 + 3.0);
+    const double t_large = (double)tiles(large, ncu) * (KB * 1.48 + 6.0);
+    const double t_read = (double)p.E * p.N * p.K / 5.0e6;  // the weights from memory, at 5 TB/s
+    if (rows <= 32 * p.E || (t_small < t_large && t_large > t_read))
         return launch_int8_tile<true, GATHER, false, 4, 4, 2, 2>(p, p.N, out_bf16, stream);
     return launch_int8_tile<true, GATHER, false, 4, 8, 4, 2>(p, p.N, out_bf16, stream);
 }
@@ -631,11 +701,12 @@ hipError_t launch_gemm_int8(const uint8_t *qa, const float *sa, const uint8_t *q
     const Int8Plan plan = plan_int8(M, N, K);
     switch (plan.kind) {
         case Int8Plan::kSplitK:
-            if (plan.tm == 1) return launch_int8_split<1>(p, plan.cols, out_bf16, stream);
-            if (plan.tm == 2) return launch_int8_split<2>(p, plan.cols, out_bf16, stream);
-            return launch_int8_split<4>(p, plan.cols, out_bf16, stream);
+            if (plan.tm == 1) return launch_int8_split_cols<1, 0>(p, plan.cols, out_bf16, stream);
+            if (plan.tm == 2) return launch_int8_split_cols<2, 0>(p, plan.cols, out_bf16, stream);
+            return launch_int8_split_cols<4, 0>(p, plan.cols, out_bf16, stream);
         case Int8Plan::kSmall: return launch_int8_tile<false, false, false, 4, 4, 2, 2>(p, N, out_bf16, stream);
-        case Int8Plan::kWide: return launch_int8_tile<false, false, false, 4, 4, 4, 2>(p, N, out_bf16, stream);
+        case Int8Plan::kTall: return launch_int8_tile<false, false, false, 4, 4, 4, 2>(p, N, out_bf16, stream);
+        case Int8Plan::kWide: return launch_int8_tile<false, false, false, 4, 4, 2, 4>(p, N, out_bf16, stream);
         default: break;
     }
     if (plan.n_tail < N) return launch_int8_tile<false, false, true, 4, 8, 4, 2>(p, plan.n_tail, out_bf16, stream);

@@ -340,8 +340,9 @@ int fp8q_moe_gather_fp8(const uint8_t *q, const float *s, int64_t T, int64_t K, 
  * ------------------------------------------------------------------------- */
 typedef enum { FP8Q_SCORE_SIGMOID = 0, FP8Q_SCORE_SOFTMAX = 1 } fp8q_score;
 
-/* Bytes of device workspace fp8q_moe_gate_topk needs (0 up to 32 tokens, then
- * E rounded up to 4 for every 32 tokens).  Returns -1 for invalid sizes. */
+/* Bytes of device workspace fp8q_moe_gate_topk needs: 0 up to 32 tokens, then E
+ * for every 16 tokens (up to 4096 tokens, E a multiple of 4) or E rounded up to
+ * a multiple of 4 for every 32.  Returns -1 for invalid sizes. */
 int64_t fp8q_moe_gate_workspace_bytes(int64_t T, int64_t E);
 
 /* Scores, group-limited top-k, weights and the expert-sorted layout.  For token t

@@ -42,7 +42,7 @@ def test_gate(lib, change, want):
 
 def test_gate_workspace(lib):
     need = lib.fp8q_moe_gate_workspace_bytes
-    assert need(0, 5) == 0 and need(32, 256) == 0 and need(33, 256) == 512 and need(65, 5) == 24
+    assert need(0, 5) == 0 and need(32, 256) == 0 and need(33, 256) == 768 and need(65, 5) == 24 and need(4097, 8) == 129 * 8
     assert need(-1, 5) == -1 and need(5, 0) == -1 and need(5, 1025) == -1
 
 

@@ -132,7 +132,7 @@ def test_masked_infinite_and_extreme_logits():
             check(sel, k, kind, None, groups, True, 1.0, got)
 
 
-@pytest.mark.parametrize("T,E,k", [(8200, 12, 2), (20000, 40, 3), (9000, 1024, 1)])
+@pytest.mark.parametrize("T,E,k", [(8200, 12, 2), (20000, 40, 3), (9000, 1024, 1), (4096, 36, 5), (4097, 36, 5), (2000, 37, 4)])
 def test_layout_of_many_tokens(T, E, k):
     """Past 256 chunks a workgroup places several of them."""
     rng = np.random.default_rng([8, T])
