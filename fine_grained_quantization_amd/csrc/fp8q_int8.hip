@@ -25,7 +25,8 @@ __device__ __forceinline__ uint32_t int8x4(uint32_t d0, uint32_t d1, double inv)
 
 // One workgroup per row, the row's first CH * 2048 elements kept in registers between the two passes.  |x| <= amax
 // and s = fl32(amax / 127) give |x / s| <= 127.008 (the most over every bf16 amax, reached where s is subnormal),
-// which rounds to at most 127: no clamp.
+// which rounds to at most 127: no clamp.  Bound by memory: 4096 x 7168 in 19-21 us (4.2-4.6 TB/s), 8192 x 7168 in 31 us
+// (5.7 TB/s); 64 rows in 4 us, a launch and one round trip.
 template <int CH>
 __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restrict__ x, int64_t ld, int64_t K,
                                                          uint8_t *__restrict__ q, float *__restrict__ s) {
@@ -71,6 +72,12 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restr
 // row operand, so that a lane's 4 result registers are 4 consecutive channels of one row).  Both tiles
 // travel in blocks of 128 codes from global memory straight into a ring of 5 LDS slots, each for one operand's block
 // (A0 W0 A1 W1 A2 W2 ...): while block kb is multiplied, kb + 1 and A's kb + 2 are on the way or there.
+// The large tile, 256 x 256 by 8 waves of 64 x 128, is bound by power: 4096 x 16384 x 7168 took 385 us with normal codes
+// and 272 us with zeros (an earlier 32 x 32 x 32 form).  So what counts is energy per product: 16 x 16 x 64 MFMAs reach
+// 4.0 Pop/s of normal codes where 32 x 32 x 32 reach 3.4 (nothing but MFMAs on every CU; 5.0 is the peak), and in that
+// order one operand changes from MFMA to MFMA.  Measured: 4096 x 18432 x 7168 in 400-410 us, 2.65 Pop/s (the library's
+// INT8 product of the same sizes, without scales: 585 us); 8192 tokens to 8 of 64 experts of 2048 x 7168 in 820-860 us.
+// 128 x 128 tiles, two workgroups to a CU, fill the chip at sizes where that tile does not (2048^3: 13 us).
 // ---------------------------------------------------------------------------------------------------------
 
 struct Int8Args {
@@ -153,9 +160,9 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         const int ch = (lane & 7) ^ swzf(r);
         if constexpr (GATHER) {
             const int64_t tok = r < nrow ? p.rtok[m0 + r] : -1;
-            avoff[j] = tok >= 0 && tok < p.T ? (int)(tok * K) + ch * 16 + kBack - 1024 * (j & 3) : kFar;
+            avoff[j] = tok >= 0 && tok < p.T ? (int)(tok * K + ch * 16 + kBack - 1024 * (j & 3)) : kFar;
         } else {
-            avoff[j] = r < nrow ? (int)(r * K) + ch * 16 + kBack - 1024 * (j & 3) : kFar;
+            avoff[j] = r < nrow ? (int)(r * K + ch * 16 + kBack - 1024 * (j & 3)) : kFar;
         }
     }
 #pragma unroll
@@ -182,9 +189,11 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         rs[2] = __builtin_amdgcn_readfirstlane(kb < KB ? rs[2] : 0);
         copy_one(index, rs, wvoff[decltype(index)::value], __builtin_amdgcn_readfirstlane(kb - 1) * 128, S::kCopyW, slot);
     };
-    // Operand fragments of step ks (64 codes): lane l takes row l % 16 and chunk 4 ks + l / 16.
+    // Operand fragments of step ks (64 codes): lane l takes row l % 16 and chunk 2 (l / 16) + ks of the block's 8.  (Which
+    // codes a step multiplies does not matter as long as both operands agree; chunk 4 ks + l / 16 would put lanes that the
+    // LDS serves together into the same banks, half of all its cycles.)
     auto frag = [&](const uint8_t *tile, int row0, int ks) {
-        return *reinterpret_cast<const v4i *>(tile + swz(row0 + (lane & 15), 4 * ks + (lane >> 4)));
+        return *reinterpret_cast<const v4i *>(tile + swz(row0 + (lane & 15), 2 * (lane >> 4) + ks));
     };
 
     v4i acc[TN][TM];
@@ -392,7 +401,9 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(
 // Few rows: a workgroup of 8 waves computes 16 TM rows x up to 16 NS channels, and the waves split K: wave w takes
 // blocks w, w + 8, ... of 128 codes, copies the block's rows of both operands into an LDS slot of its own, reads its
 // fragments, starts the copies of its next block and multiplies, with no barrier between the waves.  The 8 partial
-// sums meet in LDS by integer adds, whose order does not matter.
+// sums meet in LDS by integer adds, whose order does not matter.  Bound by memory: 1 x 18432 x 7168 in 22 us (5.9 TB/s,
+// partly from the Infinity Cache), 64 x 18432 x 7168 in 29 us (4.6 TB/s; every CU also reads all 64 rows).  One slice of
+// channels per CU is best there (72 of 18432; 40: 29 us where 72 took 26, 24: 31).
 // ---------------------------------------------------------------------------------------------------------
 
 constexpr int kSplitWaves = 8;
@@ -458,7 +469,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
             const int r = 8 * j + (lane >> 3);
             int64_t row = r < nrow ? r : -1;
             if constexpr (MODE == 2) row = row >= 0 ? p.rtok[m0 + row] : -1;
-            avoff[j] = row >= 0 && (MODE != 2 || row < p.T) ? (int)(row * K) + (j & 1 ? c0 ^ 1 : c0) * 16 : kFar;
+            avoff[j] = row >= 0 && (MODE != 2 || row < p.T) ? (int)(row * K + (j & 1 ? c0 ^ 1 : c0) * 16) : kFar;
         }
         auto issue = [&](int kb) {
             const bool in = kb < KB;
@@ -489,7 +500,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
             v4i fa[2][TM], fw[2][NS];
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) {
-                const int ch = 4 * ks + (lane >> 4);
+                const int ch = 2 * (lane >> 4) + ks;  // as in the tile kernel
 #pragma unroll
                 for (int i = 0; i < TM; i++)
                     fa[ks][i] = *reinterpret_cast<const v4i *>(slot + swz(16 * i + (lane & 15), ch));
@@ -663,7 +674,8 @@ hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t str
         const int64_t want = (ncu + p.E - 1) / p.E;
         int64_t cols = 8 * ((p.N / 8 + want - 1) / want);
         cols = cols < 80 ? cols : 80;
-        return launch_int8_split_cols<1, GATHER ? 2 : 1>(p, cols, out_bf16, stream);
+        if (p.E * tiles(p.N, cols) <= 0x7FFFFFFF)
+            return launch_int8_split_cols<1, GATHER ? 2 : 1>(p, cols, out_bf16, stream);
     }
     const int64_t small = (rows + 64 * p.E) / 128 * tiles(p.N, 128);
     const int64_t large = ((rows + 64 * p.E) / 256 + p.E / 4) * tiles(p.N, 256);
