@@ -67,11 +67,11 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restr
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Matrix product.  A workgroup of WM waves along the rows x WN along the channels (4 or 8) computes a tile of
+// Matrix product.  A workgroup of WM waves along the rows x WN along the channels (8) computes a tile of
 // BM = 16 TM WM rows x BN = 16 TN WN channels, a wave 16 TM x 16 TN of it with 16 x 16 x 64 MFMAs (weights as the
 // row operand, so that a lane's 4 result registers are 4 consecutive channels of one row).  Both tiles
-// travel in blocks of 128 codes from global memory straight into a ring of 5 LDS slots, each for one operand's block
-// (A0 W0 A1 W1 A2 W2 ...): while block kb is multiplied, kb + 1 and A's kb + 2 are on the way or there.
+// travel in blocks of 128 codes from global memory straight into a ring of LDS slots, each for one operand's block (A0 W0
+// A1 W1 A2 W2 ...): with 5 slots, while block kb is multiplied, kb + 1 and A's kb + 2 are on the way or there.
 // The large tile, 256 x 256 by 8 waves of 64 x 128, is bound by power: 4096 x 16384 x 7168 took 385 us with normal codes
 // and 272 us with zeros (an earlier 32 x 32 x 32 form).  So what counts is energy per product: 16 x 16 x 64 MFMAs reach
 // 4.0 Pop/s of normal codes where 32 x 32 x 32 reach 3.4 (nothing but MFMAs on every CU; 5.0 is the peak), and in that
@@ -103,12 +103,14 @@ constexpr int kBack = 4096;
 // An offset past every resource here (they end below 2^31 + kBack), also with an instruction's offset on top.
 constexpr int kFar = (int)0xFFFFF000u;
 
-template <int TM, int TN, int WM, int WN>
+// AHEAD: blocks that A's copies run ahead; the ring has 2 AHEAD + 1 slots (A's block kb + AHEAD is copied into the slot that
+// W's block kb - 1 has left, W's into that of A's block kb).
+template <int TM, int TN, int WM, int WN, int AHEAD>
 struct TileShape {
     static constexpr int kWaves = WM * WN;
-    static_assert(kWaves == 4 || kWaves == 8, "waves");
+    static_assert(kWaves == 8, "waves");
     static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
-    static constexpr int kSlots = 5, kSlot = (BM > BN ? BM : BN) * 128, kLds = kSlots * kSlot;
+    static constexpr int kSlots = 2 * AHEAD + 1, kSlot = (BM > BN ? BM : BN) * 128, kLds = kSlots * kSlot;
     static constexpr int kRowsA = BM / kWaves, kRowsW = BN / kWaves;  // rows that a wave copies per block
     static constexpr int kCopyA = kRowsA / 8, kCopyW = kRowsW / 8;
     static_assert(kCopyA % 2 == 0 && kCopyW % 2 == 0, "copies go out in halves");
@@ -129,16 +131,16 @@ __device__ __forceinline__ void static_for(const F &f) {
 
 // One tile at (m0, n0): rows [m0, mend) of c, W / SW the weights and their scales.  With GATHER row r's codes are
 // those of token rtok[r].
-template <bool OUT_BF16, int TM, int TN, int WM, int WN, bool GATHER>
+template <bool OUT_BF16, int TM, int TN, int WM, int WN, int AHEAD, bool GATHER>
 __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const uint8_t *W, const float *SW,
                                           int64_t m0, int64_t mend, int64_t n0) {
-    using S = TileShape<TM, TN, WM, WN>;
+    using S = TileShape<TM, TN, WM, WN, AHEAD>;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) & (S::kWaves - 1);
-    // With 8 waves, waves w and w + 4 share a SIMD; they take different rows, so that absent rows idle half of every SIMD
-    // and not both waves of some.
+    // Waves w and w + 4 share a SIMD; they take different rows, so that absent rows idle half of every SIMD and not both
+    // waves of some.
     static_assert(WM <= 4, "waves along the rows");
-    const int wn = (wave / WM) * 16 * TN, wm = (S::kWaves == 8 && wave >= 4 ? (wave % WM) ^ (WM - 1) : wave % WM) * 16 * TM;
+    const int wn = (wave / WM) * 16 * TN, wm = (wave >= 4 ? (wave % WM) ^ (WM - 1) : wave % WM) * 16 * TM;
     const int64_t K = p.K;
     const int KB = __builtin_amdgcn_readfirstlane((int)((K + 127) >> 7));
     const int64_t nrow = mend - m0 < S::BM ? mend - m0 : S::BM;
@@ -210,14 +212,19 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) {
         copy_one(j, rw, (j.value & 1 ? ok1 : ok0) ? wvoff[j.value] : kFar, (KB - 1) * 128, S::kCopyW, 1);
     });
-    static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, 1, 2); });
-    static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, 1, 3); });
-    copies_barrier<S::kCopyA + S::kCopyW>();  // block 0 is there
+    static_for<AHEAD - 1>([&](auto block) __attribute__((always_inline)) {
+        constexpr int kb = decltype(block)::value + 1;
+        static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, kb, 2 * kb); });
+        static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, kb, 2 * kb + 1); });
+    });
+    copies_barrier<(AHEAD - 1) * (S::kCopyA + S::kCopyW)>();  // block 0 is there
+
     // A block is 2 TN phases: phase g multiplies channel subtile g % TN by all row subtiles, for the 64 codes of step
     // g / TN.  Channel fragments are read kAhead phases before their use, row fragments a step before.  The last of
     // the block's fragments is read kAhead phases before the end; the barrier after that phase frees the block's slots,
     // and the next block's first fragments and the copies into A's slot follow it.
     constexpr int kAhead = 3, kPhases = 2 * TN, kBarrier = kPhases - kAhead;
+    constexpr int kLater = (AHEAD - 1) * S::kCopyA + (AHEAD - 2) * S::kCopyW;  // copies of the blocks past kb + 1
     static_assert(kPhases % (kAhead + 1) == 0 && kBarrier > TN && TM % 2 == 0, "phases");
     v4i fa[2][TM], fw[kAhead + 1];
 #pragma unroll
@@ -228,7 +235,7 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     auto block = [&](auto index, int kb) __attribute__((always_inline)) {
         constexpr int slot = decltype(index)::value;
         constexpr int s1 = (slot + 1) % S::kSlots, s2 = (slot + 2) % S::kSlots, s3 = (slot + 3) % S::kSlots,
-                      s4 = (slot + 4) % S::kSlots;
+                      last = (slot + S::kSlots - 1) % S::kSlots;  // W's block kb - 1 has left it
         const uint8_t *tA = lds + slot * S::kSlot, *tW = lds + s1 * S::kSlot;
         const uint8_t *nA = lds + s2 * S::kSlot, *nW = lds + s3 * S::kSlot;
         static_for<kPhases>([&](auto phase) __attribute__((always_inline)) {
@@ -241,17 +248,17 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
             constexpr int w0 = after < 0 ? 0 : after * S::kCopyW / kAhead;
             constexpr int w1 = after < 0 ? 0 : (after + 1) * S::kCopyW / kAhead;
             if constexpr (after == 0) {
-                copies_barrier<S::kCopyA>();  // block kb + 1 is there; A's kb + 2 may still be on the way
+                copies_barrier<kLater>();  // block kb + 1 is there; the later ones may still be on the way
                 __builtin_amdgcn_sched_barrier(0);
             }
             fw[gw % (kAhead + 1)] = frag(after < 0 ? tW : nW, wn + 16 * (gw % TN), gw / TN);
 #pragma unroll
             for (int i = r0; i < r1; i++) fa[ks ^ 1][i] = frag(ks == 0 ? tA : nA, wm + 16 * i, ks ^ 1);
             static_for<a1 - a0>([&](auto j) __attribute__((always_inline)) {
-                copy_a(Index<a0 + decltype(j)::value>{}, kb + 2, s4);
+                copy_a(Index<a0 + decltype(j)::value>{}, kb + AHEAD, last);
             });
             static_for<w1 - w0>([&](auto j) __attribute__((always_inline)) {
-                copy_w(Index<w0 + decltype(j)::value>{}, kb + 2, slot);  // the slot that A's block kb leaves
+                copy_w(Index<w0 + decltype(j)::value>{}, kb + AHEAD, slot);  // A's block kb has left it
             });
             // (every other phase takes the rows backwards, so that one operand changes from MFMA to MFMA, not two)
 #pragma unroll
@@ -283,10 +290,10 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     }
     if (__builtin_amdgcn_readfirstlane((int)(rows_here != 0)) == 0) {
         for (int kb = 0, slot = 0; kb < KB; kb++) {
-            const int s4 = slot + 4 < S::kSlots ? slot + 4 : slot + 4 - S::kSlots;
-            static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, kb + 2, s4); });
-            copies_barrier<S::kCopyA>();
-            static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, kb + 2, slot); });
+            const int last = slot > 0 ? slot - 1 : S::kSlots - 1;
+            static_for<S::kCopyA>([&](auto j) __attribute__((always_inline)) { copy_a(j, kb + AHEAD, last); });
+            copies_barrier<kLater>();
+            static_for<S::kCopyW>([&](auto j) __attribute__((always_inline)) { copy_w(j, kb + AHEAD, slot); });
             slot = slot + 2 < S::kSlots ? slot + 2 : slot + 2 - S::kSlots;
         }
         copies_barrier<0>();
@@ -298,18 +305,24 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
         }
         return;
     }
-    // Five blocks at a time, so that the slots are constants: block kb's A is in slot 2 kb % 5.
-    for (int kb = 0;; kb += 5) {
-        block(Index<0>{}, kb);
-        if (kb + 1 >= KB) break;
-        block(Index<2>{}, kb + 1);
-        if (kb + 2 >= KB) break;
-        block(Index<4>{}, kb + 2);
-        if (kb + 3 >= KB) break;
-        block(Index<1>{}, kb + 3);
-        if (kb + 4 >= KB) break;
-        block(Index<3>{}, kb + 4);
-        if (kb + 5 >= KB) break;
+    // As many blocks at a time as there are slots, so that the slots are constants: block kb's A is in slot 2 kb % kSlots.
+    static_assert(S::kSlots <= 9, "steps below");
+    for (int kb = 0;; kb += S::kSlots) {
+#define FP8Q_INT8_STEP(I)                                  \
+    if constexpr (I < S::kSlots) {                         \
+        block(Index<2 * (I) % S::kSlots>{}, kb + (I));     \
+        if (kb + (I) + 1 >= KB) break;                     \
+    }
+        FP8Q_INT8_STEP(0)
+        FP8Q_INT8_STEP(1)
+        FP8Q_INT8_STEP(2)
+        FP8Q_INT8_STEP(3)
+        FP8Q_INT8_STEP(4)
+        FP8Q_INT8_STEP(5)
+        FP8Q_INT8_STEP(6)
+        FP8Q_INT8_STEP(7)
+        FP8Q_INT8_STEP(8)
+#undef FP8Q_INT8_STEP
     }
 
     // A lane holds channels 4 (lane / 16) .. + 3 of row lane % 16 of each subtile.  Results pass through LDS so that
@@ -367,9 +380,9 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
 
 // One tile per workgroup.  GROUPED: tiles of an expert-sorted layout.  TAIL (dense): the tiles of columns [0, n_tail), then
 // tiles of half the width over the other columns, which fill what would be a last round of few whole tiles.
-template <bool OUT_BF16, bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(Int8Args p) {
-    using S = TileShape<TM, TN, WM, WN>;
+template <bool OUT_BF16, bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN, int AHEAD>
+__global__ __launch_bounds__(64 * WM * WN, TM * TN <= 8 && AHEAD == 2 ? 4 : 2) void gemm_int8_kernel(Int8Args p) {
+    using S = TileShape<TM, TN, WM, WN, AHEAD>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
     int64_t m0, mend = p.M, n0, e = 0;
     if constexpr (GROUPED) {
@@ -386,7 +399,7 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(
         if (!dense_tile_at(i, p.n_mtiles, p.n_ntiles, mt, nt)) {
             if constexpr (TAIL) {
                 if (dense_tile_at(i - p.n_mtiles * p.n_ntiles, p.n_mtiles, p.n_ntiles_tail, mt, nt))
-                    int8_tile<OUT_BF16, TM, TN / 2, WM, WN, false>(lds, p, p.qw, p.sw, mt * S::BM, p.M,
+                    int8_tile<OUT_BF16, TM, TN / 2, WM, WN, AHEAD, false>(lds, p, p.qw, p.sw, mt * S::BM, p.M,
                                                                    p.n_tail + nt * (S::BN / 2));
             }
             return;
@@ -394,7 +407,7 @@ __global__ __launch_bounds__(64 * WM * WN, 8 / (WM * WN)) void gemm_int8_kernel(
         m0 = mt * S::BM;
         n0 = nt * S::BN;
     }
-    int8_tile<OUT_BF16, TM, TN, WM, WN, GATHER>(lds, p, p.qw + e * p.N * p.K, p.sw + e * p.N, m0, mend, n0);
+    int8_tile<OUT_BF16, TM, TN, WM, WN, AHEAD, GATHER>(lds, p, p.qw + e * p.N * p.K, p.sw + e * p.N, m0, mend, n0);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -576,25 +589,25 @@ hipError_t launch_int8_split_cols(const Int8Args &p, int64_t cols, bool out_bf16
 
 constexpr int kTile = 128;  // the smallest tile's rows and channels
 
-template <bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN>
+template <bool GROUPED, bool GATHER, bool TAIL, int TM, int TN, int WM, int WN, int AHEAD = 2>
 hipError_t launch_int8_tile(Int8Args p, int64_t n_tail, bool out_bf16, hipStream_t stream) {
-    using S = TileShape<TM, TN, WM, WN>;
+    using S = TileShape<TM, TN, WM, WN, AHEAD>;
     p.n_mtiles = GROUPED ? p.M / S::BM + p.E : (p.M + S::BM - 1) / S::BM;
     p.n_ntiles = (n_tail + S::BN - 1) / S::BN;
     p.n_tail = n_tail;
     p.n_ntiles_tail = (p.N - n_tail + S::BN / 2 - 1) / (S::BN / 2);
     const dim3 grid((unsigned)((p.n_mtiles * (p.n_ntiles + p.n_ntiles_tail) + 255) / 256 * 256));
     if (out_bf16)
-        gemm_int8_kernel<true, GROUPED, GATHER, TAIL, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+        gemm_int8_kernel<true, GROUPED, GATHER, TAIL, TM, TN, WM, WN, AHEAD><<<grid, S::kWaves * 64, 0, stream>>>(p);
     else
-        gemm_int8_kernel<false, GROUPED, GATHER, TAIL, TM, TN, WM, WN><<<grid, S::kWaves * 64, 0, stream>>>(p);
+        gemm_int8_kernel<false, GROUPED, GATHER, TAIL, TM, TN, WM, WN, AHEAD><<<grid, S::kWaves * 64, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 // The dense product's kernel and its shape, by estimated time in us.  The estimates were fitted to measurements on
 // shapes from 64 x 1024 x 16384 to 4096 x 16384 x 7168; they matter by their ratios, at the crossings.
 struct Int8Plan {
-    enum Kind { kSplitK, kSmall, kTall, kWide, kLarge } kind;
+    enum Kind { kSplitK, kSmall, kDeep, kTall, kWide, kLarge } kind;
     int tm;          // kSplitK: 16-row subtiles of a workgroup
     int64_t cols;    // kSplitK: channels of a workgroup
     int64_t n_tail;  // kLarge: columns covered by whole tiles
@@ -605,11 +618,15 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
     const double KB = (double)((K + 127) / 128);
     auto tiles = [](int64_t n, int64_t t) { return (double)((n + t - 1) / t); };
     auto rounds = [](double n, double d) { return (double)(int64_t)((n + d - 1) / d); };
-    // 128 x 128 tiles, two to a CU: 0.42 us a block for a few tiles, 0.60 with one on every CU, 0.92 with two, 1.05 over
-    // many rounds.
+    // 128 x 128 tiles by 8 waves of 32 x 64, two to a CU: 0.60 us a block with one on every CU, 0.92 with two, 1.05 over
+    // many rounds.  (4 waves of 64 x 64 read a third less from the LDS and were 0 to 13% slower, with one wave a SIMD.)
+    // Where every tile has a CU to itself and K is long, the copies run 4 blocks ahead instead of 2 (the LDS then holds
+    // one tile): 512 x 4096 x 7168 33 -> 30 us, 1024 x 4096 x 7168 35 -> 31; no gain at K = 2048 and less.
     const double ts = tiles(M, 128) * tiles(N, 128);
-    Int8Plan best{Int8Plan::kSmall, 0, 0, N};
-    double cost = 5.0 + (ts <= ncu       ? KB * (0.42 + 0.18 * ts / ncu)
+    const bool deep = ts <= ncu && KB >= 32;
+    Int8Plan best{deep ? Int8Plan::kDeep : Int8Plan::kSmall, 0, 0, N};
+    double cost = 5.0 + (deep            ? KB * (0.42 + 0.07 * ts / ncu)
+                         : ts <= ncu     ? KB * (0.42 + 0.18 * ts / ncu)
                          : ts <= 2 * ncu ? KB * (0.28 + 0.32 * ts / ncu) + 3.0
                                          : rounds(ts, 2 * ncu) * (KB * 1.05 + 3.0));
     // 256 x 128 or 128 x 256 tiles, one to a CU: 0.88 us a block.
@@ -683,7 +700,7 @@ hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t str
     const double t_large = (double)tiles(large, ncu) * (KB * 1.48 + 6.0);
     const double t_read = (double)p.E * p.N * p.K / 5.0e6;  // the weights from memory, at 5 TB/s
     if (rows <= 32 * p.E || (t_small < t_large && t_large > t_read))
-        return launch_int8_tile<true, GATHER, false, 4, 4, 2, 2>(p, p.N, out_bf16, stream);
+        return launch_int8_tile<true, GATHER, false, 2, 4, 4, 2>(p, p.N, out_bf16, stream);
     return launch_int8_tile<true, GATHER, false, 4, 8, 4, 2>(p, p.N, out_bf16, stream);
 }
 
@@ -716,7 +733,8 @@ hipError_t launch_gemm_int8(const uint8_t *qa, const float *sa, const uint8_t *q
             if (plan.tm == 1) return launch_int8_split_cols<1, 0>(p, plan.cols, out_bf16, stream);
             if (plan.tm == 2) return launch_int8_split_cols<2, 0>(p, plan.cols, out_bf16, stream);
             return launch_int8_split_cols<4, 0>(p, plan.cols, out_bf16, stream);
-        case Int8Plan::kSmall: return launch_int8_tile<false, false, false, 4, 4, 2, 2>(p, N, out_bf16, stream);
+        case Int8Plan::kSmall: return launch_int8_tile<false, false, false, 2, 4, 4, 2>(p, N, out_bf16, stream);
+        case Int8Plan::kDeep: return launch_int8_tile<false, false, false, 2, 4, 4, 2, 4>(p, N, out_bf16, stream);
         case Int8Plan::kTall: return launch_int8_tile<false, false, false, 4, 4, 4, 2>(p, N, out_bf16, stream);
         case Int8Plan::kWide: return launch_int8_tile<false, false, false, 4, 4, 2, 4>(p, N, out_bf16, stream);
         default: break;

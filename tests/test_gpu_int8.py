@@ -77,7 +77,8 @@ def check_out(c, want, what):
 DENSE = [(1, 8, 16), (1, 18432, 256), (2, 24, 48), (7, 136, 112), (15, 520, 128), (16, 2048, 144), (17, 1000, 1040),
          (33, 72, 7168), (63, 264, 256), (64, 128, 400), (65, 256, 272), (100, 4104, 528), (128, 640, 1024),
          (129, 136, 2064), (200, 384, 640), (255, 248, 384), (256, 512, 128), (257, 256, 176), (300, 776, 896),
-         (513, 1032, 1168), (1037, 4104, 400), (2049, 264, 272), (3, 8, 131056)]
+         (513, 1032, 1168), (1037, 4104, 400), (2049, 264, 272), (3, 8, 131056),
+         (520, 4104, 4112), (500, 16376, 912), (801, 8216, 400), (1800, 4104, 400), (600, 16392, 144), (1290, 13000, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -174,7 +175,8 @@ def grouped_problem(T, E, k, N, K, seed, empty=()):
 
 
 GROUPED = [(1, 4, 2, 24, 48), (5, 8, 3, 136, 144), (20, 6, 2, 264, 400), (90, 5, 4, 128, 256), (64, 40, 8, 72, 272),
-           (200, 2, 1, 520, 176), (700, 3, 2, 256, 1040), (33, 300, 2, 8, 16), (513, 2, 2, 1032, 128), (16, 4, 4, 2048, 528)]
+           (200, 2, 1, 520, 176), (700, 3, 2, 256, 1040), (33, 300, 2, 8, 16), (513, 2, 2, 1032, 128), (16, 4, 4, 2048, 528),
+           (3000, 5, 2, 2056, 272)]
 
 
 @pytest.mark.parametrize("T,E,k,N,K", GROUPED)
