@@ -620,7 +620,8 @@ class _Rec:
         self.he.record(self.ev, torch.cuda.current_stream().cuda_stream)
 
 
-GEMM_SOURCES = ("fine_grained_quantization_amd/csrc/fp8q_gemm.hip", "fine_grained_quantization_amd/csrc/fp8q_device.h")
+GEMM_SOURCES = ("fine_grained_quantization_amd/csrc/fp8q_gemm.hip", "fine_grained_quantization_amd/csrc/fp8q_device.h",
+                "fine_grained_quantization_amd/csrc/fp8q_tiles.h")
 QUANT_SOURCES = ("fine_grained_quantization_amd/csrc/fp8q_quant.hip", "fine_grained_quantization_amd/csrc/fp8q_device.h")
 # The sources each reported kernel is built from (its recorded traffic is stale once they change).
 KERNEL_SOURCES = {"gemm_blockscaled": GEMM_SOURCES, "grouped_gemm_blockscaled": GEMM_SOURCES,
