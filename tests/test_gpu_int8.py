@@ -237,6 +237,26 @@ def test_gather_tokens_out_of_range_are_empty_rows():
     assert (host(c) == 0).all()
 
 
+@pytest.mark.parametrize("used", [3, 300])
+def test_gather_from_the_largest_token_array(used):
+    """T * K = 2^31 - 2048, the last tokens among the rows, by the kernel of few rows and by the tiles."""
+    T, K, N, E = 131200, 16368, 24, 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(45)
+    q = torch.randint(-127, 128, (T, K), device="cuda", dtype=torch.int8, generator=g)
+    s, sw = torch.rand(T, device="cuda", generator=g), torch.rand((E, N), device="cuda", generator=g)
+    qw = torch.randint(-127, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=g)
+    rows = (used + 127) // 128 * 128
+    row_token = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    row_token[:used] = T - 1 - torch.arange(used, device="cuda") * 400
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    say(f"int8 gather at T * K = {T * K}, {used} rows")
+    c = fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, off, out_dtype=torch.float32)
+    at = row_token[:used].long()
+    want = ref.gemm_int8(host(q[at]), host(s[at]), host(qw[0]), host(sw[0]))
+    assert np.array_equal(host(c[:used]), want) and (host(c[used:]) == 0).all()
+
+
 def test_int8_wants_its_arguments_right():
     a = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
     w = torch.zeros((16, 32), dtype=torch.int8, device="cuda")
