@@ -44,6 +44,10 @@ bool aligned_elem(const void *p, int dtype) {
 
 constexpr int64_t kMaxGrid = 0x7FFFFFFF;  // 1-D grids: workgroup count must fit in 31 bits
 constexpr int64_t kMaxK = int64_t(1) << 23;  // GEMM tiles address 256 rows of K bytes with 32-bit offsets
+// A launch has fewer than 2^32 threads: workgroups of 256 and of 512.
+constexpr int64_t kMaxGrid256 = 0xFFFFFFFFll / 256, kMaxGrid512 = 0xFFFFFFFFll / 512;
+constexpr int64_t kMaxGateTokens = 0xFFFFFFFFll / 64;  // 64 lanes a token at most
+
 constexpr int64_t kMaxInt8K = 131056;        // INT8 sums of products of codes down to -128 stay below 2^31
 
 int finish(hipError_t e) { return e == hipSuccess ? FP8Q_OK : FP8Q_ERR_HIP; }
@@ -319,7 +323,7 @@ int fp8q_moe_gate_topk(const void *logits, int dtype, int64_t ld, int64_t T, int
                        int32_t *row_token, int64_t rows, int32_t *load, void *workspace, int64_t workspace_bytes,
                        void *stream) {
     const int64_t cap = fp8q_moe_route_capacity(T, E, k);
-    if (cap < 0 || rows < cap || rows > 0x7FFFFFFF || T > 0x7FFFFFFF || ld < E) return FP8Q_ERR_SHAPE;
+    if (cap < 0 || rows < cap || rows > 0x7FFFFFFF || T > kMaxGateTokens || ld < E) return FP8Q_ERR_SHAPE;
     if (n_group < 1 || n_group > fp8q::kMoeMaxGroups || E % n_group || topk_group < 1 || topk_group > n_group ||
         k > topk_group * (E / n_group))
         return FP8Q_ERR_SHAPE;
@@ -346,7 +350,7 @@ int fp8q_moe_gate_topk(const void *logits, int dtype, int64_t ld, int64_t T, int
 int fp8q_moe_gate_backward(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, int score,
                            int renormalize, float scale, const int32_t *topk_idx, const float *grad_weight,
                            void *grad_logits, void *stream) {
-    if (T < 0 || T > 0x7FFFFFFF || E < 1 || E > fp8q::kMoeMaxExperts || k < 1 || k > E || k > fp8q::kMoeMaxK || ld < E)
+    if (T < 0 || T > kMaxGateTokens || E < 1 || E > fp8q::kMoeMaxExperts || k < 1 || k > E || k > fp8q::kMoeMaxK || ld < E)
         return FP8Q_ERR_SHAPE;
     if (dtype != FP8Q_OUT_BF16 && dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;
     if ((score != FP8Q_SCORE_SIGMOID && score != FP8Q_SCORE_SOFTMAX) || (renormalize != 0 && renormalize != 1))
@@ -374,7 +378,7 @@ int fp8q_moe_combine(const void *c, int dtype, int64_t rows, int64_t H, const in
     if ((rows > 0 && !c) || !row_of || !weight || !y) return FP8Q_ERR_NULL;
     if (!aligned16(c) || !aligned4(row_of) || !aligned4(weight) || !aligned16(add) || !aligned16(y))
         return FP8Q_ERR_ALIGN;
-    if (fp8q::moe_combine_blocks(T, H, dtype == FP8Q_OUT_BF16) > kMaxGrid) return FP8Q_ERR_SHAPE;
+    if (fp8q::moe_combine_blocks(T, H, dtype == FP8Q_OUT_BF16) > kMaxGrid256) return FP8Q_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_moe_combine(c, dtype == FP8Q_OUT_BF16, rows, H, row_of, weight, T, (int)k, add, y,
@@ -395,7 +399,7 @@ int fp8q_moe_combine_backward(const void *grad_y, const void *c, int dtype, int6
     if (!aligned16(grad_y) || !aligned16(c) || !aligned16(grad_c) || !aligned4(row_of) || !aligned4(weight) ||
         !aligned4(grad_weight) || !aligned4(row_token) || !aligned4(offsets))
         return FP8Q_ERR_ALIGN;
-    if (T + rows / 16 + 1 > kMaxGrid) return FP8Q_ERR_SHAPE;  // a workgroup per token and per 16 rows
+    if (T + rows / 16 + 1 > kMaxGrid256) return FP8Q_ERR_SHAPE;  // a workgroup per token and per 16 rows
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_moe_combine_backward(grad_y, c, dtype == FP8Q_OUT_BF16, rows, H, row_of, weight, T,
@@ -408,7 +412,7 @@ int fp8q_quant_int8(const uint16_t *x, int64_t ld, int64_t M, int64_t K, int8_t 
     if (M == 0) return FP8Q_OK;
     if (!s || (K > 0 && (!x || !q))) return FP8Q_ERR_NULL;  // K == 0: only the (zero) scales are written
     if (!aligned4(s) || (K > 0 && (!aligned16(x) || !aligned16(q)))) return FP8Q_ERR_ALIGN;
-    if (M > kMaxGrid) return FP8Q_ERR_SHAPE;  // one workgroup per row
+    if (M > kMaxGrid256) return FP8Q_ERR_SHAPE;  // one workgroup per row
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_quant_int8(x, ld, M, K, reinterpret_cast<uint8_t *>(q), s,
@@ -423,7 +427,7 @@ int fp8q_gemm_int8(const int8_t *qa, const float *sa, const int8_t *qw, const fl
     if (!qa || !sa || !qw || !sw || !c) return FP8Q_ERR_NULL;
     if (!aligned16(qa) || !aligned4(sa) || !aligned16(qw) || !aligned4(sw) || !aligned16(c)) return FP8Q_ERR_ALIGN;
     const int64_t blocks = fp8q::gemm_int8_blocks(M, N, 0);
-    if (blocks < 0 || blocks > kMaxGrid) return FP8Q_ERR_SHAPE;
+    if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_gemm_int8(reinterpret_cast<const uint8_t *>(qa), sa,
@@ -443,7 +447,7 @@ int fp8q_grouped_gemm_int8(const int8_t *qa, const float *sa, const int8_t *qw, 
     if (!aligned16(qa) || !aligned4(sa) || !aligned16(qw) || !aligned4(sw) || !aligned16(c) || !aligned4(off))
         return FP8Q_ERR_ALIGN;
     const int64_t blocks = fp8q::gemm_int8_blocks(M_total, N, E);
-    if (blocks < 0 || blocks > kMaxGrid) return FP8Q_ERR_SHAPE;
+    if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_grouped_gemm_int8(reinterpret_cast<const uint8_t *>(qa), sa, M_total, nullptr,
@@ -466,7 +470,7 @@ int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, co
         (T > 0 && (!aligned16(q) || !aligned4(s))))
         return FP8Q_ERR_ALIGN;
     const int64_t blocks = fp8q::gemm_int8_blocks(M_total, N, E);
-    if (blocks < 0 || blocks > kMaxGrid) return FP8Q_ERR_SHAPE;
+    if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_grouped_gemm_int8(reinterpret_cast<const uint8_t *>(q), s, T, row_token,

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const void *__restrict
         for (int u = 0; u < kSlots; u++) {
             const int64_t r = j0 + u < k ? row_of[t * k + j0 + u] : -1;  // the same in every lane
             const bool in = r >= 0 && r < rows;
-            w[u] = in ? weight[t * k + j0 + u] : 0.0f;
+            w[u] = in ? weight[t * k + j0 + u] : -0.0f;  // (-0 * 0 leaves every sum as it is, -0 too)
             v[u] = in ? load_stream16(src + r * chunks) : zero;
         }
 #pragma unroll

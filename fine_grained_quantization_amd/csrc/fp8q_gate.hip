@@ -718,6 +718,8 @@ hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *to
 #undef FP8Q_GATE_CASE
         default: return hipErrorInvalidValue;
     }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;  // the layout reads what this launch counts
     if (!one) {
         const int64_t per = (C + 255) / 256;  // at most 256 workgroups: each reads all counts
         moe_gate_layout_kernel<<<dim3((unsigned)((C + per - 1) / per)), kGateThreads, 0, stream>>>(o, g.T, C, g.E, g.k,

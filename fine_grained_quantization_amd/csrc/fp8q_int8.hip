@@ -691,7 +691,7 @@ hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t str
         const int64_t want = (ncu + p.E - 1) / p.E;
         int64_t cols = 8 * ((p.N / 8 + want - 1) / want);
         cols = cols < 80 ? cols : 80;
-        if (p.E * tiles(p.N, cols) <= 0x7FFFFFFF)
+        if (p.E * tiles(p.N, cols) <= 0xFFFFFFFFll / (64 * kSplitWaves))
             return launch_int8_split_cols<1, GATHER ? 2 : 1>(p, cols, out_bf16, stream);
     }
     const int64_t small = (rows + 64 * p.E) / 128 * tiles(p.N, 128);

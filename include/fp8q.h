@@ -366,7 +366,7 @@ int64_t fp8q_moe_gate_workspace_bytes(int64_t T, int64_t E);
  *   workspace   : device memory of workspace_bytes bytes, 4-byte aligned, its
  *                 contents on entry do not matter (calls that share one must not
  *                 overlap); NULL will do when 0 bytes are needed
- * Requires the sizes of fp8q_moe_route_topk, T <= 2^31 - 1, ld >= E, 1 <=
+ * Requires the sizes of fp8q_moe_route_topk, T < 2^26, ld >= E, 1 <=
  * topk_group <= n_group <= 64, E % n_group == 0, k <= topk_group * E / n_group,
  * rows >= fp8q_moe_route_capacity(T, E, k); pointers aligned to their elements.
  * One launch up to 32 tokens, two above; deterministic. */
@@ -395,7 +395,8 @@ int fp8q_moe_gate_backward(const void *logits, int dtype, int64_t ld, int64_t T,
  *   weight : fp32 [T][k];  add : [T][H] in dtype (shared expert, residual) or NULL
  *   y   : [T][H] in dtype (output)
  * fp32 sums, slots in order, rounded once.  Requires H % 8 == 0, 1 <= k <= 16,
- * T, rows, H <= 2^31 - 1, 16-byte aligned c, add and y. */
+ * T, rows, H <= 2^31 - 1, fewer than 2^24 workgroups (one for each token and 4096
+ * bytes of its row), 16-byte aligned c, add and y. */
 int fp8q_moe_combine(const void *c, int dtype, int64_t rows, int64_t H, const int32_t *row_of, const float *weight,
                      int64_t T, int64_t k, const void *add, void *y, void *stream);
 
@@ -405,8 +406,9 @@ int fp8q_moe_combine(const void *c, int dtype, int64_t rows, int64_t H, const in
  *   grad_c : [rows][H] in dtype (output): rows below offsets[E] that carry no
  *            token become zeros, rows from offsets[E] on are not written
  *   grad_weight : fp32 [T][k] (output; 0 for an empty slot)
- * Requires what fp8q_moe_combine requires, and rows of different slots to be
- * different.  fp32 sums in a fixed order. */
+ * Requires what fp8q_moe_combine requires (its workgroups: one for each token and
+ * for 16 rows), and rows of different slots to be different.  fp32 sums in a fixed
+ * order. */
 int fp8q_moe_combine_backward(const void *grad_y, const void *c, int dtype, int64_t rows, int64_t H,
                               const int32_t *row_of, const float *weight, int64_t T, int64_t k,
                               const int32_t *row_token, const int32_t *offsets, int64_t E, void *grad_c,
@@ -422,8 +424,8 @@ int fp8q_moe_combine_backward(const void *grad_y, const void *c, int dtype, int6
  *   s : fp32 [M] (output) = fl32(max_k |x| / 127)
  *   q : int8 [M][K] contiguous (output) = fl32(x / s) rounded to nearest even, in
  *       [-127, 127]; 0 where s is 0
- * Requires K % 16 == 0, ld >= K, ld % 8 == 0, 16-byte aligned x and q, 4-byte
- * aligned s; with K == 0, x and q may be null and s is set to 0. */
+ * Requires K % 16 == 0, ld >= K, ld % 8 == 0, M < 2^24, 16-byte aligned x and q,
+ * 4-byte aligned s; with K == 0, x and q may be null and s is set to 0. */
 int fp8q_quant_int8(const uint16_t *x, int64_t ld, int64_t M, int64_t K, int8_t *q, float *s, void *stream);
 
 /* C[m,n] = fl32(sum_k qa[m,k] * qw[n,k]) * (sa[m] * sw[n]), the sum exact in 32-bit integers:

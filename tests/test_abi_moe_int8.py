@@ -28,7 +28,8 @@ GATE = dict(logits=A, dtype=1, ld=64, T=40, E=64, k=4, score=0, bias=None, n_gro
     (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025, ld=1025), SHAPE), (dict(k=0), SHAPE), (dict(k=17), SHAPE),
     (dict(ld=63), SHAPE), (dict(rows=100), SHAPE), (dict(rows=1 << 31), SHAPE), (dict(n_group=0), SHAPE),
     (dict(n_group=7), SHAPE), (dict(n_group=65), SHAPE), (dict(topk_group=0), SHAPE), (dict(topk_group=9), SHAPE),
-    (dict(k=16, topk_group=1), SHAPE), (dict(T=1 << 31, rows=(1 << 31) - 1), SHAPE), (dict(dtype=2), DTYPE),
+    (dict(k=16, topk_group=1), SHAPE), (dict(T=1 << 31, rows=(1 << 31) - 1), SHAPE),
+    (dict(T=1 << 26, rows=(1 << 31) - 1), SHAPE), (dict(dtype=2), DTYPE),
     (dict(score=2), OPTION), (dict(group_top=0), OPTION), (dict(group_top=3), OPTION), (dict(renorm=2), OPTION),
     (dict(off=None), NULL), (dict(row_token=None), NULL), (dict(logits=None), NULL), (dict(idx=None), NULL),
     (dict(weight=None), NULL), (dict(row_of=None), NULL), (dict(ws=None), NULL), (dict(logits=MIS), ALIGN),
@@ -51,6 +52,7 @@ BACK = dict(logits=A, dtype=1, ld=64, T=4, E=64, k=4, score=0, renorm=1, scale=1
 
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(k=65), SHAPE), (dict(k=17), SHAPE), (dict(ld=63), SHAPE),
+    (dict(T=1 << 26), SHAPE),
     (dict(dtype=-1), DTYPE), (dict(score=-1), OPTION), (dict(renorm=-1), OPTION), (dict(T=0, logits=None), OK),
     (dict(logits=None), NULL), (dict(idx=None), NULL), (dict(gw=None), NULL), (dict(out=None), NULL),
     (dict(out=MIS), ALIGN), (dict(gw=MIS), ALIGN),
@@ -66,7 +68,8 @@ CBACK = dict(gy=A, c=A, dtype=0, rows=128, H=16, row_of=A, w=A, T=3, k=2, row_to
 
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), SHAPE), (dict(H=12), SHAPE), (dict(H=-8), SHAPE), (dict(rows=-1), SHAPE), (dict(k=0), SHAPE),
-    (dict(k=17), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=(1 << 31) - 1, H=4096), SHAPE), (dict(dtype=3), DTYPE),
+    (dict(k=17), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=(1 << 31) - 1, H=4096), SHAPE), (dict(T=1 << 24), SHAPE),
+    (dict(dtype=3), DTYPE),
     (dict(T=0, c=None), OK), (dict(H=0, c=None), OK), (dict(c=None), NULL), (dict(row_of=None), NULL),
     (dict(w=None), NULL), (dict(y=None), NULL), (dict(c=ctypes.c_void_p(4104)), ALIGN), (dict(add=MIS), ALIGN),
     (dict(y=MIS), ALIGN), (dict(w=MIS), ALIGN),
@@ -77,7 +80,7 @@ def test_combine(lib, change, want):
 
 @pytest.mark.parametrize("change,want", [
     (dict(T=-1), SHAPE), (dict(H=12), SHAPE), (dict(E=0), SHAPE), (dict(k=17), SHAPE), (dict(dtype=3), DTYPE),
-    (dict(T=0, rows=0), OK), (dict(gy=None), NULL), (dict(c=None), NULL), (dict(gw=None), NULL), (dict(gc=None), NULL),
+    (dict(T=1 << 24), SHAPE), (dict(T=0, rows=0), OK), (dict(gy=None), NULL), (dict(c=None), NULL), (dict(gw=None), NULL), (dict(gc=None), NULL),
     (dict(row_token=None), NULL), (dict(off=None), NULL), (dict(gc=MIS), ALIGN), (dict(off=MIS), ALIGN),
 ])
 def test_combine_backward(lib, change, want):
@@ -90,7 +93,7 @@ def test_int8(lib):
     assert q(A, 36, 4, 32, B, B, None) == SHAPE and q(A, 32, -1, 32, B, B, None) == SHAPE
     assert q(None, 32, 0, 32, None, None, None) == OK and q(None, 32, 4, 32, B, B, None) == NULL
     assert q(A, 0, 4, 0, None, None, None) == NULL and q(MIS, 32, 4, 32, B, B, None) == ALIGN
-    assert q(A, 32, 4, 32, B, MIS, None) == ALIGN
+    assert q(A, 32, 4, 32, B, MIS, None) == ALIGN and q(A, 32, 1 << 24, 32, B, B, None) == SHAPE
     g = lib.fp8q_gemm_int8
     assert g(A, A, A, A, B, 0, 4, 12, 32, None) == SHAPE and g(A, A, A, A, B, 0, 4, 8, 24, None) == SHAPE
     assert g(A, A, A, A, B, 0, 4, 8, 0, None) == SHAPE and g(A, A, A, A, B, 0, 4, 8, 131072, None) == SHAPE

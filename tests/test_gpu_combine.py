@@ -72,6 +72,20 @@ def test_combine_ignores_rows_out_of_range_and_keeps_nan_apart():
     assert (y[0] == 0.5).all() and (y[1] == 0.5).all() and torch.isnan(y[2]).all() and (y[3] == 0).all()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_tokens_without_rows_keep_what_is_added(dt):
+    """Bit for bit, signed zeros, infinities and NaN too."""
+    add = torch.tensor([0.0, -0.0, 1.5, -2.0, float("inf"), float("-inf"), float("nan"), 1e-38], dtype=DT[dt]).repeat(3, 2)
+    row_of = torch.full((3, 5), -1, dtype=torch.int32, device="cuda")
+    y = fq.fp8q_moe_combine(torch.ones((2, 16), dtype=DT[dt], device="cuda"), row_of, torch.ones((3, 5), device="cuda"),
+                            add=add.cuda()).cpu()
+    bits = torch.int16 if dt == "bf16" else torch.int32
+    assert torch.equal(torch.isnan(y), torch.isnan(add))
+    assert torch.equal(y.view(bits)[~torch.isnan(y)], add.view(bits)[~torch.isnan(add)])
+    y = fq.fp8q_moe_combine(torch.ones((2, 16), dtype=DT[dt], device="cuda"), row_of, torch.ones((3, 5), device="cuda"))
+    assert (y.cpu().view(bits) == 0).all()
+
+
 @pytest.mark.parametrize("T,E,k,H,dt", SHAPES)
 @pytest.mark.parametrize("empty", [0.0, 0.3])
 def test_combine_gradient(T, E, k, H, dt, empty):
