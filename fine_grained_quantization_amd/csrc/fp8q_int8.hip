@@ -75,9 +75,9 @@ __global__ __launch_bounds__(256) void quant_int8_kernel(const uint16_t *__restr
 // The large tile, 256 x 256 by 8 waves of 64 x 128, is bound by power: 4096 x 16384 x 7168 took 385 us with normal codes
 // and 272 us with zeros (an earlier 32 x 32 x 32 form).  So what counts is energy per product: 16 x 16 x 64 MFMAs reach
 // 4.0 Pop/s of normal codes where 32 x 32 x 32 reach 3.4 (nothing but MFMAs on every CU; 5.0 is the peak), and in that
-// order one operand changes from MFMA to MFMA.  Measured: 4096 x 18432 x 7168 in 400-410 us, 2.65 Pop/s (the library's
-// INT8 product of the same sizes, without scales: 585 us); 8192 tokens to 8 of 64 experts of 2048 x 7168 in 820-860 us.
-// 128 x 128 tiles, two workgroups to a CU, fill the chip at sizes where that tile does not (2048^3: 13 us).
+// order one operand changes from MFMA to MFMA.  Measured: 4096 x 18432 x 7168 in 400-425 us, 2.6 Pop/s (the library's
+// INT8 product of the same sizes, without scales: 585 us); 8192 tokens to 8 of 64 experts of 2048 x 7168 in 820-880 us.
+// 128 x 128 tiles, two workgroups to a CU, fill the chip at sizes where that tile does not (2048^3: 12.5 us).
 // ---------------------------------------------------------------------------------------------------------
 
 struct Int8Args {
