@@ -3,6 +3,10 @@
 Argument marshalling only: every step runs in the HIP library.  torch provides device memory and the
 current stream; outputs are allocated with torch when the caller does not pass them.  If the library
 is not built, every call raises -- there is no fallback path.
+
+Every call takes a ``stream`` (default: the current one) and launches there.  Ordering that stream behind the
+inputs, and the readers of the outputs behind it, is the caller's; outputs and temporaries that the call allocates
+are safe to drop at any time.
 """
 from __future__ import annotations
 
@@ -111,6 +115,33 @@ def _stream_ptr(stream):
     return s.cuda_stream
 
 
+# Memory that a call allocates belongs to the stream that the call runs on.  torch hands a freed block to the
+# stream that allocated it without waiting, so a block of the current stream's, used on another, could still have
+# work of the current stream before it, and could be reused there while the other stream has not finished with it.
+def _scratch(stream, nbytes, device):
+    """A temporary of one call: freed on return, and reused only behind the call's own launches."""
+    if stream is None:
+        return torch.empty(max(nbytes, 4), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.empty(max(nbytes, 4), dtype=torch.uint8, device=device)
+
+
+def _empty(stream, shape, dtype, device):
+    """An output of a call.  On a given stream it is that stream's, and kept from reuse until the current stream
+    too is done with what was queued there before it was freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _torch_stream(stream, device):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream, device)
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -138,9 +169,9 @@ def fp8q_quant_act_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s: torc
     _need(x, "x", _BF16, 2)
     M, K = x.shape
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (M, K), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        s = _empty(stream, (K // 128, M), dtype=torch.float32, device=x.device)
     _need(q, "q", _FP8)
     _need(s, "s", (torch.float32,))
     if q.numel() != M * K or s.numel() != (K // 128) * M:
@@ -157,9 +188,9 @@ def fp8q_quant_act_fp4_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s: 
     _need(x, "x", _BF16, 2)
     M, K = x.shape
     if q is None:
-        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (M, K // 2), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        s = _empty(stream, (K // 128, M), dtype=torch.float32, device=x.device)
     _need(q, "q", (torch.uint8,))
     _need(s, "s", (torch.float32,))
     if q.numel() != M * (K // 2) or s.numel() != (K // 128) * M:
@@ -176,9 +207,9 @@ def fp8q_quant_w_fp4_128x128(w: torch.Tensor, q: torch.Tensor | None = None, s: 
     _need(w, "w", _BF16, 2)
     N, K = w.shape
     if q is None:
-        q = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
+        q = _empty(stream, (N, K // 2), dtype=torch.uint8, device=w.device)
     if s is None:
-        s = torch.empty((N // 128, K // 128), dtype=torch.float32, device=w.device)
+        s = _empty(stream, (N // 128, K // 128), dtype=torch.float32, device=w.device)
     _need(q, "q", (torch.uint8,))
     _need(s, "s", (torch.float32,))
     if q.numel() != N * (K // 2) or s.numel() != (N // 128) * (K // 128):
@@ -195,9 +226,9 @@ def fp8q_quant_act_e5m6_1x128(x: torch.Tensor, q: torch.Tensor | None = None, s:
     _need(x, "x", _BF16, 2)
     M, K = x.shape
     if q is None:
-        q = torch.empty((M, K // 2 * 3), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (M, K // 2 * 3), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        s = _empty(stream, (K // 128, M), dtype=torch.float32, device=x.device)
     _need(q, "q", (torch.uint8,))
     _need(s, "s", (torch.float32,))
     if q.numel() != M * (K // 2 * 3) or s.numel() != M * (K // 128):
@@ -214,9 +245,9 @@ def fp8q_quant_w_per_channel(w: torch.Tensor, q: torch.Tensor | None = None, s: 
     _need(w, "w", _BF16, 2)
     N, K = w.shape
     if q is None:
-        q = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+        q = _empty(stream, (N, K), dtype=torch.uint8, device=w.device)
     if s is None:
-        s = torch.empty((N,), dtype=torch.float32, device=w.device)
+        s = _empty(stream, (N,), dtype=torch.float32, device=w.device)
     _need(q, "q", (torch.uint8,))
     _need(s, "s", (torch.float32,))
     if q.numel() != N * K or s.numel() != N:
@@ -233,10 +264,10 @@ def fp8q_quant_act_dual(x: torch.Tensor, q=None, s=None, qt=None, st=None, strea
     _need(x, "x", _BF16, 2)
     M, K = x.shape
     dev = x.device
-    q = torch.empty((M, K), dtype=torch.uint8, device=dev) if q is None else q
-    s = torch.empty((K // 128, M), dtype=torch.float32, device=dev) if s is None else s
-    qt = torch.empty((K, M), dtype=torch.uint8, device=dev) if qt is None else qt
-    st = torch.empty((M // 128, K), dtype=torch.float32, device=dev) if st is None else st
+    q = _empty(stream, (M, K), dtype=torch.uint8, device=dev) if q is None else q
+    s = _empty(stream, (K // 128, M), dtype=torch.float32, device=dev) if s is None else s
+    qt = _empty(stream, (K, M), dtype=torch.uint8, device=dev) if qt is None else qt
+    st = _empty(stream, (M // 128, K), dtype=torch.float32, device=dev) if st is None else st
     for t, name, dt, n in ((q, "q", torch.uint8, M * K), (s, "s", torch.float32, (K // 128) * M),
                            (qt, "qt", torch.uint8, M * K), (st, "st", torch.float32, (M // 128) * K)):
         _need(t, name, (dt,))
@@ -268,9 +299,9 @@ def fp8q_swiglu_quant_act_1x128(x: torch.Tensor, y: torch.Tensor | None = None, 
         M, K = x.shape
         ld = x.stride(0)
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = _empty(stream, (M, K), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty((K // 128, M), dtype=torch.float32, device=x.device)
+        s = _empty(stream, (K // 128, M), dtype=torch.float32, device=x.device)
     _need(q, "q", _FP8)
     _need(s, "s", (torch.float32,))
     if q.numel() != M * K or s.numel() != (K // 128) * M:
@@ -289,7 +320,7 @@ def fp8q_swiglu_bf16(x: torch.Tensor, y: torch.Tensor, h: torch.Tensor | None = 
         raise ValueError("x and y must have the same shape and row stride")
     M, K = x.shape
     if h is None:
-        h = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+        h = _empty(stream, (M, K), dtype=torch.bfloat16, device=x.device)
     _need(h, "h", _BF16)
     if h.numel() != M * K:
         raise ValueError("h has the wrong size")
@@ -315,9 +346,9 @@ def fp8q_quant_w_128x128(w: torch.Tensor, q: torch.Tensor | None = None, s: torc
     N, K = w.shape[-2:]
     rows = N * (lead[0] if lead else 1)
     if q is None:
-        q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        q = _empty(stream, w.shape, dtype=torch.uint8, device=w.device)
     if s is None:
-        s = torch.empty(lead + (N // 128, K // 128), dtype=torch.float32, device=w.device)
+        s = _empty(stream, lead + (N // 128, K // 128), dtype=torch.float32, device=w.device)
     _need(q, "q", _FP8)
     _need(s, "s", (torch.float32,))
     if q.numel() != w.numel() or s.numel() != (rows // 128) * (K // 128):
@@ -337,7 +368,7 @@ def fp8q_dequant_w_128x128(q: torch.Tensor, s: torch.Tensor, w: torch.Tensor | N
     if s.numel() != (rows // 128) * (K // 128):
         raise ValueError("s has the wrong size")
     if w is None:
-        w = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        w = _empty(stream, q.shape, dtype=torch.bfloat16, device=q.device)
     _need(w, "w", _BF16)
     if w.numel() != q.numel():
         raise ValueError("w has the wrong size")
@@ -367,7 +398,7 @@ def fp8q_gemm_blockscaled(qa, sa, qw, sw, out_dtype=torch.bfloat16, c=None, stre
         raise ValueError("inconsistent GEMM operand shapes")
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qa.device)
     _need(c, "c", (out_dtype,))
     if c.numel() != M * N:
         raise ValueError("c has the wrong size")
@@ -391,7 +422,7 @@ def fp8q_grouped_gemm_blockscaled(qa, sa, qw, sw, offsets, out_dtype=torch.bfloa
         raise ValueError("inconsistent grouped GEMM operand shapes")
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qa.device)
     _need(c, "c", (out_dtype,))
     if c.numel() != M * N:
         raise ValueError("c has the wrong size")
@@ -420,7 +451,7 @@ def fp8q_grouped_gemm_blockscaled_gather(q, s, row_token, qw, sw, offsets, out_d
         raise ValueError("inconsistent grouped GEMM operand shapes")
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qw.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qw.device)
     _need(c, "c", (out_dtype,))
     if c.numel() != M * N:
         raise ValueError("c has the wrong size")
@@ -453,11 +484,10 @@ def fp8q_moe_route_topk(logits, k: int, rows: int | None = None, workspace=None,
     if wbytes < 0:
         raise ValueError(f"invalid routing sizes T={T} E={E}")
     if workspace is None:
-        workspace = torch.empty(max(wbytes, 4), dtype=torch.uint8, device=logits.device)
+        workspace = _scratch(stream, wbytes, logits.device)
     if out is None:
-        dev = logits.device
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty(E + 1, dtype=torch.int32, device=dev),
-               torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.int32, device=dev))
+        out = tuple(_empty(stream, shape, dtype=torch.int32, device=logits.device)
+                    for shape in ((T, k), E + 1, (T, k), rows))
     topk_idx, offsets, row_of, row_token = out
     for t, n, size in ((topk_idx, "topk_idx", T * k), (offsets, "offsets", E + 1), (row_of, "row_of", T * k),
                        (row_token, "row_token", rows)):
@@ -483,9 +513,8 @@ def fp8q_moe_route_topk_noalloc(logits, k: int, rows: int | None = None, out=Non
     cap = fp8q_moe_route_capacity(T, E, k)
     rows = cap if rows is None else rows
     if out is None:
-        dev = logits.device
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty(E + 1, dtype=torch.int32, device=dev),
-               torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.int32, device=dev))
+        out = tuple(_empty(stream, shape, dtype=torch.int32, device=logits.device)
+                    for shape in ((T, k), E + 1, (T, k), rows))
     topk_idx, offsets, row_of, row_token = out
     for t, n, size in ((topk_idx, "topk_idx", T * k), (offsets, "offsets", E + 1), (row_of, "row_of", T * k),
                        (row_token, "row_token", rows)):
@@ -517,9 +546,9 @@ def fp8q_moe_gather_fp8(q, s, row_of, row_token, offsets, qa=None, sa=None, stre
     if s.numel() != (K // 128) * T:
         raise ValueError("s has the wrong size")
     if qa is None:
-        qa = torch.empty((rows, K), dtype=torch.uint8, device=q.device)
+        qa = _empty(stream, (rows, K), dtype=torch.uint8, device=q.device)
     if sa is None:
-        sa = torch.empty((K // 128, rows), dtype=torch.float32, device=q.device)
+        sa = _empty(stream, (K // 128, rows), dtype=torch.float32, device=q.device)
     _need(qa, "qa", _FP8)
     _need(sa, "sa", (torch.float32,))
     if qa.numel() != rows * K or sa.numel() != (K // 128) * rows:
@@ -589,13 +618,14 @@ def fp8q_moe_gate_topk(logits, k: int, score: str = "sigmoid", bias=None, n_grou
     if wbytes < 0:
         raise ValueError(f"invalid gating sizes T={T} E={E}")
     if workspace is None:
-        workspace = torch.empty(max(wbytes, 4), dtype=torch.uint8, device=logits.device)
+        workspace = _scratch(stream, wbytes, logits.device)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous device tensor")
     if out is None:
         i32 = dict(dtype=torch.int32, device=logits.device)
-        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=logits.device),
-               torch.empty(E + 1, **i32), torch.empty((T, k), **i32), torch.empty(rows, **i32), torch.empty(E, **i32))
+        out = (_empty(stream, (T, k), **i32), _empty(stream, (T, k), dtype=torch.float32, device=logits.device),
+               _empty(stream, E + 1, **i32), _empty(stream, (T, k), **i32), _empty(stream, rows, **i32),
+               _empty(stream, E, **i32))
     topk_idx, topk_weight, offsets, row_of, row_token, load = out
     _need_out(topk_idx, "topk_idx", torch.int32, T * k)
     _need_out(topk_weight, "topk_weight", torch.float32, T * k)
@@ -625,7 +655,7 @@ def fp8q_moe_gate_backward(logits, topk_idx, grad_weight, score: str = "sigmoid"
     k = topk_idx.shape[1]
     _need_out(grad_weight, "grad_weight", torch.float32, T * k)
     if grad_logits is None:
-        grad_logits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        grad_logits = _empty(stream, (T, E), dtype=logits.dtype, device=logits.device)
     _need_out(grad_logits, "grad_logits", logits.dtype, T * E)
     _check(load_library().fp8q_moe_gate_backward(
         _ptr(logits), _out_code(logits.dtype), ld, T, E, k, code, 1 if renormalize else 0, scale, _ptr(topk_idx),
@@ -645,7 +675,7 @@ def fp8q_moe_combine(c, row_of, weight, add=None, y=None, stream=None):
     if add is not None:
         _need_out(add, "add", c.dtype, T * H)
     if y is None:
-        y = torch.empty((T, H), dtype=c.dtype, device=c.device)
+        y = _empty(stream, (T, H), dtype=c.dtype, device=c.device)
     _need_out(y, "y", c.dtype, T * H)
     _check(load_library().fp8q_moe_combine(_ptr(c), _out_code(c.dtype), rows, H, _ptr(row_of), _ptr(weight), T, k,
                                            _ptr(add), _ptr(y), _stream_ptr(stream)), "fp8q_moe_combine")
@@ -666,9 +696,9 @@ def fp8q_moe_combine_backward(grad_y, c, row_of, weight, row_token, offsets, gra
     _need_out(weight, "weight", torch.float32, T * k)
     _need_out(row_token, "row_token", torch.int32, rows)
     if grad_c is None:
-        grad_c = torch.empty_like(c)
+        grad_c = _empty(stream, c.shape, dtype=c.dtype, device=c.device)
     if grad_weight is None:
-        grad_weight = torch.empty((T, k), dtype=torch.float32, device=c.device)
+        grad_weight = _empty(stream, (T, k), dtype=torch.float32, device=c.device)
     _need_out(grad_c, "grad_c", c.dtype, rows * H)
     _need_out(grad_weight, "grad_weight", torch.float32, T * k)
     _check(load_library().fp8q_moe_combine_backward(
@@ -685,9 +715,9 @@ def fp8q_quant_int8(x, q=None, s=None, stream=None):
     M, K = x.shape
     ld = x.stride(0) if M > 1 and K > 0 else (K + 7) // 8 * 8
     if q is None:
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        q = _empty(stream, (M, K), dtype=torch.int8, device=x.device)
     if s is None:
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+        s = _empty(stream, (M,), dtype=torch.float32, device=x.device)
     _need_out(q, "q", torch.int8, M * K)
     _need_out(s, "s", torch.float32, M)
     _check(load_library().fp8q_quant_int8(_ptr(x), ld, M, K, _ptr(q), _ptr(s), _stream_ptr(stream)),
@@ -708,7 +738,7 @@ def fp8q_gemm_int8(qa, sa, qw, sw, out_dtype=torch.bfloat16, c=None, stream=None
     _need_out(sw, "sw", torch.float32, N)
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qa.device)
     _need_out(c, "c", out_dtype, M * N)
     _check(load_library().fp8q_gemm_int8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(c), code, M, N, K,
                                          _stream_ptr(stream)), "fp8q_gemm_int8")
@@ -729,7 +759,7 @@ def fp8q_grouped_gemm_int8(qa, sa, qw, sw, offsets, out_dtype=torch.bfloat16, c=
     _need_out(sw, "sw", torch.float32, E * N)
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qa.device)
     _need_out(c, "c", out_dtype, M * N)
     _check(load_library().fp8q_grouped_gemm_int8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(c), code, _ptr(offsets),
                                                  E, M, N, K, _stream_ptr(stream)), "fp8q_grouped_gemm_int8")
@@ -753,7 +783,7 @@ def fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets, out_dtype=to
     _need_out(sw, "sw", torch.float32, E * N)
     code = _out_code(out_dtype)
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=qw.device)
+        c = _empty(stream, (M, N), dtype=out_dtype, device=qw.device)
     _need_out(c, "c", out_dtype, M * N)
     _check(load_library().fp8q_grouped_gemm_int8_gather(
         _ptr(q), _ptr(s), T, _ptr(row_token), _ptr(qw), _ptr(sw), _ptr(c), code, _ptr(offsets), E, M, N, K,

@@ -337,7 +337,7 @@ __device__ __forceinline__ void scan_segments(const int32_t *total, int E, int32
 }
 
 // -1 into the rows that no token has: the ends of the segments and everything from seg[E] on.  Workgroup `part`
-// of `parts` does its share.
+// of `parts` does its share.  (A workspace that another call overwrites gives other counts: no store leaves row_token.)
 __device__ __forceinline__ void fill_empty(const LayoutArgs &o, const int32_t *seg, const int32_t *total, int E,
                                            int part, int parts) {
     const int tid = threadIdx.x;
@@ -345,10 +345,10 @@ __device__ __forceinline__ void fill_empty(const LayoutArgs &o, const int32_t *s
     for (int q = tid; q < n * 128; q += kGateThreads) {
         const int e = part + parts * (q >> 7);
         const int64_t r = (int64_t)seg[e] + total[e] + (q & 127);
-        if (r < seg[e + 1]) o.row_token[r] = -1;
+        if (r < seg[e + 1] && (uint64_t)r < (uint64_t)o.rows) o.row_token[r] = -1;
     }
     // seg[E] is a multiple of 128
-    const int64_t r0 = seg[E];
+    const int64_t r0 = seg[E] > 0 ? seg[E] : 0;
     if ((reinterpret_cast<uintptr_t>(o.row_token) & 15u) == 0) {
         const i32x4 none = {-1, -1, -1, -1};
         for (int64_t r = r0 + ((int64_t)part * kGateThreads + tid) * 4; r < o.rows; r += (int64_t)parts * kGateThreads * 4) {
@@ -512,7 +512,7 @@ __global__ __launch_bounds__(kGateThreads) void moe_gate_layout_kernel(LayoutArg
             if (e < 0) continue;  // an empty slot: its row is already -1
             const int32_t r = base[e] + (c == c0 ? first_r : o.row_of[at]);
             o.row_of[at] = r;
-            if (r < o.rows) o.row_token[r] = (int32_t)(t0 + i / k);
+            if ((uint64_t)(int64_t)r < (uint64_t)o.rows) o.row_token[r] = (int32_t)(t0 + i / k);
         }
         if (c + 1 < c1) {
             __syncthreads();

@@ -181,10 +181,12 @@ __global__ __launch_bounds__(1024) void moe_scan_kernel(int32_t *__restrict__ ch
                 }
         }
     }
-    // Empty rows: each segment's padding, then everything past the last segment.
+    // Empty rows: each segment's padding, then everything past the last segment.  (Calls that share a workspace and
+    // overlap give each other wrong counts: no store leaves row_token.)
+    auto inside = [&](int64_t r) { return r < 0 ? 0 : (r < rows ? r : rows); };
     if (tid < E)
-        for (int64_t r = seg[tid] + total[tid]; r < seg[tid + 1]; r++) row_token[r] = -1;
-    for (int64_t r = seg[E] + tid; r < rows; r += 1024) row_token[r] = -1;
+        for (int64_t r = inside(seg[tid] + total[tid]), end = inside(seg[tid + 1]); r < end; r++) row_token[r] = -1;
+    for (int64_t r = inside(seg[E]) + tid; r < rows; r += 1024) row_token[r] = -1;
 }
 
 template <int KMAX>
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(64) void moe_assign_kernel(const int32_t *__restric
         if (j < k) {
             const int64_t r = (int64_t)base[j] + rk[j];
             row_of[t * k + j] = (int32_t)r;
-            if (r < rows) row_token[r] = (int32_t)t;
+            if ((uint64_t)r < (uint64_t)rows) row_token[r] = (int32_t)t;
         }
 }
 
