@@ -329,6 +329,7 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
     // whole row segments are stored: a wave's block of 16 TM rows x at most 256 bytes at a time, the 16-byte chunks of row r
     // at chunk ^ (r % 16).
     float sa[TM];
+    bool there[TM];  // (a row of no token is +0 whatever the channels' scales are: negative, infinite, NaN)
 #pragma unroll
     for (int mi = 0; mi < TM; mi++) {
         const int64_t m = m0 + wm + 16 * mi + (lane & 15);
@@ -337,6 +338,7 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
             src = src >= 0 ? p.rtok[src] : -1;
             if (src >= p.T) src = -1;
         }
+        there[mi] = !GATHER || src >= 0;
         sa[mi] = src >= 0 ? p.sa[src] : 0.0f;
     }
     constexpr int kMaxRow = S::kWaves * 16 * TM * 256 <= S::kLds ? 256 : 128;
@@ -361,7 +363,7 @@ __device__ __forceinline__ void int8_tile(uint8_t *lds, const Int8Args &p, const
                 const int r = 16 * mi + (lane & 15);
                 v4f v;
 #pragma unroll
-                for (int i = 0; i < 4; i++) v[i] = (float)acc[ni][mi][i] * (sa[mi] * sw[i]);
+                for (int i = 0; i < 4; i++) v[i] = there[mi] ? (float)acc[ni][mi][i] * (sa[mi] * sw[i]) : 0.0f;
                 const int byte = (nl - 16 * n1) * kEl;
                 store4<OUT_BF16>(blk + r * kRowBytes + ((((byte >> 4) ^ r) & (kChunks - 1)) << 4) + (byte & 15), 0, v);
             }
@@ -557,7 +559,8 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
             const float sa = src >= 0 ? p.sa[src] : 0.0f;
             v4f v;
 #pragma unroll
-            for (int r = 0; r < 4; r++) v[r] = (float)sum[(q * 4 + r) * 64 + lane] * (sa * SW[nl + r]);
+            for (int r = 0; r < 4; r++)
+                v[r] = src >= 0 ? (float)sum[(q * 4 + r) * 64 + lane] * (sa * SW[nl + r]) : 0.0f;
             store4<OUT_BF16>(p.c, m * p.N + n0 + nl, v);
         }
         __syncthreads();  // the sums have been read before the next rows' copies overwrite them

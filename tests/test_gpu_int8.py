@@ -237,6 +237,29 @@ def test_gather_tokens_out_of_range_are_empty_rows():
     assert (host(c) == 0).all()
 
 
+@pytest.mark.parametrize("T,E,rows,N,K", [(6, 16, 2048, 264, 144), (60, 2, 512, 264, 144), (1600, 2, 4096, 4104, 272)])
+def test_gathered_rows_of_no_token_are_zero_whatever_the_scales(T, E, rows, N, K):
+    """+0 beside tokens in the same tile too, by the kernel of few rows, the small tiles and the large ones; channel
+    scales negative, infinite and NaN."""
+    rng = np.random.default_rng([54, T])
+    q, s, _, _ = operands(rng, T, 8, K)
+    qw = rng.integers(-127, 128, (E, N, K), dtype=np.int8)
+    sw = rng.standard_normal((E, N)).astype(np.float32)
+    sw[:, ::5], sw[:, 1::7], sw[:, 2::9] = np.inf, -np.inf, np.nan
+    row_token = np.where(rng.random(rows) < 0.5, rng.integers(0, T, rows), -1).astype(np.int32)
+    row_token[rows // 2:rows // 2 + 20] = -1
+    off = (np.arange(E + 1) * (rows // E)).astype(np.int32)
+    for dt in (torch.bfloat16, torch.float32):
+        say(f"int8 gather, empty rows beside tokens T={T} rows={rows} {dt}")
+        c = fq.fp8q_grouped_gemm_int8_gather(*dev(q, s, row_token, qw, sw, off), out_dtype=dt)
+        bits = host(c.view(torch.int16 if dt == torch.bfloat16 else torch.int32))
+        assert (bits[row_token < 0] == 0).all()
+        fine = np.isfinite(sw[0])
+        r = np.nonzero(row_token[:rows // E] >= 0)[0]
+        want = ref.gemm_int8(q[row_token[r]], s[row_token[r]], qw[0][fine], sw[0][fine])
+        check_out(c[:rows // E][torch.from_numpy(r).cuda()][:, torch.from_numpy(fine).cuda()].contiguous(), want, "tokens")
+
+
 @pytest.mark.parametrize("used", [3, 300])
 def test_gather_from_the_largest_token_array(used):
     """T * K = 2^31 - 2048, the last tokens among the rows, by the kernel of few rows and by the tiles."""
