@@ -602,8 +602,8 @@ def fp8q_moe_gate_topk(logits, k: int, score: str = "sigmoid", bias=None, n_grou
     ``n_group`` groups (a group's value is the sum of its ``group_top`` largest keys), the weights are the chosen
     scores, divided by their sum if ``renormalize``, times ``scale``.  Experts whose logit is -inf or NaN are never
     chosen; slots without an expert get expert -1, weight 0 and row -1.  ``rows`` defaults to
-    :func:`fp8q_moe_route_capacity`; ``workspace`` (``fp8q_moe_gate_workspace_bytes(T, E)`` bytes) and ``out`` (the
-    six outputs) are allocated when not given."""
+    :func:`fp8q_moe_route_capacity`; ``workspace`` (``fp8q_moe_gate_workspace_bytes(T, E)`` bytes, or that of more
+    tokens) and ``out`` (the six outputs) are allocated when not given."""
     ld = _need_logits(logits)
     T, E = logits.shape
     lib = load_library()

@@ -331,7 +331,7 @@ int fp8q_moe_gate_topk(const void *logits, int dtype, int64_t ld, int64_t T, int
     if ((score != FP8Q_SCORE_SIGMOID && score != FP8Q_SCORE_SOFTMAX) || (group_top != 1 && group_top != 2) ||
         (renormalize != 0 && renormalize != 1))
         return FP8Q_ERR_OPTION;
-    const int64_t need = fp8q::moe_gate_workspace_bytes(T, E);
+    const int64_t need = fp8q::moe_gate_least_workspace_bytes(T, E);
     if (!offsets || !row_token) return FP8Q_ERR_NULL;
     if (T > 0 && (!logits || !topk_idx || !topk_weight || !row_of || (need > 0 && !workspace))) return FP8Q_ERR_NULL;
     if (!aligned4(offsets) || !aligned4(row_token) || !aligned4(load) || !aligned4(bias)) return FP8Q_ERR_ALIGN;
@@ -344,7 +344,7 @@ int fp8q_moe_gate_topk(const void *logits, int dtype, int64_t ld, int64_t T, int
     const fp8q::GateShape g = {logits, bias, ld, T, (int)E, (int)k, (int)n_group, (int)topk_group, (int)group_top,
                                scale, dtype == FP8Q_OUT_BF16, score == FP8Q_SCORE_SOFTMAX, renormalize != 0};
     return finish(fp8q::launch_moe_gate_topk(g, topk_idx, topk_weight, offsets, row_of, row_token, rows, load,
-                                             workspace, static_cast<hipStream_t>(stream)));
+                                             workspace, workspace_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int fp8q_moe_gate_backward(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, int score,

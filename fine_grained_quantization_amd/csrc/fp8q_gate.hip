@@ -666,24 +666,28 @@ bool lanes_aligned(const void *p, int64_t ld, int n, int R, bool bf16) {
 }  // namespace
 
 namespace {
+int64_t counts_bytes(int64_t T, int64_t E, int64_t chunk) { return (T + chunk - 1) / chunk * ((E + 3) / 4 * 4); }
 // Tokens per workgroup: 16 while that gives every CU at most one workgroup, if the counts' rows need no padding (so that
-// the workspace stays within the other routing's), else 32.
-int chunk_tokens(int64_t T, int64_t E) { return T <= 4096 && E % 4 == 0 ? 16 : kGateChunk; }
+// the workspace stays within the other routing's) and the workspace holds them, else 32.
+int chunk_tokens(int64_t T, int64_t E, int64_t workspace_bytes) {
+    return T <= 4096 && E % 4 == 0 && counts_bytes(T, E, 16) <= workspace_bytes ? 16 : kGateChunk;
+}
 }  // namespace
 
 int64_t moe_gate_workspace_bytes(int64_t T, int64_t E) {
-    if (T <= kGateChunk) return 0;
-    const int64_t chunk = chunk_tokens(T, E);
-    return (T + chunk - 1) / chunk * ((E + 3) / 4 * 4);
+    return T <= kGateChunk ? 0 : counts_bytes(T, E, chunk_tokens(T, E, INT64_MAX));
+}
+int64_t moe_gate_least_workspace_bytes(int64_t T, int64_t E) {
+    return T <= kGateChunk ? 0 : counts_bytes(T, E, kGateChunk);
 }
 
 hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *topk_weight, int32_t *offsets,
                                 int32_t *row_of, int32_t *row_token, int64_t rows, int32_t *load, void *workspace,
-                                hipStream_t stream) {
+                                int64_t workspace_bytes, hipStream_t stream) {
     const LayoutArgs o = {topk_idx, topk_weight, offsets, row_of, row_token, load, static_cast<uint8_t *>(workspace),
                           rows};
     const bool one = g.T <= kGateChunk;
-    const int chunk = one ? kGateChunk : chunk_tokens(g.T, g.E);
+    const int chunk = one ? kGateChunk : chunk_tokens(g.T, g.E, workspace_bytes);
     const int64_t C = (g.T + chunk - 1) / chunk;
     // A few tokens: 64 lanes each, the shortest way to an answer.  Many: 16 lanes each, which takes half the instructions
     // (8192 tokens, 256 experts: 15.4 us by 64 lanes, 11.0 by 16), where a lane then holds at most 32 experts.

@@ -59,10 +59,11 @@ struct GateShape {
     float scale;
     bool bf16, softmax, renorm;
 };
-int64_t moe_gate_workspace_bytes(int64_t T, int64_t E);
+int64_t moe_gate_workspace_bytes(int64_t T, int64_t E);        // to run at its best
+int64_t moe_gate_least_workspace_bytes(int64_t T, int64_t E);  // to run at all; never less for more tokens
 hipError_t launch_moe_gate_topk(const GateShape &g, int32_t *topk_idx, float *topk_weight, int32_t *offsets,
                                 int32_t *row_of, int32_t *row_token, int64_t rows, int32_t *load, void *workspace,
-                                hipStream_t stream);
+                                int64_t workspace_bytes, hipStream_t stream);
 hipError_t launch_moe_gate_backward(const GateShape &g, const int32_t *topk_idx, const float *grad_weight,
                                     void *grad_logits, hipStream_t stream);
 hipError_t launch_moe_combine(const void *c, bool bf16, int64_t rows, int64_t H, const int32_t *row_of,

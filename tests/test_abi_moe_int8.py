@@ -47,6 +47,17 @@ def test_gate_workspace(lib):
     assert need(-1, 5) == -1 and need(5, 0) == -1 and need(5, 1025) == -1
 
 
+@pytest.mark.parametrize("E", [1, 5, 8, 64, 255, 256, 1024])
+def test_gate_refuses_only_less_than_the_counts_of_32_token_chunks(lib, E):
+    for T in (33, 64, 65, 3009, 4096, 4097, 6000):
+        least = (T + 31) // 32 * ((E + 3) // 4 * 4)
+        assert least <= lib.fp8q_moe_gate_workspace_bytes(T, E)
+        change = dict(T=T, E=E, ld=E, k=1, n_group=1, topk_group=1)
+        assert lib.fp8q_moe_gate_topk(*{**GATE, **change, "wsb": least - 1}.values()) == WORKSPACE
+    needs = [lib.fp8q_moe_gate_workspace_bytes(T, E) for T in range(1, 9000)]
+    assert all((t + 31) // 32 * ((E + 3) // 4 * 4) <= min(needs[t - 1:]) for t in range(33, 9000))
+
+
 BACK = dict(logits=A, dtype=1, ld=64, T=4, E=64, k=4, score=0, renorm=1, scale=1.0, idx=A, gw=A, out=B, stream=None)
 
 

@@ -179,6 +179,22 @@ def test_gate_repeats_bit_for_bit_and_agrees_over_batch_sizes():
     assert np.array_equal(a[0][100:117], one[0]) and np.array_equal(a[1][100:117], one[1])
 
 
+@pytest.mark.parametrize("most,E", [(6000, 256), (4097, 64), (33, 8), (5000, 36)])
+def test_a_workspace_made_for_a_batch_does_for_smaller_ones(most, E):
+    """Bit for bit the results of a call with a workspace of its own."""
+    need = fq.load_library().fp8q_moe_gate_workspace_bytes
+    rng = np.random.default_rng([13, most])
+    x = torch.from_numpy(rng.standard_normal((most, E)).astype(np.float32)).cuda()
+    for T in sorted({t for t in (1, 32, 33, 40, 2000, 3009, 4095, 4096, 4097, most) if t <= most}):
+        ws = torch.full((need(most, E) + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        say(f"gate workspace for {most} tokens, T={T} E={E}")
+        for score in ("sigmoid", "softmax"):
+            got = fq.fp8q_moe_gate_topk(x[:T], 4, score=score, n_group=4, topk_group=2, workspace=ws[:need(most, E)])
+            want = fq.fp8q_moe_gate_topk(x[:T], 4, score=score, n_group=4, topk_group=2)
+            assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(got, want))
+        assert (ws[need(most, E):] == 0xA5).all()
+
+
 GRADS = [  # T, E, k, score, renorm, scale, dtype
     (1, 256, 8, "sigmoid", True, 2.5, "f32"), (7, 5, 2, "softmax", True, 1.0, "f32"),
     (130, 64, 8, "softmax", False, 1.0, "bf16"), (33, 100, 3, "sigmoid", False, 1.5, "f32"),
