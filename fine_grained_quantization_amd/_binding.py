@@ -333,7 +333,7 @@ def _need_rows(t, name):
     """A bf16 [M, K] device view whose rows are contiguous (any row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _BF16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bf16 device tensor")
-    if t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+    if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
 
 

@@ -43,3 +43,13 @@ def test_gemms_and_dequant_with_no_rows():
                                   torch.zeros((0, 4), dtype=torch.float32, device="cuda"))
     assert w.shape == (0, 512)
     torch.cuda.synchronize()
+
+
+def test_empty_rows_that_are_not_contiguous_are_refused_as_full_ones_are():
+    """The rule for rows (elements beside each other) does not depend on how many rows there are."""
+    for rows in (0, 2):
+        x = torch.zeros((rows, 512), dtype=torch.bfloat16, device="cuda")[:, ::2]
+        for f in (lambda: fq.fp8q_swiglu_bf16(x, x), lambda: fq.fp8q_swiglu_quant_act_1x128(x, x),
+                  lambda: fq.fp8q_swiglu_quant_act_1x128(x), lambda: fq.fp8q_quant_int8(x)):
+            with pytest.raises(ValueError, match="contiguous rows"):
+                f()
