@@ -29,27 +29,24 @@ class Int8MoE:
         qd, sd = fq.fp8q_quant_int8(down.view(-1, self.F))
         self.up = qu.view_as(up), su.view(self.E, F2)
         self.down = qd.view_as(down), sd.view(self.E, self.H)
-        self.rows = -1
 
     def forward(self, x, logits, shared=None):
-        """x bf16 [T, H], logits float32 [T, E], shared bf16 [T, H] or None -> y bf16 [T, H], and what backward needs."""
+        """x bf16 [T, H], logits float32 [T, E], shared bf16 [T, H] or None -> y bf16 [T, H], and what backward needs
+        (its own expert rows among it: any number of forward calls may come before a backward)."""
         idx, w, off, row_of, row_token, load = fq.fp8q_moe_gate_topk(logits, self.topk, **self.gate)
-        if self.rows != row_token.numel():  # rows past the layout's end are not written: keep them zeros
-            self.rows = row_token.numel()
-            self.c1 = torch.zeros((self.rows, 2 * self.F), dtype=torch.bfloat16, device=x.device)
-            self.c2 = torch.zeros((self.rows, self.H), dtype=torch.bfloat16, device=x.device)
         q, s = fq.fp8q_quant_int8(x)
-        fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, *self.up, off, c=self.c1)
-        h = fq.fp8q_swiglu_bf16(self.c1[:, :self.F], self.c1[:, self.F:])
+        # (Rows from off[E] on are not written: they hold what the memory held, and no result comes from them.)
+        c1 = fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, *self.up, off)
+        h = fq.fp8q_swiglu_bf16(c1[:, :self.F], c1[:, self.F:])
         q, s = fq.fp8q_quant_int8(h)
-        fq.fp8q_grouped_gemm_int8(q, s, *self.down, off, c=self.c2)
-        y = fq.fp8q_moe_combine(self.c2, row_of, w, add=shared)
-        return y, (logits, idx, w, off, row_of, row_token, load)
+        self.c2 = c2 = fq.fp8q_grouped_gemm_int8(q, s, *self.down, off)  # (self.c2: the last call's, to look at)
+        y = fq.fp8q_moe_combine(c2, row_of, w, add=shared)
+        return y, (logits, idx, w, off, row_of, row_token, c2, load)
 
     def backward(self, grad_y, saved):
-        """Gradients of the last forward: of the expert rows [rows, H] and of the logits [T, E]."""
-        logits, idx, w, off, row_of, row_token, _ = saved
-        grad_c, grad_w = fq.fp8q_moe_combine_backward(grad_y, self.c2, row_of, w, row_token, off)
+        """Gradients of the forward call that gave `saved`: of the expert rows [rows, H] and of the logits [T, E]."""
+        logits, idx, w, off, row_of, row_token, c2, _ = saved
+        grad_c, grad_w = fq.fp8q_moe_combine_backward(grad_y, c2, row_of, w, row_token, off)
         return grad_c, fq.fp8q_moe_gate_backward(logits, idx, grad_w, score="sigmoid", scale=self.gate["scale"])
 
 

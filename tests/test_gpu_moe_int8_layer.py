@@ -77,6 +77,28 @@ def test_router_gradient_against_differences():
         assert bool(((diff - gl[:, e].double()).abs() <= (1e-8 + 64 * 2.0 ** -24) * mag[:, 0]).all())
 
 
+def test_gradients_after_several_forward_calls():
+    """Each backward is that of the forward call whose values it is given, as in gradient accumulation: the same bits as
+    a backward right behind its forward call, also where a call with fewer tokens came between."""
+    layer, _, _, x, logits, shared = build(200, 512, 272, 16, 4, 6)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    parts = [(x, logits, shared), (torch.randn(x.shape, device="cuda", generator=g).bfloat16(), logits.flip(0), shared),
+             (x[:40], logits[:40], None)]
+    grads = [torch.randn(p[0].shape, device="cuda", generator=g).bfloat16() for p in parts]
+    say("int8 layer: three forward calls, then their gradients")
+    want = []
+    for p, r in zip(parts, grads):
+        y, saved = layer.forward(*p)
+        gc, gl = layer.backward(r, saved)
+        want.append((y.clone(), gc[:int(saved[3][-1])].clone(), gl.clone()))
+    calls = [layer.forward(*p) for p in parts]
+    for (y, saved), r, (wy, wc, wl) in zip(calls, grads, want):
+        gc, gl = layer.backward(r, saved)
+        assert torch.equal(gl, wl)
+        assert torch.equal(gc[:int(saved[3][-1])].view(torch.int16), wc.view(torch.int16))
+        assert torch.equal(y.view(torch.int16), wy.view(torch.int16))
+
+
 def test_layer_on_another_stream():
     layer, _, _, x, logits, shared = build(300, 512, 272, 16, 4, 4)
     want, _ = layer.forward(x, logits, shared)
