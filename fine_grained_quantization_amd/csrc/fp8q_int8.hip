@@ -423,10 +423,9 @@ __global__ __launch_bounds__(64 * WM * WN, TM * TN <= 8 && AHEAD == 2 ? 4 : 2) v
 
 constexpr int kSplitWaves = 8;
 
-// MODE 0: dense.  1: expert segments; a workgroup takes one slice of one expert's channels and walks the segment's rows
-// 16 TM at a time.  2: the same with row r's codes those of token rtok[r]; where none of the rows has a token it only
-// stores zeros.
-template <bool OUT_BF16, int MODE, int TM, int NS>
+// GATHER: expert segments, row r's codes those of token rtok[r]; a workgroup takes one slice of one expert's channels and
+// walks the segment's rows 16 TM at a time; where none of them has a token it only stores zeros.  Else dense.
+template <bool OUT_BF16, bool GATHER, int TM, int NS>
 __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(Int8Args p, int64_t cols_per_wg) {
     constexpr int kA = TM * 2048, kSlot = (TM + NS) * 2048, kSum = TM * NS * 1024;
     constexpr int kLds = kSplitWaves * kSlot > kSum ? kSplitWaves * kSlot : kSum;
@@ -436,7 +435,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
     const int64_t K = p.K;
     const int KB = (int)((K + 127) >> 7);
     int64_t m0, mend, n0, e = 0;
-    if constexpr (MODE == 0) {
+    if constexpr (!GATHER) {
         // Row tiles of one slice of channels are neighbours, so that the slice's weights are read by them together.
         const int64_t nt = blockIdx.x / p.n_mtiles;
         m0 = (blockIdx.x - nt * p.n_mtiles) * 16 * TM;
@@ -465,7 +464,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
     int *sum = reinterpret_cast<int *>(lds);
     for (; m0 < mend; m0 += 16 * TM) {
         const int64_t nrow = mend - m0 < 16 * TM ? mend - m0 : 16 * TM;
-        if constexpr (MODE == 2) {
+        if constexpr (GATHER) {
             int64_t tok = lane < nrow ? p.rtok[m0 + lane] : -1;
             static_assert(16 * TM <= 64, "a lane per row");
             if (__ballot(tok >= 0 && tok < p.T) == 0) {  // the same in every wave
@@ -478,13 +477,13 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
                 continue;
             }
         }
-        const i32x4 ra = MODE == 2 ? make_rsrc(p.qa, (uint64_t)(p.T * K)) : make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
+        const i32x4 ra = GATHER ? make_rsrc(p.qa, (uint64_t)(p.T * K)) : make_rsrc(p.qa + m0 * K, (uint64_t)(nrow * K));
 #pragma unroll
         for (int j = 0; j < 2 * TM; j++) {
             const int r = 8 * j + (lane >> 3);
             int64_t row = r < nrow ? r : -1;
-            if constexpr (MODE == 2) row = row >= 0 ? p.rtok[m0 + row] : -1;
-            avoff[j] = row >= 0 && (MODE != 2 || row < p.T) ? (int)(row * K + (j & 1 ? c0 ^ 1 : c0) * 16) : kFar;
+            if constexpr (GATHER) row = row >= 0 ? p.rtok[m0 + row] : -1;
+            avoff[j] = row >= 0 && (!GATHER || row < p.T) ? (int)(row * K + (j & 1 ? c0 ^ 1 : c0) * 16) : kFar;
         }
         auto issue = [&](int kb) {
             const bool in = kb < KB;
@@ -552,7 +551,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
             const int nl = 16 * ni + 4 * (lane >> 4);  // channels nl .. nl + 3 of the slice: all in or all out
             if (m >= mend || nl >= ncol) continue;
             int64_t src = m;
-            if constexpr (MODE == 2) {
+            if constexpr (GATHER) {
                 src = p.rtok[m];
                 if (src >= p.T) src = -1;
             }
@@ -567,26 +566,26 @@ __global__ __launch_bounds__(64 * kSplitWaves, 2) void gemm_int8_split_kernel(In
     }
 }
 
-template <int MODE, int TM, int NS>
+template <bool GATHER, int TM, int NS>
 hipError_t launch_int8_split(Int8Args p, int64_t cols, bool out_bf16, hipStream_t stream) {
-    p.n_mtiles = MODE == 0 ? (p.M + 16 * TM - 1) / (16 * TM) : p.E;
+    p.n_mtiles = GATHER ? p.E : (p.M + 16 * TM - 1) / (16 * TM);
     p.n_ntiles = (p.N + cols - 1) / cols;
     const dim3 grid((unsigned)(p.n_mtiles * p.n_ntiles));
     if (out_bf16)
-        gemm_int8_split_kernel<true, MODE, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
+        gemm_int8_split_kernel<true, GATHER, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     else
-        gemm_int8_split_kernel<false, MODE, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
+        gemm_int8_split_kernel<false, GATHER, TM, NS><<<grid, 64 * kSplitWaves, 0, stream>>>(p, cols);
     return hipGetLastError();
 }
 
-template <int TM, int MODE>
+template <int TM, bool GATHER>
 hipError_t launch_int8_split_cols(const Int8Args &p, int64_t cols, bool out_bf16, hipStream_t stream) {
     switch ((cols + 15) / 16) {
-        case 1: return launch_int8_split<MODE, TM, 1>(p, cols, out_bf16, stream);
-        case 2: return launch_int8_split<MODE, TM, 2>(p, cols, out_bf16, stream);
-        case 3: return launch_int8_split<MODE, TM, 3>(p, cols, out_bf16, stream);
-        case 4: return launch_int8_split<MODE, TM, 4>(p, cols, out_bf16, stream);
-        default: return launch_int8_split<MODE, TM, 5>(p, cols, out_bf16, stream);
+        case 1: return launch_int8_split<GATHER, TM, 1>(p, cols, out_bf16, stream);
+        case 2: return launch_int8_split<GATHER, TM, 2>(p, cols, out_bf16, stream);
+        case 3: return launch_int8_split<GATHER, TM, 3>(p, cols, out_bf16, stream);
+        case 4: return launch_int8_split<GATHER, TM, 4>(p, cols, out_bf16, stream);
+        default: return launch_int8_split<GATHER, TM, 5>(p, cols, out_bf16, stream);
     }
 }
 
@@ -678,8 +677,12 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
 }
 
 // The host sees the layout's capacity (T k + 127 E rows, rounded up to 128) and not the segments.
-//  - Up to 2 rows an expert on average, or up to 16 and so few 128 x 128 tiles that they leave CUs idle: the waves split K
-//    (one token, 8 of 64 experts of 2048 x 7168: 26 us, by 128 x 128 tiles 39; 32 tokens: 195 and 180).
+//  - Gathered rows, up to 2 an expert on average, or up to 16 and so few 128 x 128 tiles that they leave CUs idle: the waves
+//    split K.  Measured, top-8 (split K / 128 x 128 tiles): 64 experts of 2048 x 7168, one token 25 / 38 us, 4 tokens 83 / 79,
+//    32 tokens 198 / 177; 64 of 7168 x 2048, one token 40 / 37; 256 of them, one token 80 / 153; 8 experts of 2048 x 7168,
+//    top-2, one token 11 / 34, 32 tokens 23 / 38.  Not for rows in place: every 16 rows of a segment, padding too, would
+//    read the weights again, where a tile reads them once for 128 (the first layer: one token 141 / 39, 16 tokens 1018 /
+//    196; the second, 4 tokens 466 / 122).
 //  - Up to 32 rows, or where the estimated time is less: 128 x 128 tiles, two to a CU.  Measured with 64 experts of 2048 x
 //    7168 (256 x 256 tiles / 128 x 128): 4 rows on average 204 / 180 us, 16 rows 207 / 186, 64 rows 212 / 231, 256 rows 300
 //    / 359, 1024 rows 876 / 1098.
@@ -689,13 +692,16 @@ hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t str
     const int64_t rows = p.M > 127 * p.E + 64 ? p.M - 127 * p.E - 64 : 0;
     const int64_t ncu = cu_count(), KB = (p.K + 127) / 128;
     auto tiles = [](int64_t n, int64_t t) { return (n + t - 1) / t; };
-    if (rows <= 2 * p.E || (rows <= 16 * p.E && p.E * tiles(p.N, 128) <= ncu)) {
-        // A slice of channels per workgroup and expert: as few slices as put a workgroup on every CU, at most 80 channels.
-        const int64_t want = (ncu + p.E - 1) / p.E;
-        int64_t cols = 8 * ((p.N / 8 + want - 1) / want);
-        cols = cols < 80 ? cols : 80;
-        if (p.E * tiles(p.N, cols) <= 0xFFFFFFFFll / (64 * kSplitWaves))
-            return launch_int8_split_cols<1, GATHER ? 2 : 1>(p, cols, out_bf16, stream);
+    if constexpr (GATHER) {
+        if (rows <= 2 * p.E || (rows <= 16 * p.E && p.E * tiles(p.N, 128) <= ncu)) {
+            // A slice of channels per workgroup and expert: as few slices as put a workgroup on every CU, at most 80
+            // channels.
+            const int64_t want = (ncu + p.E - 1) / p.E;
+            int64_t cols = 8 * ((p.N / 8 + want - 1) / want);
+            cols = cols < 80 ? cols : 80;
+            if (p.E * tiles(p.N, cols) <= 0xFFFFFFFFll / (64 * kSplitWaves))
+                return launch_int8_split_cols<1, true>(p, cols, out_bf16, stream);
+        }
     }
     const int64_t small = (rows + 64 * p.E) / 128 * tiles(p.N, 128);
     const int64_t large = ((rows + 64 * p.E) / 256 + p.E / 4) * tiles(p.N, 256);
@@ -733,9 +739,9 @@ hipError_t launch_gemm_int8(const uint8_t *qa, const float *sa, const uint8_t *q
     const Int8Plan plan = plan_int8(M, N, K);
     switch (plan.kind) {
         case Int8Plan::kSplitK:
-            if (plan.tm == 1) return launch_int8_split_cols<1, 0>(p, plan.cols, out_bf16, stream);
-            if (plan.tm == 2) return launch_int8_split_cols<2, 0>(p, plan.cols, out_bf16, stream);
-            return launch_int8_split_cols<4, 0>(p, plan.cols, out_bf16, stream);
+            if (plan.tm == 1) return launch_int8_split_cols<1, false>(p, plan.cols, out_bf16, stream);
+            if (plan.tm == 2) return launch_int8_split_cols<2, false>(p, plan.cols, out_bf16, stream);
+            return launch_int8_split_cols<4, false>(p, plan.cols, out_bf16, stream);
         case Int8Plan::kSmall: return launch_int8_tile<false, false, false, 2, 4, 4, 2>(p, N, out_bf16, stream);
         case Int8Plan::kDeep: return launch_int8_tile<false, false, false, 2, 4, 4, 2, 4>(p, N, out_bf16, stream);
         case Int8Plan::kTall: return launch_int8_tile<false, false, false, 4, 4, 4, 2>(p, N, out_bf16, stream);

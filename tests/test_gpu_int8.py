@@ -199,6 +199,44 @@ def test_grouped_and_gather(T, E, k, N, K):
             assert (c[used:] == 77.0).all()  # rows from offsets[E] on are not written
 
 
+def call_time(f, n=10):
+    """Median over 7 loops of n calls."""
+    times = []
+    for _ in range(8):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        for _ in range(n):
+            f()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end))
+    return sorted(times[1:])[3]
+
+
+@pytest.mark.parametrize("T,E,N,K", [(1, 64, 2048, 7168), (16, 64, 2048, 7168), (4, 64, 7168, 2048)])
+def test_rows_in_place_read_the_weights_about_once(T, E, N, K):
+    """A decode batch's product with rows in place takes at most 2.5 times as long as the form that reads the tokens through
+    the layout (it has the padding to multiply too, but not the weights to read for every few rows of it)."""
+    offsets, row_token, q, s, qw, sw, _ = (dev(a)[0] for a in grouped_layout(T, E, 8, N, K))
+    rows, pad = row_token.numel(), row_token[:, None] < 0
+    qa = torch.where(pad, 0, q[row_token.clamp(min=0).long()])
+    sa = torch.where(pad[:, 0], 0.0, s[row_token.clamp(min=0).long()])
+    c = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+    say(f"int8 grouped, rows in place and gathered, T={T} E={E} N={N} K={K}")
+    place = call_time(lambda: fq.fp8q_grouped_gemm_int8(qa, sa, qw, sw, offsets, c=c))
+    gather = call_time(lambda: fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets, c=c))
+    assert place < 2.5 * gather
+
+
+def grouped_layout(T, E, k, N, K):
+    """Layout, tokens and weights without the expected result (sizes at which the host would take long)."""
+    rng = np.random.default_rng([55, T, E])
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    offsets, row_of, row_token, _ = ref.layout(idx, E, fq.fp8q_moe_route_capacity(T, E, k))
+    return (offsets, row_token, rng.integers(-127, 128, (T, K), dtype=np.int8), rng.random(T).astype(np.float32),
+            rng.integers(-127, 128, (E, N, K), dtype=np.int8), rng.random((E, N)).astype(np.float32), row_of)
+
+
 def test_grouped_offsets_that_break_the_rules():
     """Offsets off the 128-row grid, starting past 0 and ending past the buffer are cut to it."""
     E, N, K, M = 3, 40, 64, 256
