@@ -676,7 +676,9 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
     return best;
 }
 
-// The host sees the layout's capacity (T k + 127 E rows, rounded up to 128) and not the segments.
+// The host sees how many rows there are and not the segments: a capacity (T k + 127 E rows, rounded up to 128), or the rows
+// in use, all of which may carry tokens.  Where the former would leave next to none, T tokens still have a row each (64 full
+// segments of 128 rows, 2048 x 7168: 1080 us where the waves split K, 205 by 128 x 128 tiles; 8 such: 136 and 38).
 //  - Gathered rows, up to 2 an expert on average, or up to 16 and so few 128 x 128 tiles that they leave CUs idle: the waves
 //    split K.  Measured, top-8 (split K / 128 x 128 tiles): 64 experts of 2048 x 7168, one token 25 / 38 us, 4 tokens 83 / 79,
 //    32 tokens 198 / 177; 64 of 7168 x 2048, one token 40 / 37; 256 of them, one token 80 / 153; 8 experts of 2048 x 7168,
@@ -689,7 +691,8 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t K) {
 //  - Else 256 x 256 tiles.
 template <bool GATHER>
 hipError_t launch_int8_grouped(const Int8Args &p, bool out_bf16, hipStream_t stream) {
-    const int64_t rows = p.M > 127 * p.E + 64 ? p.M - 127 * p.E - 64 : 0;
+    int64_t rows = p.M > 127 * p.E + 64 ? p.M - 127 * p.E - 64 : 0;
+    if (GATHER && rows < p.T) rows = p.T < p.M ? p.T : p.M;
     const int64_t ncu = cu_count(), KB = (p.K + 127) / 128;
     auto tiles = [](int64_t n, int64_t t) { return (n + t - 1) / t; };
     if constexpr (GATHER) {

@@ -228,6 +228,26 @@ def test_rows_in_place_read_the_weights_about_once(T, E, N, K):
     assert place < 2.5 * gather
 
 
+def test_gathered_full_segments_read_the_weights_about_once():
+    """A layout cut to the rows in use, every one with a token: the gathered product is the one with rows in place, bit for
+    bit, and takes at most 2.5 times as long."""
+    E, N, K, T = 64, 2048, 2064, 1024
+    g = torch.Generator(device="cuda").manual_seed(46)
+    row_token = torch.cat([torch.randperm(T, device="cuda", generator=g)[:128] for _ in range(E)]).int()
+    off = torch.arange(E + 1, dtype=torch.int32, device="cuda") * 128
+    q = torch.randint(-127, 128, (T, K), device="cuda", dtype=torch.int8, generator=g)
+    qw = torch.randint(-127, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=g)
+    s, sw = torch.rand(T, device="cuda", generator=g), torch.rand((E, N), device="cuda", generator=g)
+    qa, sa = q[row_token.long()], s[row_token.long()]
+    say("int8 gather, full segments")
+    a = fq.fp8q_grouped_gemm_int8(qa, sa, qw, sw, off)
+    b = fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, off)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    place = call_time(lambda: fq.fp8q_grouped_gemm_int8(qa, sa, qw, sw, off, c=a))
+    gather = call_time(lambda: fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, off, c=b))
+    assert gather < 2.5 * place
+
+
 def grouped_layout(T, E, k, N, K):
     """Layout, tokens and weights without the expected result (sizes at which the host would take long)."""
     rng = np.random.default_rng([55, T, E])
@@ -316,6 +336,29 @@ def test_gather_from_the_largest_token_array(used):
     at = row_token[:used].long()
     want = ref.gemm_int8(host(q[at]), host(s[at]), host(qw[0]), host(sw[0]))
     assert np.array_equal(host(c[:used]), want) and (host(c[used:]) == 0).all()
+
+
+def test_gather_of_few_rows_from_the_largest_token_array():
+    """The same by the kernel of few rows, which more experts than half the tokens make the choice: 8200 experts, three of
+    them with tokens, T * K = 2^31 - 131088, K at its largest."""
+    T, K, N, E = 16385, 131056, 8, 8200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(47)
+    q = torch.randint(-127, 128, (T, K), device="cuda", dtype=torch.int8, generator=g)
+    s, sw = torch.rand(T, device="cuda", generator=g), torch.rand((E, N), device="cuda", generator=g)
+    qw = torch.randint(-127, 128, (E, N, K), device="cuda", dtype=torch.int8, generator=g)  # 8.6 GB
+    row_token = torch.full((384,), -1, dtype=torch.int32, device="cuda")
+    used = {0: (0, [T - 1, 0, 8192]), 4321: (128, [T - 2] * 17), E - 1: (256, [12345, T - 1])}
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    for e, (r, tokens) in used.items():
+        row_token[r:r + len(tokens)] = torch.tensor(tokens, dtype=torch.int32, device="cuda")
+        off[e + 1:] = r + 128
+    say(f"int8 gather of few rows at T * K = {T * K}")
+    c = fq.fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, off, out_dtype=torch.float32)
+    for e, (r, tokens) in used.items():
+        want = ref.gemm_int8(host(q[tokens]), host(s[tokens]), host(qw[e]), host(sw[e]))
+        assert np.array_equal(host(c[r:r + len(tokens)]), want)
+    assert (host(c)[host(row_token) < 0] == 0).all()
 
 
 def test_int8_wants_its_arguments_right():
