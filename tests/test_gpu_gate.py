@@ -179,6 +179,67 @@ def test_gate_repeats_bit_for_bit_and_agrees_over_batch_sizes():
     assert np.array_equal(a[0][100:117], one[0]) and np.array_equal(a[1][100:117], one[1])
 
 
+MANY = [  # T, E, k, score, bias, groups, renorm, scale, dtype: past 4096 tokens with E % 4 == 0, 16 lanes a token
+    (5000, 256, 8, "sigmoid", True, (8, 4, 2), True, 2.5, "f32"),    # 16 experts a lane, logits and bias as vectors
+    (4200, 256, 8, "sigmoid", True, (8, 4, 2), True, 2.5, "bf16"),
+    (4300, 512, 16, "softmax", True, (1, 1, 2), False, 1.0, "bf16"),  # 32
+    (4097, 512, 8, "softmax", True, (8, 3, 1), True, 1.0, "f32"),
+    (4500, 160, 6, "softmax", False, (8, 3, 1), True, 1.0, "f32"),   # 20 experts a group: 16 a lane, no vectors
+    (4123, 64, 6, "softmax", True, (1, 1, 1), True, 1.0, "f32"),     # 4
+    (4444, 12, 3, "sigmoid", True, (3, 2, 2), False, 1.5, "bf16"),   # 1
+    (4100, 1024, 9, "sigmoid", True, (16, 5, 2), True, 1.0, "f32"),  # 64 experts a lane would be too many: 64 lanes a token
+]
+
+
+def many(T, E, k, kind, bias, groups, dt):
+    """Logits of T tokens, the sampled ones (32 of them, the first and the last too) decided, and the bias."""
+    rng = np.random.default_rng([14, T, E])
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    b = (0.05 * rng.standard_normal(E)).astype(np.float32) if bias else None
+    at = np.sort(np.concatenate([[0, T - 1], 1 + rng.choice(T - 2, 30, replace=False)]))
+    x = 1.5 * rng.standard_normal((T, E)).astype(np.float32)
+    x = torch.from_numpy(x).to(dtype).float().numpy()
+    x[at] = draw(rng, len(at), E, k, kind, b, groups, dtype)
+    return x, b, at, dtype
+
+
+@pytest.mark.parametrize("T,E,k,kind,bias,groups,renorm,scale,dt", MANY)
+def test_many_tokens_against_the_reference(T, E, k, kind, bias, groups, renorm, scale, dt):
+    """Experts and weights of sampled tokens; the layout of all tokens from their experts."""
+    x, b, at, dtype = many(T, E, k, kind, bias, groups, dt)
+    say(f"gate many T={T} E={E} k={k} {kind} groups={groups} {dt}")
+    idx, w, offsets, row_of, row_token, load = call(x, k, dtype, score=kind, bias=b, n_group=groups[0],
+                                                    topk_group=groups[1], group_top=groups[2], renormalize=renorm,
+                                                    scale=scale)
+    for t in at:
+        eidx, ew, _ = ref.gate_token(x[t], k, kind, b, *groups, renorm, scale)
+        assert np.array_equal(idx[t], eidx)
+        assert np.all(np.abs(w[t] - ew) <= W_TOL * np.abs(ew) + 1e-37)
+    assert (idx >= 0).all() and (idx < E).all()
+    eo, er, et, el = ref.layout(idx, E, len(row_token))
+    assert np.array_equal(offsets, eo) and np.array_equal(load, el)
+    assert np.array_equal(row_of, er) and np.array_equal(row_token, et)
+
+
+@pytest.mark.parametrize("T,E,k,kind,bias,groups,renorm,scale,dt", MANY + [
+    (4600, 256, 8, "softmax", True, (8, 4, 2), True, 1.0, "f32"), (4600, 256, 8, "softmax", False, (1, 1, 2), False, 1.0, "bf16")])
+def test_a_tokens_answer_does_not_depend_on_its_batch(T, E, k, kind, bias, groups, renorm, scale, dt):
+    """Bit for bit: many tokens (16 lanes each), batches of hundreds (64 lanes) and few tokens (one launch); masked experts
+    and infinities among them."""
+    x, b, at, dtype = many(T, E, k, kind, bias, groups, dt)
+    x[5, ::3] = -np.inf
+    x[6, 1] = np.inf
+    x[7] = np.nan
+    kw = dict(score=kind, bias=b, n_group=groups[0], topk_group=groups[1], group_top=groups[2], renormalize=renorm,
+              scale=scale)
+    say(f"gate batches T={T} E={E} k={k} {kind} groups={groups} {dt}")
+    whole = call(x, k, dtype, **kw)
+    for a, n in ((0, 1), (0, 32), (3, 33), (100, 700), (T - 50, 50), (T - 31, 31), (0, 4096)):
+        part = call(x[a:a + n], k, dtype, **kw)
+        assert np.array_equal(whole[0][a:a + n], part[0])
+        assert np.array_equal(whole[1][a:a + n].view(np.uint32), part[1].view(np.uint32))
+
+
 @pytest.mark.parametrize("most,E", [(6000, 256), (4097, 64), (33, 8), (5000, 36)])
 def test_a_workspace_made_for_a_batch_does_for_smaller_ones(most, E):
     """Bit for bit the results of a call with a workspace of its own."""
