@@ -25,6 +25,13 @@ this package is its Python binding.  Entry points (same names as the C functions
   fp8q_gemm_int8(qa, sa, qw, sw)               INT8 product with scales per token and channel, bf16 or fp32 [M, N]
   fp8q_grouped_gemm_int8(qa, sa, qw, sw, offsets)            the same per expert segment
   fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets)   the same, reading token rows directly
+  fp8q_rmsnorm_quant_act_1x128(x, w, residual)  bf16 [M, K] -> (E4M3, scales, the sum, rstd) of the root-mean-square norm
+  fp8q_rmsnorm_backward(gy, h, w, rstd, gres)  its gradients: bf16 [M, K] of the input, fp32 [K] of the weight
+  fp8q_transpose_act_128x1(q, s, row_token)    an 8-bit checkpoint's transpose, groups of 128 tokens, power-of-two scales
+  fp8q_quant_act_128x1(x, row_token)           the same copy of bf16 rows (a gradient)
+  fp8q_swiglu_backward_quant(q, s, gh)         SwiGLU's gradient from its 8-bit inputs, quantized both ways
+  fp8q_gemm_wgrad(gt, eg, xt, ex)              a Linear's weight gradient from two such copies, fp32 or bf16 [N, K]
+  fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, offsets)   every expert's, [E, N, K]
 """
 from ._binding import (  # noqa: F401
     OUT_BF16,
@@ -32,11 +39,13 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     fp8q_dequant_w_128x128,
     fp8q_gemm_blockscaled,
+    fp8q_gemm_wgrad,
     fp8q_grouped_gemm_blockscaled,
     fp8q_grouped_gemm_blockscaled_gather,
     fp8q_gemm_int8,
     fp8q_grouped_gemm_int8,
     fp8q_grouped_gemm_int8_gather,
+    fp8q_grouped_gemm_wgrad,
     fp8q_moe_combine,
     fp8q_moe_combine_backward,
     fp8q_moe_gate_backward,
@@ -45,6 +54,7 @@ from ._binding import (  # noqa: F401
     fp8q_moe_route_capacity,
     fp8q_moe_route_topk,
     fp8q_moe_route_topk_noalloc,
+    fp8q_quant_act_128x1,
     fp8q_quant_act_1x128,
     fp8q_quant_act_dual,
     fp8q_quant_act_e5m6_1x128,
@@ -53,8 +63,12 @@ from ._binding import (  # noqa: F401
     fp8q_quant_w_128x128,
     fp8q_quant_w_fp4_128x128,
     fp8q_quant_w_per_channel,
+    fp8q_rmsnorm_backward,
+    fp8q_rmsnorm_quant_act_1x128,
+    fp8q_swiglu_backward_quant,
     fp8q_swiglu_bf16,
     fp8q_swiglu_quant_act_1x128,
+    fp8q_transpose_act_128x1,
     load_library,
     status_string,
 )

@@ -65,6 +65,21 @@ def load_library(path: str = LIB_PATH):
         lib.fp8q_gemm_int8.argtypes = [P, P, P, P, P, I, I64, I64, I64, P]
         lib.fp8q_grouped_gemm_int8.argtypes = [P, P, P, P, P, I, P, I64, I64, I64, I64, P]
         lib.fp8q_grouped_gemm_int8_gather.argtypes = [P, P, I64, P, P, P, P, I, P, I64, I64, I64, I64, P]
+        lib.fp8q_rmsnorm_quant_act_1x128.argtypes = [P, I64, P, I64, P, I, F, I, I64, I64, P, P, P, P, P, P]
+        lib.fp8q_rmsnorm_backward.argtypes = [P, I64, P, I64, P, I, P, P, I64, I64, P, P, P, I64, P]
+        lib.fp8q_transpose_act_128x1.argtypes = [P, P, I64, I64, P, I64, P, P, P]
+        lib.fp8q_quant_act_128x1.argtypes = [P, I64, I64, I64, P, I64, P, P, P]
+        lib.fp8q_swiglu_backward_quant.argtypes = [P, P, P, I64, I64, I64, P, P, P, P, P, P, P]
+        lib.fp8q_gemm_wgrad.argtypes = [P, P, P, P, P, I, I, I64, I64, I64, P, I64, P]
+        lib.fp8q_grouped_gemm_wgrad.argtypes = [P, P, P, P, P, I, I, P, I64, I64, I64, I64, P]
+        for f in (lib.fp8q_rmsnorm_quant_act_1x128, lib.fp8q_rmsnorm_backward, lib.fp8q_transpose_act_128x1,
+                  lib.fp8q_quant_act_128x1, lib.fp8q_swiglu_backward_quant, lib.fp8q_gemm_wgrad,
+                  lib.fp8q_grouped_gemm_wgrad):
+            f.restype = ctypes.c_int
+        lib.fp8q_rmsnorm_backward_workspace_bytes.argtypes = [I64, I64]
+        lib.fp8q_rmsnorm_backward_workspace_bytes.restype = I64
+        lib.fp8q_gemm_wgrad_workspace_bytes.argtypes = [I64, I64, I64, I]
+        lib.fp8q_gemm_wgrad_workspace_bytes.restype = I64
         for f in (lib.fp8q_moe_gate_topk, lib.fp8q_moe_gate_backward, lib.fp8q_moe_combine,
                   lib.fp8q_moe_combine_backward, lib.fp8q_quant_int8, lib.fp8q_gemm_int8, lib.fp8q_grouped_gemm_int8,
                   lib.fp8q_grouped_gemm_int8_gather):
@@ -789,3 +804,262 @@ def fp8q_grouped_gemm_int8_gather(q, s, row_token, qw, sw, offsets, out_dtype=to
         _ptr(q), _ptr(s), T, _ptr(row_token), _ptr(qw), _ptr(sw), _ptr(c), code, _ptr(offsets), E, M, N, K,
         _stream_ptr(stream)), "fp8q_grouped_gemm_int8_gather")
     return c
+
+
+# The operators below launch on the current device: their tensors have to be there.
+def _here(t, name, dtypes, ndim, device):
+    """A device tensor of one of the dtypes on ``device`` (an index), rows contiguous; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device cuda:{device}, is on {t.device}")
+    if t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims and a dtype of {dtypes}, got {t.dim()} and {t.dtype}")
+    if t.is_contiguous():
+        return t.shape[-1]
+    if ndim != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _here_flat(t, name, dtypes, size, device):
+    """A contiguous device tensor on ``device`` of a given number of elements."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == device and t.numel() == size and \
+            t.is_contiguous():
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device cuda:{device}, is on {t.device}")
+    _need(t, name, dtypes)
+    raise ValueError(f"{name} has {t.numel()} elements; expected {size}")
+
+
+def _workspace_of(workspace, need, stream, device, index):
+    """The caller's workspace, or one of this call's (None where nothing is needed)."""
+    if need < 0:
+        raise ValueError("invalid sizes")
+    if workspace is None:
+        return (_scratch(stream, need, device), need) if need > 0 else (None, 0)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+def fp8q_rmsnorm_quant_act_1x128(x, w, residual=None, eps: float = 1e-6, pow2: bool = False, h=None, q=None, s=None,
+                                 rstd=None, y=None, stream=None):
+    """Root-mean-square norm of ``x`` (+ ``residual``), quantized in 1x128 groups.  ``x`` and ``residual`` bf16 [M, K]
+    (rows may be strided), ``w`` bf16 or float32 [K] -> ``(q uint8 [M, K], s float32 [K/128, M], h bf16 [M, K], rstd
+    float32 [M])``: ``h = bf16(x + residual)`` (``x`` itself without a residual), ``rstd = 1 / sqrt(mean(h^2) + eps)``,
+    and the codes and scales of ``h * rstd * w``.  ``pow2`` makes every scale a power of two (a transposed copy of such a
+    checkpoint keeps its values).  ``h`` may be ``x`` or ``residual``, to update it in place; ``y``, a bf16 [M, K] tensor,
+    also receives the normed rows in bf16.  Outputs not given are allocated."""
+    dev = _GET_DEVICE()
+    ldx = _here(x, "x", (torch.bfloat16,), 2, dev)
+    M, K = x.shape
+    if w.dtype not in _FLOAT:
+        raise ValueError(f"w must be bf16 or float32, got {w.dtype}")
+    _here_flat(w, "w", _FLOAT, K, dev)
+    ldr = 0
+    if residual is not None:
+        ldr = _here(residual, "residual", (torch.bfloat16,), 2, dev)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        if h is None:
+            h = _empty(stream, (M, K), dtype=torch.bfloat16, device=x.device)
+        _here_flat(h, "h", (torch.bfloat16,), M * K, dev)
+    elif h is not None:
+        raise ValueError("h is written with a residual only")
+    if q is None:
+        q = _empty(stream, (M, K), dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = _empty(stream, (K // 128, M), dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = _empty(stream, (M,), dtype=torch.float32, device=x.device)
+    _here_flat(q, "q", _FP8, M * K, dev)
+    _here_flat(s, "s", _F32, (K // 128) * M, dev)
+    _here_flat(rstd, "rstd", _F32, M, dev)
+    if y is not None:
+        _here_flat(y, "y", (torch.bfloat16,), M * K, dev)
+    _check(load_library().fp8q_rmsnorm_quant_act_1x128(
+        x.data_ptr(), ldx, _ptr(residual), ldr, w.data_ptr(), OUT_BF16 if w.dtype is torch.bfloat16 else OUT_F32, eps,
+        1 if pow2 else 0, M, K, _ptr(h), _ptr(y), q.data_ptr(), s.data_ptr(), rstd.data_ptr(), _stream_ptr(stream)),
+        "fp8q_rmsnorm_quant_act_1x128")
+    return q, s, x if h is None else h, rstd
+
+
+def fp8q_rmsnorm_backward(gy, h, w, rstd, gres=None, gx=None, gw=None, workspace=None, stream=None):
+    """Gradients of the norm (the quantization is passed straight through).  ``gy`` and ``h`` bf16 [M, K] (rows may be
+    strided), ``w`` bf16 or float32 [K], ``rstd`` float32 [M] (the forward call's), ``gres`` bf16 [M, K], the gradient that
+    reaches ``h`` past the norm, or None -> ``(gx bf16 [M, K], gw float32 [K])``; ``gx`` is the gradient of ``x`` and of the
+    residual alike, and may be ``gres`` or ``gy``.  ``workspace``
+    (``fp8q_rmsnorm_backward_workspace_bytes(M, K)`` bytes) is allocated when not given."""
+    dev = _GET_DEVICE()
+    ldg = _here(gy, "gy", (torch.bfloat16,), 2, dev)
+    ldh = _here(h, "h", (torch.bfloat16,), 2, dev)
+    M, K = gy.shape
+    if h.shape != gy.shape:
+        raise ValueError("h must have gy's shape")
+    _here_flat(w, "w", _FLOAT, K, dev)
+    _here_flat(rstd, "rstd", _F32, M, dev)
+    if gres is not None:
+        _here_flat(gres, "gres", (torch.bfloat16,), M * K, dev)
+    if gx is None:
+        gx = _empty(stream, (M, K), dtype=torch.bfloat16, device=gy.device)
+    if gw is None:
+        gw = _empty(stream, (K,), dtype=torch.float32, device=gy.device)
+    _here_flat(gx, "gx", (torch.bfloat16,), M * K, dev)
+    _here_flat(gw, "gw", _F32, K, dev)
+    lib = load_library()
+    workspace, nbytes = _workspace_of(workspace, lib.fp8q_rmsnorm_backward_workspace_bytes(M, K), stream, gy.device, dev)
+    _check(lib.fp8q_rmsnorm_backward(gy.data_ptr(), ldg, h.data_ptr(), ldh, w.data_ptr(),
+                                     OUT_BF16 if w.dtype is torch.bfloat16 else OUT_F32, rstd.data_ptr(), _ptr(gres), M,
+                                     K, gx.data_ptr(), gw.data_ptr(), _ptr(workspace), nbytes, _stream_ptr(stream)),
+           "fp8q_rmsnorm_backward")
+    return gx, gw
+
+
+def _copy_outputs(row_token, T, K, qt, et, stream, device, index):
+    rows = T
+    if row_token is not None:
+        _here(row_token, "row_token", _I32, 1, index)
+        rows = row_token.numel()
+    nb = (rows + 127) // 128
+    if qt is None:
+        qt = _empty(stream, (K, nb * 128), dtype=torch.uint8, device=device)
+    if et is None:
+        et = _empty(stream, (nb, K), dtype=torch.uint8, device=device)
+    _here_flat(qt, "qt", _FP8, K * nb * 128, index)
+    _here_flat(et, "et", _U8, nb * K, index)
+    return rows, qt, et
+
+
+def fp8q_transpose_act_128x1(q, s, row_token=None, qt=None, et=None, stream=None):
+    """The backward copy of an 8-bit checkpoint: its transpose in groups of 128 tokens with power-of-two scales.  ``q``
+    E4M3 [T, K], ``s`` float32 [K/128, T] -> ``(qt uint8 [K, Mp], et uint8 [Mp/128, K])``, Mp the rows rounded up to 128
+    (columns past them hold zeros) and ``2 ** (et - 127)`` the scales.  ``row_token`` int32 [rows] picks each row's token
+    (outside [0, T): zeros), as the expert-sorted layouts give it; without it row r is token r."""
+    dev = _GET_DEVICE()
+    _need(q, "q", _FP8, 2)
+    _here(q, "q", _FP8, 2, dev)
+    T, K = q.shape
+    _here_flat(s, "s", _F32, (K // 128) * T, dev)
+    rows, qt, et = _copy_outputs(row_token, T, K, qt, et, stream, q.device, dev)
+    _check(load_library().fp8q_transpose_act_128x1(q.data_ptr(), s.data_ptr(), T, K, _ptr(row_token), rows, qt.data_ptr(),
+                                                   et.data_ptr(), _stream_ptr(stream)), "fp8q_transpose_act_128x1")
+    return qt, et
+
+
+def fp8q_quant_act_128x1(x, row_token=None, qt=None, et=None, stream=None):
+    """:func:`fp8q_transpose_act_128x1` of bf16 rows ``x`` [T, K] (which may be strided): a gradient, or an input that was
+    kept in bf16."""
+    dev = _GET_DEVICE()
+    ld = _here(x, "x", (torch.bfloat16,), 2, dev)
+    T, K = x.shape
+    rows, qt, et = _copy_outputs(row_token, T, K, qt, et, stream, x.device, dev)
+    _check(load_library().fp8q_quant_act_128x1(x.data_ptr(), ld, T, K, _ptr(row_token), rows, qt.data_ptr(),
+                                               et.data_ptr(), _stream_ptr(stream)), "fp8q_quant_act_128x1")
+    return qt, et
+
+
+def fp8q_swiglu_backward_quant(q, s, gh, out=None, stream=None):
+    """SwiGLU's gradient from the 8-bit checkpoint of its inputs, quantized for both backward products.  ``q`` E4M3
+    [M, 2F] (gate columns, then up columns), ``s`` float32 [2F/128, M], ``gh`` bf16 [M, F] (rows may be strided), the
+    gradient of the output h -> ``(gq uint8 [M, 2F], gs float32 [2F/128, M], gqt uint8 [2F, Mp], get uint8 [Mp/128, 2F],
+    hqt uint8 [F, Mp], het uint8 [Mp/128, F])``: the inputs' gradients in 1x128 groups, their backward copy, and the
+    backward copy of the recomputed h."""
+    dev = _GET_DEVICE()
+    _need(q, "q", _FP8, 2)
+    _here(q, "q", _FP8, 2, dev)
+    M, F2 = q.shape
+    if F2 % 256:
+        raise ValueError("q must hold gate and up columns, each a multiple of 128")
+    F = F2 // 2
+    _here_flat(s, "s", _F32, (F2 // 128) * M, dev)
+    ldg = _here(gh, "gh", (torch.bfloat16,), 2, dev)
+    if gh.shape != (M, F):
+        raise ValueError(f"gh must have shape {(M, F)}, got {tuple(gh.shape)}")
+    nb = (M + 127) // 128
+    if out is None:
+        u8 = dict(dtype=torch.uint8, device=q.device)
+        out = (_empty(stream, (M, F2), **u8), _empty(stream, (F2 // 128, M), dtype=torch.float32, device=q.device),
+               _empty(stream, (F2, nb * 128), **u8), _empty(stream, (nb, F2), **u8), _empty(stream, (F, nb * 128), **u8),
+               _empty(stream, (nb, F), **u8))
+    gq, gs, gqt, get, hqt, het = out
+    _here_flat(gq, "gq", _FP8, M * F2, dev)
+    _here_flat(gs, "gs", _F32, (F2 // 128) * M, dev)
+    _here_flat(gqt, "gqt", _FP8, F2 * nb * 128, dev)
+    _here_flat(get, "get", _U8, nb * F2, dev)
+    _here_flat(hqt, "hqt", _FP8, F * nb * 128, dev)
+    _here_flat(het, "het", _U8, nb * F, dev)
+    _check(load_library().fp8q_swiglu_backward_quant(
+        q.data_ptr(), s.data_ptr(), gh.data_ptr(), ldg, M, F, gq.data_ptr(), gs.data_ptr(), gqt.data_ptr(),
+        get.data_ptr(), hqt.data_ptr(), het.data_ptr(), _stream_ptr(stream)), "fp8q_swiglu_backward_quant")
+    return gq, gs, gqt, get, hqt, het
+
+
+def _wgrad_operands(gt, eg, xt, ex, dev):
+    for t, n in ((gt, "gt"), (xt, "xt")):
+        _need(t, n, _FP8, 2)
+        _here(t, n, _FP8, 2, dev)
+    N, M = gt.shape
+    K = xt.shape[0]
+    if xt.shape[1] != M or M % 128:
+        raise ValueError("gt and xt must have the same number of columns, a multiple of 128")
+    _here_flat(eg, "eg", _U8, (M // 128) * N, dev)
+    _here_flat(ex, "ex", _U8, (M // 128) * K, dev)
+    return M, N, K
+
+
+def _wgrad_output(dw, shape, out_dtype, accumulate, stream, device, index):
+    code = _out_code(out_dtype)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw, the gradient to add to")
+        dw = _empty(stream, shape, dtype=out_dtype, device=device)
+    size = 1
+    for n in shape:
+        size *= n
+    _here_flat(dw, "dw", (out_dtype,), size, index)
+    return code, dw
+
+
+def fp8q_gemm_wgrad(gt, eg, xt, ex, out_dtype=torch.float32, accumulate: bool = False, dw=None, workspace=None,
+                    stream=None):
+    """A Linear's weight gradient ``dW = dY^T x`` from the backward copies of dY and x (:func:`fp8q_transpose_act_128x1`,
+    :func:`fp8q_quant_act_128x1`, :func:`fp8q_swiglu_backward_quant`).  ``gt`` E4M3 [N, M], ``eg`` uint8 [M/128, N], ``xt``
+    E4M3 [K, M], ``ex`` uint8 [M/128, K] (M a multiple of 128; N and K of 16) -> ``dw`` [N, K] in ``out_dtype``, added to
+    what ``dw`` holds with ``accumulate``.  ``workspace``
+    (``fp8q_gemm_wgrad_workspace_bytes(M, N, K, out_dtype code)`` bytes) is allocated when not given."""
+    dev = _GET_DEVICE()
+    M, N, K = _wgrad_operands(gt, eg, xt, ex, dev)
+    code, dw = _wgrad_output(dw, (N, K), out_dtype, accumulate, stream, gt.device, dev)
+    lib = load_library()
+    workspace, nbytes = _workspace_of(workspace, lib.fp8q_gemm_wgrad_workspace_bytes(M, N, K, code), stream, gt.device, dev)
+    _check(lib.fp8q_gemm_wgrad(gt.data_ptr(), eg.data_ptr(), xt.data_ptr(), ex.data_ptr(), dw.data_ptr(), code,
+                               1 if accumulate else 0, M, N, K, _ptr(workspace), nbytes, _stream_ptr(stream)),
+           "fp8q_gemm_wgrad")
+    return dw
+
+
+def fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, offsets, out_dtype=torch.float32, accumulate: bool = False, dw=None,
+                            stream=None):
+    """:func:`fp8q_gemm_wgrad` for every expert of an expert-sorted layout: ``dw`` [E, N, K], expert e's from the columns
+    ``[offsets[e], offsets[e + 1])`` of the copies.  ``offsets`` int32 device [E+1]; an empty expert's gradient is 0 (or
+    stays, with ``accumulate``)."""
+    dev = _GET_DEVICE()
+    M, N, K = _wgrad_operands(gt, eg, xt, ex, dev)
+    _here(offsets, "offsets", _I32, 1, dev)
+    E = offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets must have E + 1 elements, E at least 1")
+    code, dw = _wgrad_output(dw, (E, N, K), out_dtype, accumulate, stream, gt.device, dev)
+    _check(load_library().fp8q_grouped_gemm_wgrad(
+        gt.data_ptr(), eg.data_ptr(), xt.data_ptr(), ex.data_ptr(), dw.data_ptr(), code, 1 if accumulate else 0,
+        offsets.data_ptr(), E, M, N, K, _stream_ptr(stream)), "fp8q_grouped_gemm_wgrad")
+    return dw

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_moe.hip", "fp8q_gate.hip", "fp8q_combine.hip",
-           "fp8q_int8.hip"]
+           "fp8q_int8.hip", "fp8q_norm.hip", "fp8q_checkpoint.hip", "fp8q_wgrad.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -48,6 +48,7 @@ constexpr int64_t kMaxK = int64_t(1) << 23;  // GEMM tiles address 256 rows of K
 constexpr int64_t kMaxGrid256 = 0xFFFFFFFFll / 256, kMaxGrid512 = 0xFFFFFFFFll / 512;
 constexpr int64_t kMaxGateTokens = 0xFFFFFFFFll / 64;  // 64 lanes a token at most
 
+constexpr int64_t kMaxNormRows = int64_t(1) << 22;  // a workgroup of up to 1024 threads a row
 constexpr int64_t kMaxInt8K = 131056;        // INT8 sums of products of codes down to -128 stay below 2^31
 
 int finish(hipError_t e) { return e == hipSuccess ? FP8Q_OK : FP8Q_ERR_HIP; }
@@ -477,6 +478,140 @@ int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, co
                                                  reinterpret_cast<const uint8_t *>(qw), sw, c,
                                                  out_dtype == FP8Q_OUT_BF16, off, E, M_total, N, K,
                                                  static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const void *w,
+                                 int w_dtype, float eps, int pow2, int64_t M, int64_t K, uint16_t *h, uint16_t *y,
+                                 uint8_t *q, float *s, float *rstd, void *stream) {
+    if (M < 0 || M >= kMaxNormRows || K < 0 || K > 0x7FFFFFFF || K % 128 || ldx < K || ldx % 8 ||
+        (residual && (ldr < K || ldr % 8)))
+        return FP8Q_ERR_SHAPE;
+    if (w_dtype != FP8Q_OUT_BF16 && w_dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;
+    if (!(eps > 0.0f && eps <= 3.402823466e38f) || (pow2 != 0 && pow2 != 1)) return FP8Q_ERR_OPTION;
+    if (M == 0 || K == 0) return FP8Q_OK;
+    if (!x || !w || !q != !s || (residual && !h) || (!q && !y && !rstd && !h)) return FP8Q_ERR_NULL;
+    if (!residual && h) return FP8Q_ERR_OPTION;  // there is no sum to write
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
+        !aligned4(s) || !aligned4(rstd))
+        return FP8Q_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(fp8q::launch_rmsnorm_quant_act_1x128(x, ldx, residual, ldr, w, w_dtype == FP8Q_OUT_BF16, eps,
+                                                       pow2 != 0, M, K, h, y, q, s, rstd,
+                                                       static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) {
+    if (M < 0 || M >= kMaxNormRows || K < 0 || K % 128 || K > fp8q::kMaxNormGradK) return -1;
+    return fp8q::rmsnorm_backward_workspace_bytes(M, K);
+}
+
+int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w, int w_dtype,
+                          const float *rstd, const uint16_t *gres, int64_t M, int64_t K, uint16_t *gx, float *gw,
+                          void *workspace, int64_t workspace_bytes, void *stream) {
+    const int64_t need = fp8q_rmsnorm_backward_workspace_bytes(M, K);
+    if (need < 0 || ldg < K || ldg % 8 || ldh < K || ldh % 8) return FP8Q_ERR_SHAPE;
+    if (w_dtype != FP8Q_OUT_BF16 && w_dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;
+    if (K == 0 || (M == 0 && !gw)) return FP8Q_OK;
+    if (M > 0 && (!gy || !h || !w || !rstd || !gx || (gw && !workspace))) return FP8Q_ERR_NULL;
+    if (!aligned16(gy) || !aligned16(h) || !aligned16(w) || !aligned4(rstd) || !aligned16(gres) || !aligned16(gx) ||
+        !aligned16(gw) || !aligned16(workspace))
+        return FP8Q_ERR_ALIGN;
+    if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(fp8q::launch_rmsnorm_backward(gy, ldg, h, ldh, w, w_dtype == FP8Q_OUT_BF16, rstd, gres, M, K, gx, gw,
+                                                static_cast<float *>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+// Tiles of 128 x 128, or -1 where there are 2^23 and more.
+static int64_t square_tiles(int64_t rows, int64_t K) {
+    const int64_t mt = (rows + 127) / 128, kt = K / 128;
+    if (mt > 0 && kt >= (kMaxGrid512 + mt) / mt) return -1;
+    return mt * kt < kMaxGrid512 ? mt * kt : -1;
+}
+
+static int transpose_128x1(const void *x, const float *s, bool codes, int64_t ld, int64_t T, int64_t K,
+                           const int32_t *row_token, int64_t rows, uint8_t *qt, uint8_t *et, void *stream) {
+    if (T < 0 || T > 0x7FFFFFFF || rows < 0 || rows > 0x7FFFFFFF || K < 0 || K % 128 || (!row_token && rows != T && rows != 0) ||
+        ld < K || ld % 8 || square_tiles(rows, K) < 0)
+        return FP8Q_ERR_SHAPE;
+    if (rows == 0 || K == 0) return FP8Q_OK;
+    if ((T > 0 && (!x || (codes && !s))) || !qt || !et) return FP8Q_ERR_NULL;
+    if (!aligned16(x) || !aligned4(s) || !aligned4(row_token) || !aligned16(qt)) return FP8Q_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(fp8q::launch_transpose_128x1(x, s, codes, ld, T, K, row_token, rows, qt, et,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_transpose_act_128x1(const uint8_t *q, const float *s, int64_t T, int64_t K, const int32_t *row_token,
+                             int64_t rows, uint8_t *qt, uint8_t *et, void *stream) {
+    return transpose_128x1(q, s, true, K, T, K, row_token, rows, qt, et, stream);
+}
+
+int fp8q_quant_act_128x1(const uint16_t *x, int64_t ld, int64_t T, int64_t K, const int32_t *row_token, int64_t rows,
+                         uint8_t *qt, uint8_t *et, void *stream) {
+    return transpose_128x1(x, nullptr, false, ld, T, K, row_token, rows, qt, et, stream);
+}
+
+int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t *gh, int64_t ldg, int64_t M, int64_t F,
+                               uint8_t *gq, float *gs, uint8_t *gqt, uint8_t *get, uint8_t *hqt, uint8_t *het,
+                               void *stream) {
+    if (M < 0 || M > 0x7FFFFFFF || F < 0 || F % 128 || ldg < F || ldg % 8 || square_tiles(M, F) < 0)
+        return FP8Q_ERR_SHAPE;
+    if (M == 0 || F == 0) return FP8Q_OK;
+    if (!q || !s || !gh || !gq || !gs || !gqt || !get || !hqt || !het) return FP8Q_ERR_NULL;
+    if (!aligned16(q) || !aligned4(s) || !aligned16(gh) || !aligned16(gq) || !aligned4(gs) || !aligned16(gqt) ||
+        !aligned16(get) || !aligned16(hqt) || !aligned16(het))
+        return FP8Q_ERR_ALIGN;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(fp8q::launch_swiglu_backward_quant(q, s, gh, ldg, M, F, gq, gs, gqt, get, hqt, het,
+                                                     static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
+    if (M < 0 || M % 128 || M > kMaxK || N < 0 || N % 16 || K < 0 || K % 16) return -1;
+    if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_F32) return -1;
+    const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, 1);
+    if (blocks < 0 || blocks > kMaxGrid512) return -1;
+    return fp8q::gemm_wgrad_workspace_bytes(M, N, K, out_dtype == FP8Q_OUT_BF16);
+}
+
+static int wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
+                 int accumulate, bool grouped, const int32_t *off, int64_t E, int64_t M, int64_t N, int64_t K,
+                 void *workspace, int64_t workspace_bytes, void *stream) {
+    if (E < 1 || E > 0x7FFFFFFF || M < 0 || M % 128 || M > kMaxK || N < 0 || N % 16 || K < 0 || K % 16)
+        return FP8Q_ERR_SHAPE;
+    const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, E);
+    if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;
+    if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;
+    if (accumulate != 0 && accumulate != 1) return FP8Q_ERR_OPTION;
+    if (N == 0 || K == 0 || (M == 0 && accumulate)) return FP8Q_OK;
+    const int64_t need = grouped ? 0 : fp8q::gemm_wgrad_workspace_bytes(M, N, K, out_dtype == FP8Q_OUT_BF16);
+    if (!dw || (M > 0 && (!gt || !eg || !xt || !ex)) || (grouped && !off) || (need > 0 && !workspace))
+        return FP8Q_ERR_NULL;
+    if (!aligned16(gt) || !aligned16(eg) || !aligned16(xt) || !aligned16(ex) || !aligned16(dw) || !aligned4(off) ||
+        !aligned16(workspace))
+        return FP8Q_ERR_ALIGN;
+    if (workspace_bytes < need) return FP8Q_ERR_WORKSPACE;
+    int rc = check_device();
+    if (rc) return rc;
+    return finish(fp8q::launch_gemm_wgrad(gt, eg, xt, ex, dw, out_dtype == FP8Q_OUT_BF16, accumulate != 0, off, E, M, N,
+                                          K, static_cast<float *>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+int fp8q_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
+                    int accumulate, int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
+                    void *stream) {
+    return wgrad(gt, eg, xt, ex, dw, out_dtype, accumulate, false, nullptr, 1, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int fp8q_grouped_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw,
+                            int out_dtype, int accumulate, const int32_t *off, int64_t E, int64_t M_total, int64_t N,
+                            int64_t K, void *stream) {
+    return wgrad(gt, eg, xt, ex, dw, out_dtype, accumulate, true, off, E, M_total, N, K, nullptr, 0, stream);
 }
 
 }  // extern "C"

@@ -102,6 +102,19 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     return (uint32_t)r;
 }
 
+// Power-of-two scales as E8M0 bytes (value 2^(byte - 127)).  The byte of a group whose largest magnitude has the fp32
+// pattern `amax`: the least power p with amax <= 448 p, at least 2^-127; 448 = 1.75 * 2^8.  An all-zero group gets 0.
+__device__ __forceinline__ uint32_t pow2_byte(uint32_t amax) {
+    const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return (uint32_t)(e < 0 ? 0 : e);
+}
+// The power itself, and its reciprocal (both exact in fp32 for bytes up to 248, the largest of a finite group; 2^-127 is
+// subnormal).
+__device__ __forceinline__ float pow2_value(uint32_t byte) {
+    return __uint_as_float(byte > 0 ? byte << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float pow2_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
 // Quantize the 4 bf16 values of two packed dwords to 4 codes (element order preserved).
 __device__ __forceinline__ uint32_t quant4(uint32_t d0, uint32_t d1, double inv_s) {
     return encode4(quotient(bf16_lo(d0), inv_s), quotient(bf16_hi(d0), inv_s), quotient(bf16_lo(d1), inv_s),

@@ -84,6 +84,32 @@ hipError_t launch_grouped_gemm_int8(const uint8_t *qa, const float *sa, int64_t 
                                     int64_t E, int64_t M_total, int64_t N, int64_t K, hipStream_t stream);
 // Upper bound on the workgroups of an INT8 product (E == 0: dense); -1 past 2^40.
 int64_t gemm_int8_blocks(int64_t M, int64_t N, int64_t E);
+// Multiprocessor count of the current device (cached).
+int cu_count();
+// The norm in front of an FP8 Linear and its gradients; residual, gres, h, y, q (with s), rstd and gw may be null.
+hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,
+                                          const void *w, bool w_bf16, float eps, bool pow2, int64_t M, int64_t K,
+                                          uint16_t *h, uint16_t *y, uint8_t *q, float *s, float *rstd,
+                                          hipStream_t stream);
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+constexpr int64_t kMaxNormGradK = 20480;
+hipError_t launch_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w,
+                                   bool w_bf16, const float *rstd, const uint16_t *gres, int64_t M, int64_t K,
+                                   uint16_t *gx, float *gw, float *workspace, hipStream_t stream);
+// Transposed copies in groups of 128 tokens with power-of-two scales, from an 8-bit checkpoint (codes and s) or from bf16
+// rows ld elements apart; row_token null: rows == T.
+hipError_t launch_transpose_128x1(const void *x, const float *s, bool codes, int64_t ld, int64_t T, int64_t K,
+                                  const int32_t *row_token, int64_t rows, uint8_t *qt, uint8_t *et, hipStream_t stream);
+hipError_t launch_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t *gh, int64_t ldg, int64_t M,
+                                        int64_t F, uint8_t *gq, float *gs, uint8_t *gqt, uint8_t *get, uint8_t *hqt,
+                                        uint8_t *het, hipStream_t stream);
+// Weight gradients from transposed copies; off null: one product over all M columns (E is 1).
+int64_t gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_bf16);
+// Upper bound on the workgroups of E weight gradients; -1 past 2^40.
+int64_t gemm_wgrad_blocks(int64_t N, int64_t K, int64_t E);
+hipError_t launch_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw,
+                             bool out_bf16, bool accumulate, const int32_t *off, int64_t E, int64_t M, int64_t N,
+                             int64_t K, float *workspace, hipStream_t stream);
 // Number of workgroups the dense GEMM launches for an M x N output (for grid-size validation).
 int64_t gemm_blocks(int64_t M, int64_t N);
 // Number of workgroups a grouped GEMM launches for M rows, N columns and E experts; -1 when that count

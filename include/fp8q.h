@@ -455,6 +455,131 @@ int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, co
                                   const int8_t *qw, const float *sw, void *c, int out_dtype, const int32_t *off,
                                   int64_t E, int64_t M_total, int64_t N, int64_t K, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The norm in front of an FP8 Linear, and the backward pass from 8-bit
+ * checkpoints (page "The Definitive Information To Deepseek", the passage on
+ * caching the Linear's input in FP8 for the backward pass).
+ *
+ * A backward copy of activations or gradients [M, C] is their transpose in
+ * groups of 128 tokens of one channel, whose scales are powers of two:
+ *   qt : E4M3 [C, Mp], Mp = M rounded up to 128; columns from M on hold zeros
+ *   et : uint8 [Mp/128][C], an E8M0 exponent each: the value is 2^(et - 127)
+ *   et[mb][c] = 127 + the least e >= -127 with max_{m in mb} |v[m,c]| <= 448 * 2^e
+ *               (0 where the group is all zeros)
+ *   qt[c,m]   = E4M3_RNE(v[m,c] * 2^(127 - et)).
+ * Multiplying by a power of two is exact, so a checkpoint whose own scales are
+ * powers of two keeps its values in the copy, but for those that fall below
+ * E4M3's normal range.
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm of x (plus a residual), quantized in 1x128 groups:
+ *   h[m,k]  = bf16(x[m,k] + residual[m,k])      (without a residual h is x)
+ *   rstd[m] = 1 / sqrt(sum_k h[m,k]^2 / K + eps)
+ *   y[m,k]  = rstd[m] * h[m,k] * w[k]           (fp32; h * w is exact for bf16 w)
+ *   pow2 0: s[kb][m] = fl32(max_k |y| / 448),  q[m,k] = E4M3_RNE(y / s), the
+ *           quotient formed without the factor rstd, which cancels
+ *   pow2 1: s[kb][m] = the least power of two p >= 2^-127 with max_k |y| <= 448 p,
+ *           q[m,k] = E4M3_RNE(y / s)            (either way s is 0 where y is)
+ *   x        : bf16 [M, K], rows ldx elements apart
+ *   residual : bf16 [M, K], rows ldr elements apart, or NULL
+ *   w        : [K] in w_dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32)
+ *   h        : bf16 [M, K] (output; with a residual only, and then required).  It may
+ *              be x or residual itself when that array is contiguous.
+ *   y        : bf16 [M, K] (output, or NULL) the normed rows rounded to bf16
+ *   q, s     : E4M3 [M, K], fp32 [K/128][M] (outputs, or both NULL)
+ *   rstd     : fp32 [M] (output, or NULL), what fp8q_rmsnorm_backward takes
+ * Requires K % 128 == 0, ldx and ldr >= K and multiples of 8, M < 2^22, a
+ * positive finite eps, sums of squares finite in fp32; rstd and s 4-byte
+ * aligned, the rest to 16 bytes.  fp32 sums in a fixed order.  One launch. */
+int fp8q_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const void *w,
+                                 int w_dtype, float eps, int pow2, int64_t M, int64_t K, uint16_t *h, uint16_t *y,
+                                 uint8_t *q, float *s, float *rstd, void *stream);
+
+/* Bytes of device workspace for fp8q_rmsnorm_backward (never more for fewer
+ * tokens of the same K).  Returns -1 for invalid sizes. */
+int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
+
+/* The norm's gradients (the quantization is passed straight through):
+ *   gx[m,k] = bf16(gres[m,k] + rstd[m] * (gy[m,k] w[k] - h[m,k] rstd[m]^2 mean_k(gy w h)))
+ *   gw[k]   = sum_m gy[m,k] h[m,k] rstd[m]
+ *   gy   : bf16 [M, K], rows ldg elements apart: the gradient of y
+ *   h    : bf16 [M, K], rows ldh elements apart: the normed input (h above)
+ *   rstd : fp32 [M] as the forward call gave it
+ *   gres : bf16 [M, K], contiguous, or NULL: the gradient that reaches h past the norm
+ *   gx   : bf16 [M, K] (output), the gradient of x and of the residual alike; it may
+ *          be gres, or gy when that is contiguous
+ *   gw   : fp32 [K] (output, or NULL, and then no workspace is needed); 0 when M is 0
+ *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, its contents
+ *          on entry do not matter (calls that share one must not overlap)
+ * Requires K % 128 == 0, K <= 20480, ldg and ldh >= K and multiples of 8, M < 2^22.
+ * fp32 arithmetic, sums in a fixed order.  Two launches at most. */
+int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w, int w_dtype,
+                          const float *rstd, const uint16_t *gres, int64_t M, int64_t K, uint16_t *gx, float *gw,
+                          void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Backward copies (above) of an 8-bit checkpoint, and of bf16 rows:
+ *   q : E4M3 [T, K], s : fp32 [K/128][T]; v = fl32(E4M3(q) * s)
+ *   x : bf16 [T, K], rows ld elements apart
+ *   row_token : DEVICE int32 [rows]: row r of the copy is token row_token[r] (a value
+ *       outside [0, T): zeros), or NULL: row r is token r, and rows must be T (or 0)
+ *   qt : E4M3 [K, Mp], et : uint8 [Mp/128][K] with Mp = rows rounded up to 128
+ * Requires T, rows < 2^31, K % 128 == 0, ld >= K, ld % 8 == 0, fewer than 2^23 tiles of
+ * 128 x 128; q, x and qt 16-byte aligned, s and row_token 4-byte.  q, s and x may be
+ * NULL when T is 0.  One launch. */
+int fp8q_transpose_act_128x1(const uint8_t *q, const float *s, int64_t T, int64_t K, const int32_t *row_token,
+                             int64_t rows, uint8_t *qt, uint8_t *et, void *stream);
+int fp8q_quant_act_128x1(const uint16_t *x, int64_t ld, int64_t T, int64_t K, const int32_t *row_token, int64_t rows,
+                         uint8_t *qt, uint8_t *et, void *stream);
+
+/* SwiGLU's gradient from the 8-bit checkpoint of its inputs, in the forms that the
+ * two backward products take (h = SiLU(x) u is recomputed):
+ *   x = fl32(E4M3(q[m,f]) * s[f/128][m]), u the same of column F + f,  p = 1 / (1 + e^-x)
+ *   dx = gh u (p + x p (1 - p)),  du = gh x p,  h = x p u        (fp32)
+ *   q  : E4M3 [M, 2F] (gate columns, then up columns), s : fp32 [2F/128][M]
+ *   gh : bf16 [M, F], rows ldg elements apart: the gradient of h
+ *   gq : E4M3 [M, 2F], gs : fp32 [2F/128][M]   (outputs) dx | du in 1x128 groups, scale
+ *        fl32(amax / 448)
+ *   gqt : E4M3 [2F, Mp], get : uint8 [Mp/128][2F]   (outputs) their backward copy
+ *   hqt : E4M3 [F, Mp], het : uint8 [Mp/128][F]     (outputs) that of h
+ * Requires F % 128 == 0, ldg >= F, ldg % 8 == 0, fewer than 2^23 tiles of 128 x 128;
+ * s, gs 4-byte aligned, the rest to 16 bytes.  One launch. */
+int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t *gh, int64_t ldg, int64_t M, int64_t F,
+                               uint8_t *gq, float *gs, uint8_t *gqt, uint8_t *get, uint8_t *hqt, uint8_t *het,
+                               void *stream);
+
+/* Bytes of device workspace for fp8q_gemm_wgrad with this out_dtype (0 for most
+ * sizes).  Returns -1 for invalid sizes. */
+int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype);
+
+/* A Linear's weight gradient dW = dY^T x from the backward copies of dY and x:
+ *   dw[n,k] = sum_mb 2^(eg[mb][n] + ex[mb][k] - 254) sum_{m in mb} gt[n,m] xt[k,m]   (+ dw[n,k] if accumulate)
+ *   gt : E4M3 [N, M], eg : uint8 [M/128][N];  xt : E4M3 [K, M], ex : uint8 [M/128][K]
+ *   dw : [N, K] in out_dtype (output, and input if accumulate is 1)
+ * fp32 out: bf16 matrix instructions on the exact values, fp32 sums.  bf16 out: FP8
+ * matrix instructions, whose sums are about 1.4e-5 off (relative to a result's rms),
+ * rounded once.
+ *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, contents on
+ *          entry do not matter (calls that share one must not overlap); NULL will do
+ *          when 0 bytes are needed
+ * Requires M % 128 == 0, M <= 2^23, N % 16 == 0, K % 16 == 0; all pointers 16-byte
+ * aligned.  With M 0, dw becomes 0 (or stays). */
+int fp8q_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
+                    int accumulate, int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
+                    void *stream);
+
+/* The same for every expert of an expert-sorted layout: dw[e] over the columns
+ * [off[e], off[e+1]) of the copies.
+ *   off : DEVICE int32 [E+1], the layout's segment starts: non-decreasing multiples of
+ *         128 up to M_total (an empty expert's gradient is 0, or stays if accumulate).
+ *         Offsets that break this are cut to [0, M_total] and to multiples of 128 below
+ *         them, a segment that ends before it starts is empty, and every access stays
+ *         inside the buffers.  Columns that no segment covers are not read.
+ *   dw  : [E][N][K] in out_dtype
+ * Requires E >= 1 and what fp8q_gemm_wgrad requires of M_total, N and K. */
+int fp8q_grouped_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw,
+                            int out_dtype, int accumulate, const int32_t *off, int64_t E, int64_t M_total, int64_t N,
+                            int64_t K, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,164 @@
+"""Weight gradients from backward copies, dense and per expert.
+
+Bounds per element, B = sum |g| |x| (scaled): fp32 results add bf16 products with fp32 accumulation, at most M roundings of
+2^-23 B; bf16 results come from FP8 instructions, whose alignment of 128 products cuts at most 2^-14 of their magnitudes (a
+largest error of 2^-16.8 B was measured), and round by 2^-8 once.  With small whole numbers every sum is exact, and results are
+compared bit for bit."""
+import pytest
+import torch
+
+import fine_grained_quantization_amd as fq
+from backward_reference import copy_values, e4m3
+from gpu_util import require_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def copies(C, M, seed, whole=False):
+    g = torch.Generator(device="cuda").manual_seed(seed * 1000 + C + M)
+    if whole:
+        v = torch.randint(-2, 3, (C, M), device="cuda", generator=g).float()
+        return e4m3(v), torch.randint(126, 129, (M // 128, C), dtype=torch.uint8, device="cuda", generator=g)
+    return (e4m3(130 * torch.randn((C, M), device="cuda", generator=g)),
+            torch.randint(112, 126, (M // 128, C), dtype=torch.uint8, device="cuda", generator=g))
+
+
+def check(dw, g, x, dtype, base=None, exact=False):
+    want = g @ x.t()
+    size = g.abs() @ x.abs().t()
+    if base is not None:
+        want = want + base.double()
+        size = size + base.double().abs()
+    if exact:
+        assert torch.equal(dw.double(), want.to(dtype).double())
+        return
+    M = g.shape[1]
+    if dtype is torch.float32:
+        assert bool(((dw.double() - want).abs() <= (M + 4) * 2.0 ** -23 * size).all())
+        assert float((dw.double() - want).norm()) <= 2e-6 * float(want.norm())
+    else:
+        assert bool(((dw.double() - want).abs() <= 2.0 ** -8 * want.abs() + 1.01 * 2.0 ** -14 * size).all())
+
+
+SIZES = [(128, 16, 16), (128, 128, 128), (256, 64, 4096), (384, 144, 2064), (1024, 576, 2064), (4096, 512, 272), (640, 2320, 272),
+         (256, 4112, 4368), (896, 4096, 4352), (16384, 64, 80), (128, 8192, 8192), (8192, 256, 256), (2048, 1040, 1040)]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_wgrad(M, N, K, dtype, accumulate):
+    say(f"wgrad M={M} N={N} K={K} {dtype} accumulate={accumulate}")
+    for whole in (True, False):
+        gt, eg = copies(N, M, 1, whole)
+        xt, ex = copies(K, M, 2, whole)
+        base = torch.randint(-9, 9, (N, K), device="cuda").to(dtype) if accumulate else None
+        dw = base.clone() if accumulate else torch.full((N, K), float("nan"), dtype=dtype, device="cuda")
+        got = fq.fp8q_gemm_wgrad(gt, eg, xt, ex, out_dtype=dtype, accumulate=accumulate, dw=dw)
+        assert got is dw
+        check(dw, copy_values(gt, eg), copy_values(xt, ex), dtype, base, whole)
+        if not accumulate:
+            again = fq.fp8q_gemm_wgrad(gt, eg, xt, ex, out_dtype=dtype)
+            assert torch.equal(again, dw)
+
+
+def test_scales_of_every_exponent():
+    """Each channel's scale from 2^-127 up, on either side: fp32 results are the exact products (one code of 1 a channel)."""
+    M, C = 128, 240
+    one = torch.zeros((C, M), device="cuda")
+    one[:, 3] = 1.5
+    e = torch.arange(1, C + 1, device="cuda").to(torch.uint8).view(1, C)
+    mid = torch.full((1, C), 127, dtype=torch.uint8, device="cuda")
+    q = e4m3(one)
+    for dtype in (torch.float32, torch.bfloat16):
+        for eg, ex in ((e, mid), (mid, e)):
+            dw = fq.fp8q_gemm_wgrad(q, eg.contiguous(), q, ex.contiguous(), out_dtype=dtype)
+            want = (copy_values(q, eg) @ copy_values(q, ex).t()).to(dtype)
+            assert torch.equal(dw, want)
+
+
+def layout(loads, pad_blocks, device="cuda"):
+    off = [0]
+    for n in loads:
+        off.append(off[-1] + (n + 127) // 128 * 128)
+    return torch.tensor(off, dtype=torch.int32, device=device), off[-1] + 128 * pad_blocks
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,K", [(64, 128), (272, 400), (1040, 2064)])
+@pytest.mark.parametrize("loads", [[1], [0, 300, 0, 128, 5, 700, 0], [0, 0, 0], [2000] + [60] * 20])
+def test_experts(loads, N, K, dtype, accumulate):
+    off, M = layout(loads, 3)
+    E = len(loads)
+    say(f"wgrad of {E} experts N={N} K={K} {dtype} accumulate={accumulate}")
+    for whole in (True, False):
+        gt, eg = copies(N, M, 3, whole)
+        xt, ex = copies(K, M, 4, whole)
+        gt[:, int(off[-1]):] = 0x7F  # columns that no segment covers are not read: NaN there changes nothing
+        xt[:, int(off[-1]):] = 0x7F
+        base = torch.randint(-9, 9, (E, N, K), device="cuda").to(dtype) if accumulate else None
+        dw = base.clone() if accumulate else torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
+        fq.fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, off, out_dtype=dtype, accumulate=accumulate, dw=dw)
+        g, x = copy_values(gt, eg), copy_values(xt, ex)
+        for e in range(E):
+            a, b = int(off[e]), int(off[e + 1])
+            check(dw[e], g[:, a:b], x[:, a:b], dtype, base[e] if accumulate else None, whole)
+
+
+def test_segments_that_break_the_rules():
+    """Cut to the columns and to whole blocks; an end before its start is an empty segment."""
+    M, N, K = 512, 64, 80
+    gt, eg = copies(N, M, 5, True)
+    xt, ex = copies(K, M, 6, True)
+    g, x = copy_values(gt, eg), copy_values(xt, ex)
+    for off, spans in (([-300, 200, 2 ** 31 - 1], [(0, 128), (128, 512)]), ([256, 128, 130, 700], [(0, 0), (128, 128), (128, 512)]),
+                       ([600, 900], [(0, 0)]), ([-2 ** 31, 384], [(0, 384)])):
+        o = torch.tensor(off, dtype=torch.int32, device="cuda")
+        dw = fq.fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, o)
+        for e, (a, b) in enumerate(spans):
+            check(dw[e], g[:, a:b], x[:, a:b], torch.float32, None, True)
+
+
+def test_no_tokens():
+    z = torch.empty((64, 0), dtype=torch.uint8, device="cuda")
+    s = torch.empty((0, 64), dtype=torch.uint8, device="cuda")
+    dw = torch.full((64, 64), 3.0, device="cuda")
+    assert fq.fp8q_gemm_wgrad(z, s, z, s, accumulate=True, dw=dw) is dw and bool((dw == 3).all())
+    assert bool((fq.fp8q_gemm_wgrad(z, s, z, s, dw=dw) == 0).all())
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert bool((fq.fp8q_grouped_gemm_wgrad(z, s, z, s, off, out_dtype=torch.bfloat16) == 0).all())
+
+
+def test_copies_past_2_gib():
+    """M * C past 2^31 in the column operand: offsets of tiles are formed in 64 bits."""
+    M, N, K = 65536, 32, 32784
+    gt, eg = copies(N, M, 7, True)
+    xt = torch.zeros((K, M), dtype=torch.uint8, device="cuda")
+    tail, ex_tail = copies(16, M, 8, True)
+    xt[-16:] = tail
+    ex = torch.full((M // 128, K), 127, dtype=torch.uint8, device="cuda")
+    ex[:, -16:] = ex_tail
+    say("wgrad, column operand of 2.1 GB")
+    for dtype in (torch.float32, torch.bfloat16):
+        dw = fq.fp8q_gemm_wgrad(gt, eg, xt, ex, out_dtype=dtype)
+        want = copy_values(gt, eg) @ copy_values(tail, ex_tail).t()
+        assert torch.equal(dw[:, -16:].double(), want.to(dtype).double()) and int((dw[:, :-16] != 0).sum()) == 0
+
+
+def test_gradients_past_4_gib():
+    """E * N * K past 2^32 bytes."""
+    E, N, K = 40, 8192, 4096
+    off, M = layout([128] * E, 0)
+    gt, eg = copies(N, M, 9, True)
+    xt, ex = copies(K, M, 10, True)
+    say("wgrad of 40 experts of 8192 x 4096, fp32 (5.4 GB)")
+    dw = fq.fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, off)
+    g, x = copy_values(gt, eg), copy_values(xt, ex)
+    for e in (0, 17, 31, 32, 39):
+        check(dw[e], g[:, 128 * e:128 * e + 128], x[:, 128 * e:128 * e + 128], torch.float32, None, True)
