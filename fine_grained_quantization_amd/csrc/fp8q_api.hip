@@ -49,6 +49,7 @@ constexpr int64_t kMaxGrid256 = 0xFFFFFFFFll / 256, kMaxGrid512 = 0xFFFFFFFFll /
 constexpr int64_t kMaxGateTokens = 0xFFFFFFFFll / 64;  // 64 lanes a token at most
 
 constexpr int64_t kMaxNormRows = int64_t(1) << 22;  // a workgroup of up to 1024 threads a row
+constexpr int64_t kMaxWgrad = int64_t(1) << 20;     // 256 rows of fp32 results are addressed with 32-bit offsets
 constexpr int64_t kMaxInt8K = 131056;        // INT8 sums of products of codes down to -128 stay below 2^31
 
 int finish(hipError_t e) { return e == hipSuccess ? FP8Q_OK : FP8Q_ERR_HIP; }
@@ -572,7 +573,7 @@ int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t 
 }
 
 int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
-    if (M < 0 || M % 128 || M > kMaxK || N < 0 || N % 16 || K < 0 || K % 16) return -1;
+    if (M < 0 || M % 128 || M > kMaxK || N < 0 || N > kMaxWgrad || N % 16 || K < 0 || K > kMaxWgrad || K % 16) return -1;
     if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_F32) return -1;
     const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, 1);
     if (blocks < 0 || blocks > kMaxGrid512) return -1;
@@ -582,7 +583,8 @@ int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out
 static int wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
                  int accumulate, bool grouped, const int32_t *off, int64_t E, int64_t M, int64_t N, int64_t K,
                  void *workspace, int64_t workspace_bytes, void *stream) {
-    if (E < 1 || E > 0x7FFFFFFF || M < 0 || M % 128 || M > kMaxK || N < 0 || N % 16 || K < 0 || K % 16)
+    if (E < 1 || E > 0x7FFFFFFF || M < 0 || M % 128 || M > kMaxK || N < 0 || N > kMaxWgrad || N % 16 || K < 0 ||
+        K > kMaxWgrad || K % 16)
         return FP8Q_ERR_SHAPE;
     const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, E);
     if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;

@@ -19,9 +19,20 @@ __device__ fp8q_i32x4 fp8q_raw_buffer_load_b128(fp8q_i32x4 rsrc, int voffset, in
 __device__ float fp8q_raw_buffer_load_f32(fp8q_i32x4 rsrc, int voffset, int soffset,
                                           int aux) __asm("llvm.amdgcn.raw.buffer.load.f32");
 
+typedef int fp8q_i32x2 __attribute__((ext_vector_type(2)));
+
+// LLVM's raw buffer stores from registers (16 / 8 bytes per lane); out-of-range lanes store nothing.
+__device__ void fp8q_raw_buffer_store_b128(fp8q_i32x4 data, fp8q_i32x4 rsrc, int voffset, int soffset,
+                                           int aux) __asm("llvm.amdgcn.raw.buffer.store.v4i32");
+__device__ void fp8q_raw_buffer_store_b64(fp8q_i32x2 data, fp8q_i32x4 rsrc, int voffset, int soffset,
+                                          int aux) __asm("llvm.amdgcn.raw.buffer.store.v2i32");
+__device__ fp8q_i32x2 fp8q_raw_buffer_load_b64(fp8q_i32x4 rsrc, int voffset, int soffset,
+                                               int aux) __asm("llvm.amdgcn.raw.buffer.load.v2i32");
+
 namespace fp8q {
 
 typedef fp8q_i32x4 i32x4;
+typedef fp8q_i32x2 i32x2;
 
 // A byte offset past every buffer this library builds (they are < 2^31 bytes): loads there return 0
 // without touching memory.

@@ -222,14 +222,91 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(WgradArgs p) {
         }
 }
 
+// ---------------------------------------------------------------------------------------------------------
+// Large results: 256 x 256 tiles by 8 waves of 64 x 128, one workgroup to a CU, each walking up to 64 tiles b, b + G, ... as one
+// stream of blocks of 128 tokens: the copies of the next tile's first blocks are under way while a tile's results are stored.
+// A ring of 5 LDS slots of one operand's block each (A0 B0 A1 B1 A2 ...): while block s is multiplied, s + 1 and A's s + 2
+// are on the way or there.  Block s has A in slot 2 s mod 5; A's s + 2 goes where B's s - 1 was, B's s + 2 where A's s was.
+// The scale bytes come straight into registers, a block ahead.
+// ---------------------------------------------------------------------------------------------------------
+
+constexpr int kSlot = 256 * 128, kSlots = 5, kMostTiles = 64;
+
+// Waits for this wave's LDS reads and for all but its last N loads and stores, then for the workgroup.
+template <int N>
+__device__ __forceinline__ void copies_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+struct WgradTile {
+    int e, n0, k0, nrow, ncol, b0, KB;  // expert, corner, rows and columns that exist, first block, blocks
+};
+
+// A workgroup's tiles, one to a lane, in 32-bit arithmetic: tile T = expert by expert, each in the dense order (columns of 16
+// tiles along k, in them squares of 16 x 16 in blocks of 4 x 8).
+struct WgradTiles {
+    int e, at;  // at: n tile << 16 | k tile
+
+    // Returns the tile's blocks; -1: there is no such tile.
+    __device__ __forceinline__ int init(const WgradArgs &p, uint32_t t) {
+        const uint32_t nt = (uint32_t)p.n_tiles, kt = (uint32_t)p.k_tiles, per = nt * kt;
+        uint32_t T = (t / 256) * 256 + (t % 8) * 32 + (t % 256) / 8;  // xcd_order
+        e = at = 0;
+        if (T >= (uint32_t)p.E * per) return -1;
+        e = (int)(T / per);
+        T -= (uint32_t)e * per;
+        const uint32_t sg = T / (16 * nt), hn = min(kt - 16 * sg, 16u);
+        uint32_t j = T - sg * 16 * nt;
+        const uint32_t sm = j / (16 * hn), hm = min(nt - 16 * sm, 16u);
+        j -= sm * 16 * hn;
+        const uint32_t qn = j / (8 * hm), wq = min(hn - 8 * qn, 8u);
+        j -= qn * 8 * hm;
+        const uint32_t qm = j / (4 * wq), hq = min(hm - 4 * qm, 4u);
+        j -= qm * 4 * wq;
+        at = (int)((16 * sm + 4 * qm + j % hq) << 16 | (16 * sg + 8 * qn + j / hq));
+        int b0, KB;
+        blocks(p, e, b0, KB);
+        return KB;
+    }
+    // An expert's blocks: its segment, cut to [0, M) and to whole blocks.
+    static __device__ __forceinline__ void blocks(const WgradArgs &p, int e, int &b0, int &KB) {
+        int lo = 0, hi = (int)p.M;
+        if (p.off != nullptr) {
+            lo = p.off[e];
+            hi = p.off[e + 1];
+            lo = lo < 0 ? 0 : (lo > (int)p.M ? (int)p.M : lo & ~127);
+            hi = hi < lo ? lo : (hi > (int)p.M ? (int)p.M : hi & ~127);
+        }
+        b0 = lo >> 7;
+        KB = (hi - lo) >> 7;
+    }
+    __device__ __forceinline__ WgradTile get(const WgradArgs &p, int i) const {
+        WgradTile w;
+        const int x = __builtin_amdgcn_readlane(at, i);
+        w.e = __builtin_amdgcn_readlane(e, i);
+        w.n0 = ((uint32_t)x >> 16) * 256;
+        w.k0 = (x & 0xFFFF) * 256;
+        w.nrow = min((int)p.N - w.n0, 256);
+        w.ncol = min((int)p.K - w.k0, 256);
+        blocks(p, w.e, w.b0, w.KB);
+        w.b0 = __builtin_amdgcn_readfirstlane(w.b0);
+        w.KB = __builtin_amdgcn_readfirstlane(w.KB);
+        return w;
+    }
+};
+
 // A lane holds, of row 4 (4 g + r) + a of a wave's 64, columns 4 i .. 4 i + 3 of each of its 2 column groups: 16 lanes store 64
-// consecutive columns.
-template <bool EXACT, bool ACCUMULATE, typename Tile>
-__device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const Tile &w, int wm, int wn, int i,
-                                            int g) {
+// consecutive columns.  32 stores whatever the tile's size (those past it are out of range): the waits for copies that are
+// older than the stores count on it.
+template <bool EXACT, bool ACCUMULATE>
+__device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const WgradTile &w, int row, int col) {
     constexpr bool kBf16 = !EXACT;
-    const int64_t base = ((int64_t)w.e * p.N + w.n0) * p.K + w.k0;
-    const int row = wm * 64 + 16 * g, col = wn * 128 + 4 * i;
+    constexpr int kEl = kBf16 ? 2 : 4;
+    const i32x4 rs = make_rsrc(static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl,
+                               (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * kEl));
+    // (rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there)
+    const int pitch = (int)p.K * kEl, at = row * pitch + col * kEl;
+    const int at0 = col < w.ncol ? at : kOutOfRange, at1 = col + 64 < w.ncol ? at + 64 * kEl : kOutOfRange;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
         v4f old[4][2];
@@ -238,16 +315,11 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)
             for (int a = 0; a < 4; a++)
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    const bool in = row + 4 * r + a < w.nrow && col + 64 * c < w.ncol;
-                    const int64_t at = base + (int64_t)(row + 4 * r + a) * p.K + col + 64 * c;
                     if constexpr (kBf16) {
-                        const uint2 o = in ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.dw) + at)
-                                           : (uint2){0u, 0u};
-                        old[a][c] = (v4f){bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y)};
+                        const i32x2 o = fp8q_raw_buffer_load_b64(rs, c ? at1 : at0, (4 * r + a) * pitch, 0);
+                        old[a][c] = (v4f){bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
                     } else {
-                        const float4 o = in ? *reinterpret_cast<const float4 *>(static_cast<const float *>(p.dw) + at)
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-                        old[a][c] = (v4f){o.x, o.y, o.z, o.w};
+                        old[a][c] = __builtin_bit_cast(v4f, fp8q_raw_buffer_load_b128(rs, c ? at1 : at0, (4 * r + a) * pitch, 0));
                     }
                 }
         }
@@ -257,79 +329,41 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)
             for (int c = 0; c < 2; c++) {
                 v4f v = {acc[a][4 * c][r], acc[a][4 * c + 1][r], acc[a][4 * c + 2][r], acc[a][4 * c + 3][r]};
                 if constexpr (ACCUMULATE) v += old[a][c];
-                if (row + 4 * r + a < w.nrow && col + 64 * c < w.ncol)
-                    store4<kBf16>(p.dw, base + (int64_t)(row + 4 * r + a) * p.K + col + 64 * c, v);
+                if constexpr (kBf16)
+                    fp8q_raw_buffer_store_b64((i32x2){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])}, rs,
+                                              c ? at1 : at0, (4 * r + a) * pitch, 0);
+                else
+                    fp8q_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rs, c ? at1 : at0, (4 * r + a) * pitch, 0);
             }
     }
 }
 
-// ---------------------------------------------------------------------------------------------------------
-// Large results: 256 x 256 tiles by 8 waves of 64 x 128, one workgroup to a CU, each walking tiles b, b + G, ... as one
-// stream of blocks of 128 tokens: the copies of the next tile's first blocks are under way while a tile's results are stored.
-// A ring of 5 LDS slots of one operand's block each (A0 B0 A1 B1 A2 ...): while block s is multiplied, s + 1 and A's s + 2
-// are on the way or there.  Block s has A in slot 2 s mod 5; A's s + 2 goes where B's s - 1 was, B's s + 2 where A's s was.
-// The scale bytes come straight into registers, two blocks ahead.
-// ---------------------------------------------------------------------------------------------------------
-
-constexpr int kSlot = 256 * 128, kSlots = 5;
-
-// Waits for this wave's LDS reads and for all but its last N loads, then for the workgroup.
-template <int N>
-__device__ __forceinline__ void copies_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
-
-// Tile T of the product(s): expert by expert, each in the dense order (columns of 16 tiles along k, in them 16 x 16 squares
-// of 4 x 8 blocks), in 32-bit arithmetic.
-struct WgradTile {
-    int e, n0, k0, nrow, ncol, b0, KB;
-};
-
-__device__ __forceinline__ WgradTile wgrad_tile(const WgradArgs &p, uint32_t T) {
-    const uint32_t nt = (uint32_t)p.n_tiles, kt = (uint32_t)p.k_tiles, per = nt * kt;
-    WgradTile w;
-    w.e = 0;
-    if (p.off != nullptr) {
-        w.e = T / per;
-        T -= w.e * per;
-    }
-    const uint32_t sg = T / (16 * nt), hn = min(kt - 16 * sg, 16u);
-    uint32_t j = T - sg * 16 * nt;
-    const uint32_t sm = j / (16 * hn), hm = min(nt - 16 * sm, 16u);
-    j -= sm * 16 * hn;
-    const uint32_t qn = j / (8 * hm), wq = min(hn - 8 * qn, 8u);
-    j -= qn * 8 * hm;
-    const uint32_t qm = j / (4 * wq), hq = min(hm - 4 * qm, 4u);
-    j -= qm * 4 * wq;
-    w.n0 = (16 * sm + 4 * qm + j % hq) * 256;
-    w.k0 = (16 * sg + 8 * qn + j / hq) * 256;
-    int lo = 0, hi = (int)p.M;
-    if (p.off != nullptr) {  // the segment, cut to [0, M) and to whole blocks
-        lo = p.off[w.e];
-        hi = p.off[w.e + 1];
-        lo = lo < 0 ? 0 : (lo > (int)p.M ? (int)p.M : lo & ~127);
-        hi = hi < lo ? lo : (hi > (int)p.M ? (int)p.M : hi & ~127);
-    }
-    w.nrow = min((int)p.N - w.n0, 256);
-    w.ncol = min((int)p.K - w.k0, 256);
-    w.e = __builtin_amdgcn_readfirstlane(w.e);
-    w.n0 = __builtin_amdgcn_readfirstlane(w.n0);
-    w.k0 = __builtin_amdgcn_readfirstlane(w.k0);
-    w.nrow = __builtin_amdgcn_readfirstlane(w.nrow);
-    w.ncol = __builtin_amdgcn_readfirstlane(w.ncol);
-    w.b0 = __builtin_amdgcn_readfirstlane(lo >> 7);
-    w.KB = __builtin_amdgcn_readfirstlane((hi - lo) >> 7);
-    return w;
-}
-
 template <bool EXACT, bool ACCUMULATE>
-__global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p, uint32_t tiles) {
+__global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
     const int wm = wave & 3, wn = wave >> 2;
     const int i = lane & 15, g = lane >> 4;
+    const int row = wm * 64 + 16 * g, col = wn * 128 + 4 * i;  // of the lane's results
     const int64_t ld = p.M;
+    WgradTiles list;
+    const int blocks = list.init(p, blockIdx.x + gridDim.x * lane);
+    const uint64_t work = __ballot(blocks > 0);
+    if constexpr (!ACCUMULATE) {  // tiles of no tokens: zeros
+        for (uint64_t none = __ballot(blocks == 0); none != 0; none &= none - 1) {
+            const WgradTile w = list.get(p, __builtin_ctzll(none));
+            constexpr int kEl = EXACT ? 4 : 2;
+            uint8_t *c = static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl;
+            const int chunks = w.ncol * kEl / 16;
+            for (int at = tid; at < w.nrow * chunks; at += 512) {
+                const int r = at / chunks;
+                *reinterpret_cast<u32x4 *>(c + r * p.K * kEl + (at - r * chunks) * 16) = (u32x4){0u, 0u, 0u, 0u};
+            }
+        }
+    }
+    if (work == 0) return;
+
     // Copies: an instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, chunk l % 8, which holds logical chunk
     // (l % 8) ^ wswz(row).  Rows past the operand are past its resource: their offset is at least nrow * ld.
     int voff[4];
@@ -338,36 +372,24 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p, uint3
         const int r = wave * 32 + j * 8 + (lane >> 3);
         voff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
     }
-    // The stream's issue end: the tile and block that are copied next.
-    uint32_t next = blockIdx.x;  // tile after the issue tile, in the launch's order
-    i32x4 ra = make_rsrc(p.gt, 0), rb = ra, sra = ra, srb = ra;
+    // The stream's issue end: the block that is copied next.
+    uint64_t ahead = work;  // tiles from its tile on
+    i32x4 ra, rb, sra, srb;
     int ikb = 0, iKB = 0, vsa = 0, vsb0 = 0, vsb1 = 0;
-    auto next_tile = [&]() __attribute__((always_inline)) {
+    auto open_tile = [&]() __attribute__((always_inline)) {  // the first of `ahead`; none: nothing is read
+        const WgradTile w = list.get(p, ahead ? __builtin_ctzll(ahead) : 0);
         ikb = 0;
-        iKB = 0;
-        while (iKB == 0 && next < tiles) {
-            const uint32_t T = (uint32_t)xcd_order(next);
-            next += gridDim.x;
-            if (T >= (uint32_t)(p.E * p.n_tiles * p.k_tiles)) continue;
-            const WgradTile w = wgrad_tile(p, T);
-            if (w.KB == 0) continue;
-            iKB = w.KB;
-            // (the range check takes the lane's and the scalar offset together)
-            ra = make_rsrc(p.gt + w.n0 * ld + (int64_t)w.b0 * 128, (uint64_t)((w.nrow - 1) * ld + w.KB * 128));
-            rb = make_rsrc(p.xt + w.k0 * ld + (int64_t)w.b0 * 128, (uint64_t)((w.ncol - 1) * ld + w.KB * 128));
-            sra = make_rsrc(p.eg + (int64_t)w.b0 * p.N + w.n0, (uint64_t)((w.KB - 1) * p.N + w.nrow));
-            srb = make_rsrc(p.ex + (int64_t)w.b0 * p.K + w.k0, (uint64_t)((w.KB - 1) * p.K + w.ncol));
-            vsa = wm * 64 + 4 * i;
-            vsb0 = wn * 128 + 4 * i;
-            vsb1 = vsb0 + 64;
-            vsa = vsa < w.nrow ? vsa : kOutOfRange;
-            vsb0 = vsb0 < w.ncol ? vsb0 : kOutOfRange;
-            vsb1 = vsb1 < w.ncol ? vsb1 : kOutOfRange;
-        }
-        if (iKB == 0) ra[2] = rb[2] = sra[2] = srb[2] = 0;  // the stream has ended: nothing is read
-    };
-    auto advance = [&]() __attribute__((always_inline)) {
-        if (++ikb >= iKB) next_tile();
+        iKB = ahead ? w.KB : 0x7FFFFFFF;
+        // (the range check takes the lane's and the scalar offset together)
+        ra = make_rsrc(p.gt + w.n0 * ld + (int64_t)w.b0 * 128, ahead ? (uint64_t)((w.nrow - 1) * ld + w.KB * 128) : 0);
+        rb = make_rsrc(p.xt + w.k0 * ld + (int64_t)w.b0 * 128, ahead ? (uint64_t)((w.ncol - 1) * ld + w.KB * 128) : 0);
+        sra = make_rsrc(p.eg + (int64_t)w.b0 * p.N + w.n0, ahead ? (uint64_t)((w.KB - 1) * p.N + w.nrow) : 0);
+        srb = make_rsrc(p.ex + (int64_t)w.b0 * p.K + w.k0, ahead ? (uint64_t)((w.KB - 1) * p.K + w.ncol) : 0);
+        const int a = wm * 64 + 4 * i;
+        vsa = a < w.nrow ? a : kOutOfRange;
+        vsb0 = col < w.ncol ? col : kOutOfRange;
+        vsb1 = col + 64 < w.ncol ? col + 64 : kOutOfRange;
+        ahead &= ahead - 1;
     };
     auto copy_a = [&](int j, int slot) __attribute__((always_inline)) {
         fp8q_raw_buffer_load_lds(ra, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, voff[j], ikb * 128, 0, 0);
@@ -380,28 +402,8 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p, uint3
         s[1] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb0, ikb * (int)p.K, 0));
         s[2] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb1, ikb * (int)p.K, 0));
     };
-    const int z = ((i & 7) ^ (i >> 3));
-    const int frag0 = i * 512 + (((2 * g) ^ z) << 4);  // chunk 2 g of row 4 i of a wave's rows; chunk 2 g + 1: ^ 16
+    const int frag0 = i * 512 + (((2 * g) ^ (i & 7) ^ (i >> 3)) << 4);  // chunk 2 g of row 4 i of a wave's; chunk 2 g + 1: ^ 16
     const int fa_at = wm * 8192 + frag0, fb_at = wn * 16384 + frag0;
-
-    uint32_t sc[3], sc1[3], sc2[3];
-    next_tile();
-    if (iKB > 0) {
-        scales(sc);
-#pragma unroll
-        for (int j = 0; j < 4; j++) copy_a(j, 0);
-#pragma unroll
-        for (int j = 0; j < 4; j++) copy_b(j, 1);
-        advance();
-        scales(sc1);
-#pragma unroll
-        for (int j = 0; j < 4; j++) copy_a(j, 2);
-#pragma unroll
-        for (int j = 0; j < 4; j++) copy_b(j, 3);
-        copies_barrier<8>();  // block 0 is there
-    }
-    int slot = 0;
-    auto wrap = [](int s) { return s >= kSlots ? s - kSlots : s; };
     auto read8 = [&](int at0, int at1, int off) __attribute__((always_inline)) {  // 32 codes of a row: both chunks
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(lds + at0 + off);
         const u32x4 hi = *reinterpret_cast<const u32x4 *>(lds + at1 + off);
@@ -410,43 +412,70 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p, uint3
         f[4] = (int)hi[0]; f[5] = (int)hi[1]; f[6] = (int)hi[2]; f[7] = (int)hi[3];
         return f;
     };
+
+    uint32_t sc[2][3];  // block s's are in sc[s % 2]
+    open_tile();
+    scales(sc[0]);
+#pragma unroll
+    for (int j = 0; j < 4; j++) copy_a(j, 0);
+#pragma unroll
+    for (int j = 0; j < 4; j++) copy_b(j, 1);
+    if (++ikb >= iKB) open_tile();
+#pragma unroll
+    for (int j = 0; j < 4; j++) copy_a(j, 2);
+#pragma unroll
+    for (int j = 0; j < 4; j++) copy_b(j, 3);
+    copies_barrier<8>();  // block 0 is there
+    int slot = 0;
+    auto wrap = [](int s) { return s >= kSlots ? s - kSlots : s; };
     v4f acc[4][8];
     v8i fa[4], fb[4];
-    if (iKB >= 0) {
 #pragma unroll
-        for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
+    for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
 #pragma unroll
-        for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 128);
-    }
-    auto mfma = [&](auto a_, auto b_) __attribute__((always_inline)) {
+    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 128);
+    auto mfma = [&](const uint32_t (&s)[3], auto a_, auto b_) __attribute__((always_inline)) {
         constexpr int a = decltype(a_)::value, b = decltype(b_)::value;
-        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a], fb[b & 3], acc[a][b], 0, 0, a, (int)sc[0], b & 3,
-                                                                     (int)sc[1 + b / 4]);
+        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a], fb[b & 3], acc[a][b], 0, 0, a, (int)s[0], b & 3,
+                                                                     (int)s[1 + b / 4]);
     };
+    bool stored = false;  // a tile's results were stored between this block and the one before
     // One block.  Phases 0 to 4: column subtile b by the 4 row subtiles, while subtile b + 3 is read.  Then everything of
     // the block is in registers: the barrier frees its slots, and subtiles 5 to 7 are taken row by row, each row's fragment
     // being replaced by the next block's when it is done.  (Every other phase runs backwards, so that one operand changes
     // from MFMA to MFMA.)
-    auto block = [&]() __attribute__((always_inline)) {
+    auto block = [&](auto turn_) __attribute__((always_inline)) {
+        constexpr int turn = decltype(turn_)::value;
+        uint32_t(&s)[3] = sc[turn];
         const int nA = wrap(slot + 2), last = wrap(slot + 4);
         const int b0 = wrap(slot + 1) * kSlot + fb_at, b1 = b0 ^ 16;             // this block's columns
         const int nb0 = wrap(slot + 3) * kSlot + fb_at, nb1 = nb0 ^ 16;          // the next block's
         const int na0 = nA * kSlot + fa_at, na1 = na0 ^ 16;
-        advance();  // (here, where no matrix instruction could be moved behind its branches)
-        scales(sc2);
+        scales(sc[turn ^ 1]);
+        if (++ikb >= iKB) open_tile();  // (here, where no matrix instruction could be moved behind its branch)
         static_for<5>([&](auto b_) __attribute__((always_inline)) {
             constexpr int b = decltype(b_)::value;
             fb[(b + 3) & 3] = read8(b0, b1, ((b + 3) / 4) * 8192 + ((b + 3) & 3) * 128);
             if constexpr (b < 4) copy_a(b, last);
             static_for<4>([&](auto a_) __attribute__((always_inline)) {
-                mfma(Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
+                mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
             });
             __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
             if constexpr (b < 4) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
             __builtin_amdgcn_sched_barrier(0);
         });
-        copies_barrier<4>();
+        // (the compiler would move the phases above behind the branch)
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int b = 0; b < 5; b++) asm volatile("" : "+v"(acc[a][b]));
+        // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's 32 stores, which need
+        // not have reached memory.
+        if (stored)
+            copies_barrier<39>();
+        else
+            copies_barrier<7>();
         __builtin_amdgcn_sched_barrier(0);
         fb[0] = read8(nb0, nb1, 0);
         static_for<4>([&](auto a_) __attribute__((always_inline)) {
@@ -454,32 +483,38 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p, uint3
             copy_b(a, slot);
             static_for<3>([&](auto c_) __attribute__((always_inline)) {
                 constexpr int c = decltype(c_)::value;
-                mfma(a_, Index<5 + ((a & 1) ? 2 - c : c)>{});
+                mfma(s, a_, Index<5 + ((a & 1) ? 2 - c : c)>{});
             });
             fa[a] = read8(na0, na1, a * 128);
             __builtin_amdgcn_sched_barrier(0);
         });
         fb[1] = read8(nb0, nb1, 128);
         fb[2] = read8(nb0, nb1, 256);
-#pragma unroll
-        for (int j = 0; j < 3; j++) {
-            sc[j] = sc1[j];
-            sc1[j] = sc2[j];
-        }
         slot = nA;
+        stored = false;
     };
-    const uint32_t count = (uint32_t)(p.E * p.n_tiles * p.k_tiles);
-    for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        const uint32_t T = (uint32_t)xcd_order(t);
-        if (T >= count) continue;
-        const WgradTile w = wgrad_tile(p, T);
-        if (ACCUMULATE && w.KB == 0) continue;
-#pragma unroll
-        for (int a = 0; a < 4; a++)
-#pragma unroll
-            for (int b = 0; b < 8; b++) acc[a][b] = (v4f){0.f, 0.f, 0.f, 0.f};
-        for (int kb = 0; kb < w.KB; kb++) block();
-        wgrad_store<EXACT, ACCUMULATE>(p, acc, w, wm, wn, i, g);
+#define FP8Q_WGRAD_ZERO()                         \
+    _Pragma("unroll") for (int a = 0; a < 4; a++) \
+        _Pragma("unroll") for (int b = 0; b < 8; b++) acc[a][b] = (v4f){0.f, 0.f, 0.f, 0.f};
+    FP8Q_WGRAD_ZERO()
+    uint64_t todo = work;  // tiles from the one being multiplied on
+    int left = list.get(p, __builtin_ctzll(todo)).KB;
+    for (;;) {
+        // (two blocks at a time, so that a block's scales stay in the registers that they were loaded into)
+#define FP8Q_WGRAD_STEP(TURN)                                                                                  \
+    block(Index<TURN>{});                                                                                      \
+    if (--left == 0) {                                                                                         \
+        wgrad_store<EXACT, ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
+        todo &= todo - 1;                                                                                      \
+        if (todo == 0) break;                                                                                  \
+        left = list.get(p, __builtin_ctzll(todo)).KB;                                      \
+        stored = true;                                                                                         \
+        FP8Q_WGRAD_ZERO()                                                                                      \
+    }
+        FP8Q_WGRAD_STEP(0)
+        FP8Q_WGRAD_STEP(1)
+#undef FP8Q_WGRAD_STEP
+#undef FP8Q_WGRAD_ZERO
     }
 }
 
@@ -489,9 +524,8 @@ hipError_t launch_wgrad(WgradArgs p, hipStream_t stream) {
     if (!EXACT && p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count() / 2) {
         p.n_tiles = tiles(p.N, 256);
         p.k_tiles = tiles(p.K, 256);
-        const int64_t n = (p.E * p.n_tiles * p.k_tiles + 255) / 256 * 256;
-        const int64_t wgs = cu_count() / 8 * 8;
-        wgrad_stream_kernel<EXACT, ACCUMULATE><<<dim3((unsigned)(n < wgs ? n : wgs)), 512, 0, stream>>>(p, (uint32_t)n);
+        const int64_t n = p.E * p.n_tiles * p.k_tiles, wgs = (n + 256 * kMostTiles - 1) / (256 * kMostTiles) * 256;
+        wgrad_stream_kernel<EXACT, ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
     } else if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count()) {
         using S = WgradShape<4, 2, 2>;
         p.n_tiles = tiles(p.N, S::BM);
