@@ -295,13 +295,24 @@ struct WgradTiles {
     }
 };
 
-// A lane holds, of row 4 (4 g + r) + a of a wave's 64, columns 4 i .. 4 i + 3 of each of its 2 column groups: 16 lanes store 64
-// consecutive columns.  32 stores whatever the tile's size (those past it are out of range): the waits for copies that are
-// older than the stores count on it.
+// Columns of a wave's 128 in its 8 column subtiles, so that a lane's results are 16 bytes of consecutive columns: column
+// 8 i + b of them is column i of subtile b (bf16), or 64 (b / 4) + 4 i + b % 4 (fp32).  The chunks' places follow suit.
+template <bool EXACT>
+__device__ __forceinline__ int cswz(int r) {
+    return EXACT ? wswz(r) : ((r >> 3) & 7) ^ ((r >> 6) & 1);
+}
+
+// A lane holds row 4 (4 g + r) + a of a wave's 64, and of it columns 8 i .. 8 i + 7, or 4 i .. 4 i + 3 of either half: 16 lanes
+// store 256 consecutive bytes.  Streaming stores: 64 gradients of 2048 x 7168 that nothing else delays (one block each) take
+// 313 us with them (6.0 TB/s), 432 without.  kStores of them whatever the tile's size (those past it are out of range): the
+// waits for copies that are older than the stores count on it.
+template <bool EXACT>
+constexpr int kStores = EXACT ? 32 : 16;
+constexpr int kNonTemporal = 2;
+
 template <bool EXACT, bool ACCUMULATE>
 __device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const WgradTile &w, int row, int col) {
-    constexpr bool kBf16 = !EXACT;
-    constexpr int kEl = kBf16 ? 2 : 4;
+    constexpr int kEl = EXACT ? 4 : 2;
     const i32x4 rs = make_rsrc(static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl,
                                (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * kEl));
     // (rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there)
@@ -309,32 +320,38 @@ __device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)
     const int at0 = col < w.ncol ? at : kOutOfRange, at1 = col + 64 < w.ncol ? at + 64 * kEl : kOutOfRange;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-        v4f old[4][2];
+        i32x4 old[4][2];
         if constexpr (ACCUMULATE) {
 #pragma unroll
-            for (int a = 0; a < 4; a++)
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    if constexpr (kBf16) {
-                        const i32x2 o = fp8q_raw_buffer_load_b64(rs, c ? at1 : at0, (4 * r + a) * pitch, 0);
-                        old[a][c] = (v4f){bf16_lo(o[0]), bf16_hi(o[0]), bf16_lo(o[1]), bf16_hi(o[1])};
-                    } else {
-                        old[a][c] = __builtin_bit_cast(v4f, fp8q_raw_buffer_load_b128(rs, c ? at1 : at0, (4 * r + a) * pitch, 0));
-                    }
-                }
+            for (int a = 0; a < 4; a++) {
+                old[a][0] = fp8q_raw_buffer_load_b128(rs, at0, (4 * r + a) * pitch, 0);
+                if constexpr (EXACT) old[a][1] = fp8q_raw_buffer_load_b128(rs, at1, (4 * r + a) * pitch, 0);
+            }
         }
 #pragma unroll
-        for (int a = 0; a < 4; a++)
+        for (int a = 0; a < 4; a++) {
+            if constexpr (EXACT) {
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                v4f v = {acc[a][4 * c][r], acc[a][4 * c + 1][r], acc[a][4 * c + 2][r], acc[a][4 * c + 3][r]};
-                if constexpr (ACCUMULATE) v += old[a][c];
-                if constexpr (kBf16)
-                    fp8q_raw_buffer_store_b64((i32x2){(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])}, rs,
-                                              c ? at1 : at0, (4 * r + a) * pitch, 0);
-                else
-                    fp8q_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rs, c ? at1 : at0, (4 * r + a) * pitch, 0);
+                for (int c = 0; c < 2; c++) {
+                    v4f v = {acc[a][4 * c][r], acc[a][4 * c + 1][r], acc[a][4 * c + 2][r], acc[a][4 * c + 3][r]};
+                    if constexpr (ACCUMULATE) v += __builtin_bit_cast(v4f, old[a][c]);
+                    fp8q_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rs, c ? at1 : at0, (4 * r + a) * pitch,
+                                               kNonTemporal);
+                }
+            } else {
+                i32x4 o;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    float x = acc[a][2 * c][r], y = acc[a][2 * c + 1][r];
+                    if constexpr (ACCUMULATE) {
+                        x += bf16_lo((uint32_t)old[a][0][c]);
+                        y += bf16_hi((uint32_t)old[a][0][c]);
+                    }
+                    o[c] = (int)pack_bf16x2(x, y);
+                }
+                fp8q_raw_buffer_store_b128(o, rs, at0, (4 * r + a) * pitch, kNonTemporal);
             }
+        }
     }
 }
 
@@ -345,7 +362,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
     const int wm = wave & 3, wn = wave >> 2;
     const int i = lane & 15, g = lane >> 4;
-    const int row = wm * 64 + 16 * g, col = wn * 128 + 4 * i;  // of the lane's results
+    const int row = wm * 64 + 16 * g, col = wn * 128 + (EXACT ? 4 : 8) * i;  // of the lane's results
     const int64_t ld = p.M;
     WgradTiles list;
     const int blocks = list.init(p, blockIdx.x + gridDim.x * lane);
@@ -365,12 +382,13 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     if (work == 0) return;
 
     // Copies: an instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, chunk l % 8, which holds logical chunk
-    // (l % 8) ^ wswz(row).  Rows past the operand are past its resource: their offset is at least nrow * ld.
-    int voff[4];
+    // (l % 8) ^ wswz(row) (cswz for columns).  Rows past the operand are past its resource: their offset is at least nrow * ld.
+    int avoff[4], bvoff[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const int r = wave * 32 + j * 8 + (lane >> 3);
-        voff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
+        avoff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
+        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz<EXACT>(r)) << 4);
     }
     // The stream's issue end: the block that is copied next.
     uint64_t ahead = work;  // tiles from its tile on
@@ -388,22 +406,24 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         const int a = wm * 64 + 4 * i;
         vsa = a < w.nrow ? a : kOutOfRange;
         vsb0 = col < w.ncol ? col : kOutOfRange;
-        vsb1 = col + 64 < w.ncol ? col + 64 : kOutOfRange;
+        vsb1 = EXACT ? (col + 64 < w.ncol ? col + 64 : kOutOfRange) : vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
         ahead &= ahead - 1;
     };
     auto copy_a = [&](int j, int slot) __attribute__((always_inline)) {
-        fp8q_raw_buffer_load_lds(ra, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, voff[j], ikb * 128, 0, 0);
+        fp8q_raw_buffer_load_lds(ra, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, avoff[j], ikb * 128, 0, 0);
     };
     auto copy_b = [&](int j, int slot) __attribute__((always_inline)) {
-        fp8q_raw_buffer_load_lds(rb, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, voff[j], ikb * 128, 0, 0);
+        fp8q_raw_buffer_load_lds(rb, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, bvoff[j], ikb * 128, 0, 0);
     };
     auto scales = [&](uint32_t (&s)[3]) __attribute__((always_inline)) {
         s[0] = __float_as_uint(fp8q_raw_buffer_load_f32(sra, vsa, ikb * (int)p.N, 0));
         s[1] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb0, ikb * (int)p.K, 0));
         s[2] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb1, ikb * (int)p.K, 0));
     };
-    const int frag0 = i * 512 + (((2 * g) ^ (i & 7) ^ (i >> 3)) << 4);  // chunk 2 g of row 4 i of a wave's; chunk 2 g + 1: ^ 16
-    const int fa_at = wm * 8192 + frag0, fb_at = wn * 16384 + frag0;
+    // Chunk 2 g of the lane's row of a wave's first subtile; chunk 2 g + 1: ^ 16.
+    const int chunk = ((2 * g) ^ (i & 7) ^ (i >> 3)) << 4;
+    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * (EXACT ? 512 : 1024) + chunk;
+    auto b_off = [](int b) { return EXACT ? (b / 4) * 8192 + (b & 3) * 128 : b * 128; };
     auto read8 = [&](int at0, int at1, int off) __attribute__((always_inline)) {  // 32 codes of a row: both chunks
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(lds + at0 + off);
         const u32x4 hi = *reinterpret_cast<const u32x4 *>(lds + at1 + off);
@@ -433,7 +453,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #pragma unroll
     for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
 #pragma unroll
-    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 128);
+    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b_off(b));
     auto mfma = [&](const uint32_t (&s)[3], auto a_, auto b_) __attribute__((always_inline)) {
         constexpr int a = decltype(a_)::value, b = decltype(b_)::value;
         acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a], fb[b & 3], acc[a][b], 0, 0, a, (int)s[0], b & 3,
@@ -455,7 +475,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         if (++ikb >= iKB) open_tile();  // (here, where no matrix instruction could be moved behind its branch)
         static_for<5>([&](auto b_) __attribute__((always_inline)) {
             constexpr int b = decltype(b_)::value;
-            fb[(b + 3) & 3] = read8(b0, b1, ((b + 3) / 4) * 8192 + ((b + 3) & 3) * 128);
+            fb[(b + 3) & 3] = read8(b0, b1, b_off(b + 3));
             if constexpr (b < 4) copy_a(b, last);
             static_for<4>([&](auto a_) __attribute__((always_inline)) {
                 mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
@@ -470,10 +490,10 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         for (int a = 0; a < 4; a++)
 #pragma unroll
             for (int b = 0; b < 5; b++) asm volatile("" : "+v"(acc[a][b]));
-        // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's 32 stores, which need
+        // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's stores, which need
         // not have reached memory.
         if (stored)
-            copies_barrier<39>();
+            copies_barrier<7 + kStores<EXACT>>();
         else
             copies_barrier<7>();
         __builtin_amdgcn_sched_barrier(0);
@@ -488,8 +508,8 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
             fa[a] = read8(na0, na1, a * 128);
             __builtin_amdgcn_sched_barrier(0);
         });
-        fb[1] = read8(nb0, nb1, 128);
-        fb[2] = read8(nb0, nb1, 256);
+        fb[1] = read8(nb0, nb1, b_off(1));
+        fb[2] = read8(nb0, nb1, b_off(2));
         slot = nA;
         stored = false;
     };
