@@ -514,11 +514,12 @@ int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, in
     if (need < 0 || ldg < K || ldg % 8 || ldh < K || ldh % 8) return FP8Q_ERR_SHAPE;
     if (w_dtype != FP8Q_OUT_BF16 && w_dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;
     if (K == 0 || (M == 0 && !gw)) return FP8Q_OK;
-    if (M > 0 && (!gy || !h || !w || !rstd || !gx || (gw && !workspace))) return FP8Q_ERR_NULL;
+    if (M > 0 && (!gy || !h || !w || !rstd || !gx || (gw && need > 0 && !workspace)))
+        return FP8Q_ERR_NULL;
     if (!aligned16(gy) || !aligned16(h) || !aligned16(w) || !aligned4(rstd) || !aligned16(gres) || !aligned16(gx) ||
         !aligned16(gw) || !aligned16(workspace))
         return FP8Q_ERR_ALIGN;
-    if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;
+    if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;  // (need may be 0)
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_rmsnorm_backward(gy, ldg, h, ldh, w, w_dtype == FP8Q_OUT_BF16, rstd, gres, M, K, gx, gw,
@@ -559,7 +560,8 @@ int fp8q_quant_act_128x1(const uint16_t *x, int64_t ld, int64_t T, int64_t K, co
 int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t *gh, int64_t ldg, int64_t M, int64_t F,
                                uint8_t *gq, float *gs, uint8_t *gqt, uint8_t *get, uint8_t *hqt, uint8_t *het,
                                void *stream) {
-    if (M < 0 || M > 0x7FFFFFFF || F < 0 || F % 128 || ldg < F || ldg % 8 || square_tiles(M, F) < 0)
+    if (M < 0 || M > 0x7FFFFFFF || F < 0 || F > kMaxWgrad || F % 128 || ldg < F || ldg > kMaxK || ldg % 8 ||
+        square_tiles(M, F) < 0)
         return FP8Q_ERR_SHAPE;
     if (M == 0 || F == 0) return FP8Q_OK;
     if (!q || !s || !gh || !gq || !gs || !gqt || !get || !hqt || !het) return FP8Q_ERR_NULL;

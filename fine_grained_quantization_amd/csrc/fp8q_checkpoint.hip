@@ -11,21 +11,14 @@
 namespace fp8q {
 namespace {
 
-constexpr int kThreads = 512;        // a thread holds 4 tokens x 8 channels of a tile
-constexpr int kR = 4, kG = kThreads / 16;
+constexpr int kThreads = 512;
 
-// Column maxima by token group, then (dead by then) the transposed codes: tile row = channel, 128 code bytes = 8 pieces of
-// 16 bytes; piece p of row r sits at p ^ ((r / 8) & 7), which spreads one store instruction's 4-byte writes over the banks.
-union ColumnTile {
-    uint32_t top[kG][128];
-    uint32_t tile[128 * 32];
-};
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 // 8 codes to fp32 values times s.
 __device__ __forceinline__ void decode8(const uint2 &d, float s, float *v) {
-    typedef float f2 __attribute__((ext_vector_type(2)));
-    const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.x, true);
-    const f2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.y, true);
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.x, true);
+    const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8((int)d.y, true);
     v[0] = a[0] * s; v[1] = a[1] * s; v[2] = b[0] * s; v[3] = b[1] * s;
     v[4] = c[0] * s; v[5] = c[1] * s; v[6] = e[0] * s; v[7] = e[1] * s;
 }
@@ -35,45 +28,86 @@ __device__ __forceinline__ void widen8(const u32x4 &d, float *v) {
     v[4] = bf16_lo(d.z); v[5] = bf16_hi(d.z); v[6] = bf16_lo(d.w); v[7] = bf16_hi(d.w);
 }
 
-__device__ __forceinline__ void column_tops(const float (&v)[kR][8], ColumnTile &sh, int g, int chunk) {
+// The scale bytes of 8 channels are maxima of the bytes of their values (pow2_byte grows with its argument), two to a dword; until
+// the last maximum they are 8 more than the bytes, and not yet cut off below.
+typedef u16x2 Bytes8[4];
+
+template <int R>
+__device__ __forceinline__ void column_bytes(const float (&v)[R][8], Bytes8 &e) {
+    uint32_t t[8];
 #pragma unroll
     for (int c = 0; c < 8; c++) {
-        uint32_t a = 0;
+        float a = __builtin_fabsf(v[0][c]);
 #pragma unroll
-        for (int j = 0; j < kR; j++) a = max(a, __float_as_uint(v[j][c]) & 0x7FFFFFFFu);
-        sh.top[g][chunk * 8 + c] = a;
+        for (int j = 1; j < R; j++) a = __builtin_fmaxf(a, __builtin_fabsf(v[j][c]));
+        t[c] = (__float_as_uint(a) + kPow2Round) >> 23;
     }
+#pragma unroll
+    for (int d = 0; d < 4; d++) e[d] = __builtin_bit_cast(u16x2, t[2 * d] | t[2 * d + 1] << 16);
 }
 
-// After column_tops and a barrier: threads [t0, t0 + 128) form the channels' scale bytes.
-__device__ __forceinline__ void column_scales(const ColumnTile &sh, uint8_t *bytes, uint8_t *et, int i) {
-    uint32_t a = 0;
+// Maxima over the lanes whose numbers differ in bits [log2 FROM, 6).
+template <int FROM>
+__device__ __forceinline__ void lanes_max(Bytes8 &e) {
 #pragma unroll
-    for (int g = 0; g < kG; g++) a = max(a, sh.top[g][i]);
-    const uint32_t e = pow2_byte(a);
-    bytes[i] = (uint8_t)e;
-    et[i] = (uint8_t)e;
+    for (int o = FROM; o < 64; o <<= 1)
+#pragma unroll
+        for (int d = 0; d < 4; d++)
+            e[d] = __builtin_elementwise_max(e[d], __builtin_bit_cast(u16x2, __shfl_xor(__builtin_bit_cast(int, e[d]), o, 64)));
 }
 
-// After the scales and a barrier: the thread's codes into the tile.
-__device__ __forceinline__ void column_codes(const float (&v)[kR][8], ColumnTile &sh, const uint8_t *bytes, int g,
-                                             int chunk) {
-    const uint2 b = *reinterpret_cast<const uint2 *>(bytes + chunk * 8);
+__device__ __forceinline__ u32x4 as_dwords(const Bytes8 &e) {
+    return (u32x4){__builtin_bit_cast(uint32_t, e[0]), __builtin_bit_cast(uint32_t, e[1]), __builtin_bit_cast(uint32_t, e[2]),
+                   __builtin_bit_cast(uint32_t, e[3])};
+}
+
+// The channels' bytes of all 8 waves' tokens.
+template <int CHUNKS>
+__device__ __forceinline__ void waves_max(const u32x4 (&all)[8][CHUNKS], int chunk, Bytes8 &e) {
 #pragma unroll
-    for (int c = 0; c < 8; c++) {
-        const float inv = pow2_inverse(((c < 4 ? b.x : b.y) >> (8 * (c & 3))) & 255u);
-        const uint32_t w = encode4(v[0][c] * inv, v[1][c] * inv, v[2][c] * inv, v[3][c] * inv);
-        sh.tile[(chunk * 8 + c) * 32 + (((g >> 2) ^ (chunk & 7)) << 2) + (g & 3)] = w;
+    for (int d = 0; d < 4; d++) e[d] = (u16x2){0, 0};
+#pragma unroll
+    for (int w = 0; w < 8; w++) {
+        const u32x4 o = all[w][chunk];
+#pragma unroll
+        for (int d = 0; d < 4; d++) {
+            const uint32_t x = o[d];  // (a bit cast of a vector's element would be one of its first)
+            e[d] = __builtin_elementwise_max(e[d], __builtin_bit_cast(u16x2, x));
+        }
     }
+#pragma unroll
+    for (int d = 0; d < 4; d++) e[d] = __builtin_elementwise_max(e[d], (u16x2){8, 8}) - (u16x2){8, 8};
 }
 
-// After another barrier: the tile's rows to the channel-major copy (rows ld bytes apart).
-__device__ __forceinline__ void column_store(const ColumnTile &sh, uint8_t *qt, int64_t ld, int t) {
+__device__ __forceinline__ uint2 packed_bytes(const Bytes8 &e) {
+    return (uint2){(uint32_t)e[0].x | (uint32_t)e[0].y << 8 | (uint32_t)e[1].x << 16 | (uint32_t)e[1].y << 24,
+                   (uint32_t)e[2].x | (uint32_t)e[2].y << 8 | (uint32_t)e[3].x << 16 | (uint32_t)e[3].y << 24};
+}
+
+// 4 codes of values times 2^-e, e a scale byte; the conversion applies the power.
+__device__ __forceinline__ uint32_t encode4_pow2(float a, float b, float c, float d, uint32_t byte) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float p = pow2_value(byte);
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, p, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, p, true);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Streaming store: the copies are larger than any cache where their time matters.
+__device__ __forceinline__ void store_stream16(void *p, const u32x4 &v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
+}
+
+// A tile of transposed codes: a row of 128 bytes a channel, 8 pieces of 16 bytes; piece p of channel c sits at p ^ ((c / 8) & 7),
+// which spreads one store instruction's writes (channels 8 apart) over the banks.
+template <int CHANNELS>
+__device__ __forceinline__ void column_store(const uint32_t (&tile)[CHANNELS * 32], uint8_t *qt, int64_t ld, int t) {
 #pragma unroll
-    for (int i = 0; i < 1024 / kThreads; i++) {
+    for (int i = 0; i < CHANNELS * 8 / kThreads; i++) {
         const int p = t + i * kThreads, row = p >> 3, piece = p & 7;
-        *reinterpret_cast<u32x4 *>(qt + row * ld + piece * 16) =
-            *reinterpret_cast<const u32x4 *>(&sh.tile[row * 32 + ((piece ^ ((row >> 3) & 7)) << 2)]);
+        store_stream16(qt + row * ld + piece * 16,
+                       *reinterpret_cast<const u32x4 *>(&tile[row * 32 + ((piece ^ ((row >> 3) & 7)) << 2)]));
     }
 }
 
@@ -85,41 +119,79 @@ struct TransposeArgs {
     uint8_t *qt, *et;
 };
 
+// A workgroup takes 128 tokens x 256 channels (the last may have 128): a thread 8 tokens x 8 channels.
 template <bool CODES>
 __global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs p) {
-    __shared__ __align__(16) ColumnTile sh;
-    __shared__ __align__(8) uint8_t bytes[128];
-    const int t = threadIdx.x, chunk = t & 15, g = t >> 4;
-    const int64_t KB = p.K >> 7, kb = blockIdx.x % KB, mb = blockIdx.x / KB;
-    float v[kR][8];
-#pragma unroll
-    for (int j = 0; j < kR; j++) {
-        const int64_t m = mb * 128 + g * kR + j;
-        int64_t tok = m < p.rows ? m : -1;
-        if (p.row_token != nullptr && tok >= 0) tok = p.row_token[m];
-        if (tok >= p.T) tok = -1;
-        if constexpr (CODES) {
-            uint2 d = {0u, 0u};
-            float s = 0.f;
-            if (tok >= 0) {
-                d = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(p.x) + tok * p.K + kb * 128 + chunk * 8);
-                s = p.s[kb * p.T + tok];
-            }
-            decode8(d, s, v[j]);
-        } else {
-            u32x4 d = {0u, 0u, 0u, 0u};
-            if (tok >= 0)
-                d = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.x) + tok * p.ld + kb * 128 + chunk * 8);
-            widen8(d, v[j]);
-        }
+    __shared__ __align__(16) uint32_t tile[256 * 32];
+    __shared__ u32x4 all[8][32];
+    const int t = threadIdx.x, lane = t & 63, chunk = t & 31, g = t >> 5;
+    // Rows in place: neighbours share rows.  Routed rows: each XCD (workgroups b with the same b % 8) takes an eighth of all
+    // tiles, channels by channels, so that a token's 256 channels come from its L2 after the first of the token's rows.
+    const int64_t KQ = (p.K + 255) >> 8, MB = p.cols >> 7;
+    int64_t kq, mb;
+    if (p.row_token == nullptr) {
+        kq = blockIdx.x % KQ;
+        mb = blockIdx.x / KQ;
+        if (mb >= MB) return;
+    } else {
+        const int64_t t8 = (KQ * MB + 7) / 8, i = (blockIdx.x % 8) * t8 + blockIdx.x / 8;
+        if (i >= KQ * MB) return;
+        kq = i / MB;
+        mb = i % MB;
     }
-    column_tops(v, sh, g, chunk);
+    const int64_t k0 = kq * 256;
+    const bool in = k0 + chunk * 8 < p.K;
+    int64_t tok[8];
+    const int64_t m0 = mb * 128 + g * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        tok[j] = m0 + j < p.rows && in ? m0 + j : -1;
+        if (p.row_token != nullptr && tok[j] >= 0) tok[j] = p.row_token[m0 + j];
+        if (tok[j] >= p.T) tok[j] = -1;
+    }
+    float v[8][8];
+    if constexpr (CODES) {
+        const uint8_t *x = static_cast<const uint8_t *>(p.x) + k0 + chunk * 8;
+        const float *s = p.s + (k0 / 128 + (chunk >> 4)) * p.T;
+        uint2 d[8];
+        float sc[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            d[j] = tok[j] >= 0 ? *reinterpret_cast<const uint2 *>(x + tok[j] * p.K) : (uint2){0u, 0u};
+            sc[j] = tok[j] >= 0 ? s[tok[j]] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) decode8(d[j], sc[j], v[j]);
+    } else {
+        const uint16_t *x = static_cast<const uint16_t *>(p.x) + k0 + chunk * 8;
+        u32x4 d[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            d[j] = tok[j] >= 0 ? *reinterpret_cast<const u32x4 *>(x + tok[j] * p.ld) : (u32x4){0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; j++) widen8(d[j], v[j]);
+    }
+    Bytes8 e;
+    column_bytes(v, e);
+    lanes_max<32>(e);
+    if (lane < 32) all[t >> 6][chunk] = as_dwords(e);
     __syncthreads();
-    if (t < 128) column_scales(sh, bytes, p.et + mb * p.K + kb * 128, t);
+    waves_max(all, chunk, e);
+    if (t < 32 && in) *reinterpret_cast<uint2 *>(p.et + mb * p.K + k0 + chunk * 8) = packed_bytes(e);
+#pragma unroll
+    for (int c = 0; c < 8; c++) {
+        const uint32_t byte = e[c / 2][c % 2];
+        const uint2 w = {encode4_pow2(v[0][c], v[1][c], v[2][c], v[3][c], byte),
+                         encode4_pow2(v[4][c], v[5][c], v[6][c], v[7][c], byte)};
+        *reinterpret_cast<uint2 *>(&tile[(chunk * 8 + c) * 32 + (((g >> 1) ^ (chunk & 7)) << 2) + (g & 1) * 2]) = w;
+    }
     __syncthreads();
-    column_codes(v, sh, bytes, g, chunk);
-    __syncthreads();
-    column_store(sh, p.qt + kb * 128 * p.cols + mb * 128, p.cols, t);
+    uint8_t *qt = p.qt + k0 * p.cols + mb * 128;
+    if (k0 + 256 <= p.K) {
+        column_store<256>(tile, qt, p.cols, t);
+    } else {
+        column_store<128>(reinterpret_cast<const uint32_t(&)[128 * 32]>(tile), qt, p.cols, t);
+    }
 }
 
 struct SwigluArgs {
@@ -132,77 +204,128 @@ struct SwigluArgs {
     uint8_t *gqt, *get, *hqt, *het;
 };
 
-// Codes of a token's 128 channels (the 16 lanes of a DPP row) and their scale.
-__device__ __forceinline__ void row_codes(const float (&v)[8], uint8_t *q, float *s, bool first) {
-    uint32_t a = 0;
+// Codes of a token's 128 channels (the 16 lanes of a DPP row) and their scale.  (The reciprocal is within an ulp, and the
+// values themselves are within a few.)
+__device__ __forceinline__ float row_codes(const float (&v)[8], uint8_t *q) {
+    float a = __builtin_fabsf(v[0]);
 #pragma unroll
-    for (int i = 0; i < 8; i++) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const float top = __uint_as_float(row16_max(a));
-    const float inv = top > 0.0f ? 448.0f / top : 0.0f;
+    for (int i = 1; i < 8; i++) a = __builtin_fmaxf(a, __builtin_fabsf(v[i]));
+    const float top = __uint_as_float(row16_max(__float_as_uint(a)));
+    const float inv = top > 0.0f ? 448.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
     uint2 o;
     o.x = encode4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     o.y = encode4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
     *reinterpret_cast<uint2 *>(q) = o;
-    if (first) *s = top / 448.0f;
+    return group_scale(top);
 }
 
-__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(SwigluArgs p) {
-    __shared__ __align__(16) ColumnTile sh[3];
-    __shared__ __align__(8) uint8_t bytes[3][128];
-    const int t = threadIdx.x, chunk = t & 15, g = t >> 4;
-    const int64_t FB = p.F >> 7, fb = blockIdx.x % FB, mb = blockIdx.x / FB;
-    float dx[kR][8], du[kR][8], h[kR][8];
+// Tiles of 128 tokens x 128 channels, a thread 4 tokens x 8 channels of each of the three results: 96 registers of them.  Two
+// workgroups to a CU would leave 128 registers and spill; so one walks tiles b, b + G, ..., with the next tile's inputs on the
+// way (40 more registers) while it computes.
+__global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs p) {
+    __shared__ __align__(16) uint32_t tile[3][128 * 32];
+    __shared__ __align__(16) uint32_t top[3][128];  // the channels' bytes, as in column_bytes
+    const int t = threadIdx.x, lane = t & 63, chunk = t & 15, g = t >> 4;
+    const uint32_t FB = (uint32_t)(p.F >> 7), tiles = FB * (uint32_t)(p.cols >> 7);  // (fewer than 2^23)
+    const int ldq = (int)(2 * p.F), ldg = (int)p.ldg;  // (offsets within a tile's 128 rows are 32 bits)
+    uint2 xq[4], uq[4];
+    u32x4 gq[4];
+    float sx[4], su[4];
+    auto load = [&](uint32_t i) __attribute__((always_inline)) {
+        const int64_t fb = i % FB, mb = i / FB;
+        const int rows = (int)(p.M - mb * 128 < 128 ? p.M - mb * 128 : 128);
+        const uint8_t *q0 = p.q + mb * 128 * 2 * p.F + fb * 128;
+        const uint16_t *g0 = p.gh + mb * 128 * p.ldg + fb * 128;
+        const float *sx0 = p.s + fb * p.M + mb * 128, *su0 = sx0 + FB * p.M;
 #pragma unroll
-    for (int j = 0; j < kR; j++) {
-        const int64_t m = mb * 128 + g * kR + j;
-        uint2 a = {0u, 0u}, b = {0u, 0u};
-        u32x4 d = {0u, 0u, 0u, 0u};
-        float sa = 0.f, sb = 0.f;
-        if (m < p.M) {
-            const uint8_t *row = p.q + m * 2 * p.F + fb * 128 + chunk * 8;
-            a = *reinterpret_cast<const uint2 *>(row);
-            b = *reinterpret_cast<const uint2 *>(row + p.F);
-            d = *reinterpret_cast<const u32x4 *>(p.gh + m * p.ldg + fb * 128 + chunk * 8);
-            sa = p.s[fb * p.M + m];
-            sb = p.s[(fb + FB) * p.M + m];
+        for (int j = 0; j < 4; j++) {
+            const int m = g * 4 + j, r = m < rows ? m : rows - 1;
+            xq[j] = *reinterpret_cast<const uint2 *>(q0 + (r * ldq + chunk * 8));
+            uq[j] = *reinterpret_cast<const uint2 *>(q0 + p.F + (r * ldq + chunk * 8));
+            gq[j] = load_stream16(g0 + (r * ldg + chunk * 8));
+            sx[j] = sx0[r];
+            su[j] = su0[r];
         }
-        float x[8], u[8], gr[8];
-        decode8(a, sa, x);
-        decode8(b, sb, u);
-        widen8(d, gr);
+    };
+    load(blockIdx.x);
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+        const int64_t fb = i % FB, mb = i / FB;
+        const int rows = (int)(p.M - mb * 128 < 128 ? p.M - mb * 128 : 128);
+        uint8_t *oq = p.gq + mb * 128 * 2 * p.F + fb * 128;
+        float *osx = p.gs + fb * p.M + mb * 128, *osu = osx + FB * p.M;
+        if (t < 384) top[t >> 7][t & 127] = 0;
+        uint2 x0[4], u0[4];
+        u32x4 g0[4];
+        float sx0[4], su0[4];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float e = __expf(-x[i]);
-            const float sg = 1.0f / (1.0f + e);
-            const float silu = x[i] * sg;
-            du[j][i] = gr[i] * silu;
-            dx[j][i] = gr[i] * u[i] * (sg * (1.0f + x[i] * (1.0f - sg)));
-            h[j][i] = silu * u[i];
+        for (int j = 0; j < 4; j++) {
+            const bool in = g * 4 + j < rows;  // (rows past the last one: zeros)
+            x0[j] = xq[j];
+            u0[j] = uq[j];
+            g0[j] = gq[j];
+            sx0[j] = in ? sx[j] : 0.f;
+            su0[j] = in ? su[j] : 0.f;
         }
-        if (m < p.M) {
-            uint8_t *q = p.gq + m * 2 * p.F + fb * 128 + chunk * 8;
-            row_codes(dx[j], q, p.gs + fb * p.M + m, chunk == 0);
-            row_codes(du[j], q + p.F, p.gs + (fb + FB) * p.M + m, chunk == 0);
+        if (i + gridDim.x < tiles) load(i + gridDim.x);
+        float v[3][4][8];  // dx, du, h
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int m = g * 4 + j;
+            float x[8], u[8], gr[8];
+            decode8(x0[j], sx0[j], x);
+            decode8(u0[j], su0[j], u);
+            widen8(g0[j], gr);
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                const float e = __builtin_amdgcn_exp2f(x[c] * -1.44269504088896340736f);
+                const float sg = __builtin_amdgcn_rcpf(1.0f + e);  // 0 where e is infinite
+                const float silu = x[c] * sg;
+                v[1][j][c] = gr[c] * silu;
+                v[2][j][c] = silu * u[c];
+                // p + x p (1 - p) = p + silu (1 - p)
+                v[0][j][c] = gr[c] * u[c] * __builtin_fmaf(silu, 1.0f - sg, sg);
+            }
+            if (m < rows) {
+                const float s0 = row_codes(v[0][j], oq + (m * ldq + chunk * 8));
+                const float s1 = row_codes(v[1][j], oq + p.F + (m * ldq + chunk * 8));
+                if (chunk == 0) {
+                    osx[m] = s0;
+                    osu[m] = s1;
+                }
+            }
         }
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            Bytes8 e;
+            column_bytes(v[k], e);
+            lanes_max<16>(e);
+            if (lane < 16) {
+#pragma unroll
+                for (int c = 0; c < 8; c++) atomicMax(&top[k][chunk * 8 + c], (uint32_t)e[c / 2][c % 2]);
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            uint32_t byte[8];
+#pragma unroll
+            for (int c = 0; c < 8; c++) byte[c] = max(top[k][chunk * 8 + c], 8u) - 8u;
+            uint8_t *et = k == 2 ? p.het + mb * p.F : p.get + mb * 2 * p.F + k * p.F;
+            if (t >> 4 == k)
+                *reinterpret_cast<uint2 *>(et + fb * 128 + chunk * 8) =
+                    (uint2){byte[0] | byte[1] << 8 | byte[2] << 16 | byte[3] << 24,
+                            byte[4] | byte[5] << 8 | byte[6] << 16 | byte[7] << 24};
+#pragma unroll
+            for (int c = 0; c < 8; c++)
+                tile[k][(chunk * 8 + c) * 32 + (((g >> 2) ^ (chunk & 7)) << 2) + (g & 3)] =
+                    encode4_pow2(v[k][0][c], v[k][1][c], v[k][2][c], v[k][3][c], byte[c]);
+        }
+        lds_barrier();
+        column_store<128>(tile[0], p.gqt + fb * 128 * p.cols + mb * 128, p.cols, t);
+        column_store<128>(tile[1], p.gqt + (p.F + fb * 128) * p.cols + mb * 128, p.cols, t);
+        column_store<128>(tile[2], p.hqt + fb * 128 * p.cols + mb * 128, p.cols, t);
     }
-    column_tops(dx, sh[0], g, chunk);
-    column_tops(du, sh[1], g, chunk);
-    column_tops(h, sh[2], g, chunk);
-    __syncthreads();
-    if (t < 384) {
-        const int k = t >> 7;
-        uint8_t *et = k == 0 ? p.get + mb * 2 * p.F + fb * 128 : k == 1 ? p.get + mb * 2 * p.F + p.F + fb * 128
-                                                                      : p.het + mb * p.F + fb * 128;
-        column_scales(sh[k], bytes[k], et, t & 127);
-    }
-    __syncthreads();
-    column_codes(dx, sh[0], bytes[0], g, chunk);
-    column_codes(du, sh[1], bytes[1], g, chunk);
-    column_codes(h, sh[2], bytes[2], g, chunk);
-    __syncthreads();
-    column_store(sh[0], p.gqt + fb * 128 * p.cols + mb * 128, p.cols, t);
-    column_store(sh[1], p.gqt + (p.F + fb * 128) * p.cols + mb * 128, p.cols, t);
-    column_store(sh[2], p.hqt + fb * 128 * p.cols + mb * 128, p.cols, t);
 }
 
 }  // namespace
@@ -212,7 +335,7 @@ hipError_t launch_transpose_128x1(const void *x, const float *s, bool codes, int
                                   hipStream_t stream) {
     const int64_t cols = (rows + 127) / 128 * 128;
     const TransposeArgs p = {x, s, ld, T, K, rows, cols, row_token, qt, et};
-    const dim3 grid((unsigned)(cols / 128 * (K / 128)));
+    const dim3 grid((unsigned)((cols / 128 * ((K + 255) / 256) + 7) / 8 * 8));
     if (codes)
         transpose_kernel<true><<<grid, kThreads, 0, stream>>>(p);
     else
@@ -225,7 +348,8 @@ hipError_t launch_swiglu_backward_quant(const uint8_t *q, const float *s, const 
                                         uint8_t *het, hipStream_t stream) {
     const int64_t cols = (M + 127) / 128 * 128;
     const SwigluArgs p = {q, s, gh, ldg, M, F, cols, gq, gs, gqt, get, hqt, het};
-    swiglu_backward_kernel<<<dim3((unsigned)(cols / 128 * (F / 128))), kThreads, 0, stream>>>(p);
+    const int64_t tiles = cols / 128 * (F / 128), wgs = cu_count();
+    swiglu_backward_kernel<<<dim3((unsigned)(tiles < wgs ? tiles : wgs)), kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 

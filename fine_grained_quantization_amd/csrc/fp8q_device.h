@@ -19,20 +19,13 @@ __device__ fp8q_i32x4 fp8q_raw_buffer_load_b128(fp8q_i32x4 rsrc, int voffset, in
 __device__ float fp8q_raw_buffer_load_f32(fp8q_i32x4 rsrc, int voffset, int soffset,
                                           int aux) __asm("llvm.amdgcn.raw.buffer.load.f32");
 
-typedef int fp8q_i32x2 __attribute__((ext_vector_type(2)));
-
-// LLVM's raw buffer stores from registers (16 / 8 bytes per lane); out-of-range lanes store nothing.
+// LLVM's raw buffer store from registers (16 bytes per lane); out-of-range lanes store nothing.
 __device__ void fp8q_raw_buffer_store_b128(fp8q_i32x4 data, fp8q_i32x4 rsrc, int voffset, int soffset,
                                            int aux) __asm("llvm.amdgcn.raw.buffer.store.v4i32");
-__device__ void fp8q_raw_buffer_store_b64(fp8q_i32x2 data, fp8q_i32x4 rsrc, int voffset, int soffset,
-                                          int aux) __asm("llvm.amdgcn.raw.buffer.store.v2i32");
-__device__ fp8q_i32x2 fp8q_raw_buffer_load_b64(fp8q_i32x4 rsrc, int voffset, int soffset,
-                                               int aux) __asm("llvm.amdgcn.raw.buffer.load.v2i32");
 
 namespace fp8q {
 
 typedef fp8q_i32x4 i32x4;
-typedef fp8q_i32x2 i32x2;
 
 // A byte offset past every buffer this library builds (they are < 2^31 bytes): loads there return 0
 // without touching memory.
@@ -115,9 +108,10 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
 
 // Power-of-two scales as E8M0 bytes (value 2^(byte - 127)).  The byte of a group whose largest magnitude has the fp32
 // pattern `amax`: the least power p with amax <= 448 p, at least 2^-127; 448 = 1.75 * 2^8.  An all-zero group gets 0.
+// (A mantissa past 0x600000 carries into the exponent when 0x1FFFFF is added.)
+constexpr uint32_t kPow2Round = 0x1FFFFFu;
 __device__ __forceinline__ uint32_t pow2_byte(uint32_t amax) {
-    const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return (uint32_t)(e < 0 ? 0 : e);
+    return max((amax + kPow2Round) >> 23, 8u) - 8u;
 }
 // The power itself, and its reciprocal (both exact in fp32 for bytes up to 248, the largest of a finite group; 2^-127 is
 // subnormal).

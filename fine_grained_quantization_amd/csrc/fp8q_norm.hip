@@ -181,8 +181,10 @@ hipError_t launch_norm(const NormArgs &p, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Gradients.  A workgroup takes rows m = b, b + G, ... and keeps, in registers, its columns' part of gw; the parts [G][K]
-// meet in the workspace and a second launch adds them in order.
+// Gradients.  A workgroup takes rows b, b + G, ..., the next row on the way while one is summed up, and keeps its columns'
+// weights and parts of gw in registers; the parts [G][K] meet in the workspace and a second launch adds them in order.
+// Up to kFewRows rows gw needs no parts: in the same launch further workgroups read g and h again (from the caches) and sum
+// up 64 columns each.
 // ---------------------------------------------------------------------------------------------------------
 
 struct NormGradArgs {
@@ -192,61 +194,91 @@ struct NormGradArgs {
     const float *rstd;
     uint16_t *gx;
     float *part;  // [G][K], or null
+    float *gw;    // for the further workgroups, from number G on
+    int64_t G;
 };
 
-// Columns [k0, k0 + 2048 CH) of a row are this pass's; K > 2048 CH takes the general kernel below.
-template <bool W_BF16, int CH>
-__global__ __launch_bounds__(256) void rmsnorm_backward_kernel(NormGradArgs p) {
-    __shared__ float part[2][4];
+constexpr int64_t kFewRows = 128;
+
+template <bool W_BF16, int THREADS, int CH>
+__global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs p) {
+    __shared__ float part[2][THREADS / 64];
+    __shared__ float sums[THREADS / 8][64];
     const int t = threadIdx.x;
-    const int64_t chunks = p.K >> 3, G = gridDim.x;
-    float gw[CH][8];
+    if (blockIdx.x >= p.G) {  // gw of 64 columns: 8 threads a row, 8 columns each
+        const int64_t k0 = (blockIdx.x - p.G) * 64 + (t & 7) * 8;
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int64_t m = t >> 3; m < p.M; m += THREADS / 8) {
+            const u32x4 g = *reinterpret_cast<const u32x4 *>(p.g + m * p.ldg + k0);
+            const u32x4 h = *reinterpret_cast<const u32x4 *>(p.h + m * p.ldh + k0);
+            const float r = p.rstd[m];
 #pragma unroll
-    for (int j = 0; j < CH; j++)
+            for (int i = 0; i < 8; i++) s[i] = __builtin_fmaf(elem(g, i) * elem(h, i), r, s[i]);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; i++) gw[j][i] = 0.f;
-    int flip = 0;
-    for (int64_t m = blockIdx.x; m < p.M; m += G, flip ^= 1) {
-        const float r = p.rstd[m];
-        u32x4 g[CH], h[CH];
+        for (int i = 0; i < 8; i++) sums[t >> 3][(t & 7) * 8 + i] = s[i];
+        __syncthreads();
+        if (t < 64) {
+            float sum = 0.f;
+            for (int i = 0; i < THREADS / 8; i++) sum += sums[i][t];
+            p.gw[(blockIdx.x - p.G) * 64 + t] = sum;
+        }
+        return;
+    }
+    const int64_t chunks = p.K >> 3;
+    float gw[CH][8], w[CH][8];
+    u32x4 g[CH], h[CH], a[CH];
+    auto load = [&](int64_t m) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-            const int64_t c = t + 256 * j;
-            const bool in = c < chunks;
-            g[j] = in ? *reinterpret_cast<const u32x4 *>(p.g + m * p.ldg + c * 8) : (u32x4){0u, 0u, 0u, 0u};
-            h[j] = in ? *reinterpret_cast<const u32x4 *>(p.h + m * p.ldh + c * 8) : (u32x4){0u, 0u, 0u, 0u};
+            const int64_t c = t + THREADS * j;
+            const bool in = m < p.M && c < chunks;
+            g[j] = in ? load_stream16(p.g + m * p.ldg + c * 8) : (u32x4){0u, 0u, 0u, 0u};
+            h[j] = in ? load_stream16(p.h + m * p.ldh + c * 8) : (u32x4){0u, 0u, 0u, 0u};
+            a[j] = in && p.gres != nullptr ? *reinterpret_cast<const u32x4 *>(p.gres + m * p.K + c * 8) : (u32x4){0u, 0u, 0u, 0u};
         }
+    };
+    constexpr bool kAhead = CH == 1;  // (more chunks a thread: their registers would not suffice for two rows)
+    if constexpr (kAhead) load(blockIdx.x);
+#pragma unroll
+    for (int j = 0; j < CH; j++) {
+        const int64_t c = t + THREADS * j;
+#pragma unroll
+        for (int i = 0; i < 8; i++) gw[j][i] = w[j][i] = 0.f;
+        if (c < chunks) load_w8<W_BF16>(p.w, c * 8, w[j]);
+    }
+    int flip = 0;
+    for (int64_t m = blockIdx.x; m < p.M; m += p.G, flip ^= 1) {
+        const float r = p.rstd[m];
+        if constexpr (!kAhead) load(m);
+        u32x4 g0[CH], h0[CH], a0[CH];
+#pragma unroll
+        for (int j = 0; j < CH; j++) {
+            g0[j] = g[j];
+            h0[j] = h[j];
+            a0[j] = a[j];
+        }
+        if constexpr (kAhead) load(m + p.G);
         float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < CH; j++) {
-            const int64_t c = t + 256 * j;
-            if (c < chunks) {
-                float w[8];
-                load_w8<W_BF16>(p.w, c * 8, w);
+        for (int j = 0; j < CH; j++)
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float gh = elem(g[j], i) * elem(h[j], i);
-                    gw[j][i] = __builtin_fmaf(gh, r, gw[j][i]);
-                    dot = __builtin_fmaf(gh, w[i], dot);
-                }
+            for (int i = 0; i < 8; i++) {
+                const float gh = elem(g0[j], i) * elem(h0[j], i);
+                gw[j][i] = __builtin_fmaf(gh, r, gw[j][i]);
+                dot = __builtin_fmaf(gh, w[j][i], dot);
             }
-        }
         // (two buffers in turn: a wave may reach the next row's sum while others still read this one)
-        const float sum = block_sum<256>(dot, part[flip]);
+        const float sum = block_sum<THREADS>(dot, part[flip]);
         const float f = r * r * sum / (float)p.K;
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-            const int64_t c = t + 256 * j;
+            const int64_t c = t + THREADS * j;
             if (c >= chunks) continue;
-            float w[8], o[8];
-            load_w8<W_BF16>(p.w, c * 8, w);
+            float o[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) o[i] = r * (elem(g[j], i) * w[i] - elem(h[j], i) * f);
-            if (p.gres != nullptr) {
-                const u32x4 a = *reinterpret_cast<const u32x4 *>(p.gres + m * p.K + c * 8);
-#pragma unroll
-                for (int i = 0; i < 8; i++) o[i] += elem(a, i);
-            }
+            for (int i = 0; i < 8; i++)
+                o[i] = elem(a0[j], i) + r * (elem(g0[j], i) * w[j][i] - elem(h0[j], i) * f);
             const u32x4 v = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
                              pack_bf16x2(o[6], o[7])};
             *reinterpret_cast<u32x4 *>(p.gx + m * p.K + c * 8) = v;
@@ -255,7 +287,7 @@ __global__ __launch_bounds__(256) void rmsnorm_backward_kernel(NormGradArgs p) {
     if (p.part != nullptr) {
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-            const int64_t c = t + 256 * j;
+            const int64_t c = t + THREADS * j;
             if (c < chunks) {
                 float *o = p.part + blockIdx.x * p.K + c * 8;
                 *reinterpret_cast<float4 *>(o) = make_float4(gw[j][0], gw[j][1], gw[j][2], gw[j][3]);
@@ -265,40 +297,39 @@ __global__ __launch_bounds__(256) void rmsnorm_backward_kernel(NormGradArgs p) {
     }
 }
 
-// gw[k] = sum over the G parts, in order.
-__global__ __launch_bounds__(256) void rmsnorm_gw_kernel(const float *__restrict__ part, int64_t G, int64_t K,
-                                                         float *__restrict__ gw) {
-    __shared__ float sum[8][32];
+// gw[k] = sum over the G parts: 32 threads a column, each its parts in order, then those sums in order.
+__global__ __launch_bounds__(1024) void rmsnorm_gw_kernel(const float *__restrict__ part, int64_t G, int64_t K,
+                                                          float *__restrict__ gw) {
+    __shared__ float sum[32][32];
     const int64_t k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int slice = threadIdx.x >> 5;
     float s = 0.f;
-    for (int64_t g = slice; g < G; g += 8) s += part[g * K + k];
+    for (int64_t g = slice; g < G; g += 32) s += part[g * K + k];
     sum[slice][threadIdx.x & 31] = s;
     __syncthreads();
     if (slice == 0) {
-        for (int i = 1; i < 8; i++) s += sum[i][threadIdx.x];
+        for (int i = 1; i < 32; i++) s += sum[i][threadIdx.x];
         gw[k] = s;
     }
 }
 
-int64_t norm_groups(int64_t M) {
-    const int64_t most = 2 * cu_count();
+// Two workgroups of 1024 threads to a CU, or eight of 256.
+int64_t norm_groups(int64_t M, int64_t K) {
+    const int64_t most = (K <= 2048 ? 8 : 2) * cu_count();
     return M < most ? M : most;
 }
 
 template <bool W_BF16>
-void launch_norm_backward(const NormGradArgs &p, int64_t G, hipStream_t stream) {
-    const dim3 grid((unsigned)G);
-    const int64_t ch = (p.K + 2047) / 2048;
-    if (ch <= 1) rmsnorm_backward_kernel<W_BF16, 1><<<grid, 256, 0, stream>>>(p);
-    else if (ch <= 2) rmsnorm_backward_kernel<W_BF16, 2><<<grid, 256, 0, stream>>>(p);
-    else if (ch <= 4) rmsnorm_backward_kernel<W_BF16, 4><<<grid, 256, 0, stream>>>(p);
-    else rmsnorm_backward_kernel<W_BF16, 10><<<grid, 256, 0, stream>>>(p);
+void launch_norm_backward(const NormGradArgs &p, hipStream_t stream) {
+    const dim3 grid((unsigned)(p.G + (p.gw != nullptr ? p.K / 64 : 0)));
+    if (p.K <= 2048) rmsnorm_backward_kernel<W_BF16, 256, 1><<<grid, 256, 0, stream>>>(p);
+    else if (p.K <= 8192) rmsnorm_backward_kernel<W_BF16, 1024, 1><<<grid, 1024, 0, stream>>>(p);
+    else rmsnorm_backward_kernel<W_BF16, 1024, 3><<<grid, 1024, 0, stream>>>(p);
 }
 
 }  // namespace
 
-int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) { return norm_groups(M) * K * 4; }
+int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K) { return M <= kFewRows ? 0 : norm_groups(M, K) * K * 4; }
 
 hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,
                                           const void *w, bool w_bf16, float eps, bool pow2, int64_t M, int64_t K,
@@ -312,15 +343,17 @@ hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const 
 hipError_t launch_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w,
                                    bool w_bf16, const float *rstd, const uint16_t *gres, int64_t M, int64_t K,
                                    uint16_t *gx, float *gw, float *workspace, hipStream_t stream) {
-    const int64_t G = norm_groups(M);
-    const NormGradArgs p = {gy, h, gres, ldg, ldh, M, K, w, rstd, gx, gw != nullptr ? workspace : nullptr};
-    if (M > 0) {
-        if (w_bf16) launch_norm_backward<true>(p, G, stream);
-        else launch_norm_backward<false>(p, G, stream);
+    const int64_t G = norm_groups(M, K);
+    const bool few = M <= kFewRows;
+    const NormGradArgs p = {gy, h, gres, ldg, ldh, M, K, w, rstd, gx, gw != nullptr && !few ? workspace : nullptr,
+                            few ? gw : nullptr, G};
+    if (M > 0 || gw != nullptr) {
+        if (w_bf16) launch_norm_backward<true>(p, stream);
+        else launch_norm_backward<false>(p, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (gw != nullptr) rmsnorm_gw_kernel<<<dim3((unsigned)(K / 32)), 256, 0, stream>>>(workspace, G, K, gw);
+    if (p.part != nullptr) rmsnorm_gw_kernel<<<dim3((unsigned)(K / 32)), 1024, 0, stream>>>(workspace, G, K, gw);
     return hipGetLastError();
 }
 

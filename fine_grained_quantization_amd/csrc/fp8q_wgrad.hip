@@ -238,6 +238,12 @@ __device__ __forceinline__ void copies_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// The same in every lane, but the compiler may not see that.
+__device__ __forceinline__ void uniform(i32x4 &r) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) r[k] = __builtin_amdgcn_readfirstlane(r[k]);
+}
+
 struct WgradTile {
     int e, n0, k0, nrow, ncol, b0, KB;  // expert, corner, rows and columns that exist, first block, blocks
 };
@@ -295,90 +301,80 @@ struct WgradTiles {
     }
 };
 
-// Columns of a wave's 128 in its 8 column subtiles, so that a lane's results are 16 bytes of consecutive columns: column
-// 8 i + b of them is column i of subtile b (bf16), or 64 (b / 4) + 4 i + b % 4 (fp32).  The chunks' places follow suit.
-template <bool EXACT>
-__device__ __forceinline__ int cswz(int r) {
-    return EXACT ? wswz(r) : ((r >> 3) & 7) ^ ((r >> 6) & 1);
-}
-
-// A lane holds row 4 (4 g + r) + a of a wave's 64, and of it columns 8 i .. 8 i + 7, or 4 i .. 4 i + 3 of either half: 16 lanes
-// store 256 consecutive bytes.  Streaming stores: 64 gradients of 2048 x 7168 that nothing else delays (one block each) take
-// 313 us with them (6.0 TB/s), 432 without.  kStores of them whatever the tile's size (those past it are out of range): the
-// waits for copies that are older than the stores count on it.
-template <bool EXACT>
-constexpr int kStores = EXACT ? 32 : 16;
-constexpr int kNonTemporal = 2;
-
-template <bool EXACT, bool ACCUMULATE>
-__device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const WgradTile &w, int row, int col) {
-    constexpr int kEl = EXACT ? 4 : 2;
-    const i32x4 rs = make_rsrc(static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl,
-                               (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * kEl));
-    // (rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there)
-    const int pitch = (int)p.K * kEl, at = row * pitch + col * kEl;
-    const int at0 = col < w.ncol ? at : kOutOfRange, at1 = col + 64 < w.ncol ? at + 64 * kEl : kOutOfRange;
-#pragma unroll
-    for (int r = 0; r < 4; r++) {
-        i32x4 old[4][2];
-        if constexpr (ACCUMULATE) {
-#pragma unroll
-            for (int a = 0; a < 4; a++) {
-                old[a][0] = fp8q_raw_buffer_load_b128(rs, at0, (4 * r + a) * pitch, 0);
-                if constexpr (EXACT) old[a][1] = fp8q_raw_buffer_load_b128(rs, at1, (4 * r + a) * pitch, 0);
-            }
-        }
-#pragma unroll
-        for (int a = 0; a < 4; a++) {
-            if constexpr (EXACT) {
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    v4f v = {acc[a][4 * c][r], acc[a][4 * c + 1][r], acc[a][4 * c + 2][r], acc[a][4 * c + 3][r]};
-                    if constexpr (ACCUMULATE) v += __builtin_bit_cast(v4f, old[a][c]);
-                    fp8q_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rs, c ? at1 : at0, (4 * r + a) * pitch,
-                                               kNonTemporal);
-                }
-            } else {
-                i32x4 o;
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    float x = acc[a][2 * c][r], y = acc[a][2 * c + 1][r];
-                    if constexpr (ACCUMULATE) {
-                        x += bf16_lo((uint32_t)old[a][0][c]);
-                        y += bf16_hi((uint32_t)old[a][0][c]);
-                    }
-                    o[c] = (int)pack_bf16x2(x, y);
-                }
-                fp8q_raw_buffer_store_b128(o, rs, at0, (4 * r + a) * pitch, kNonTemporal);
-            }
+// Zeros into the tiles of no tokens.
+template <int EL>
+__device__ __forceinline__ void wgrad_zero(const WgradArgs &p, const WgradTiles &list, uint64_t none, int tid, int threads) {
+    for (; none != 0; none &= none - 1) {
+        const WgradTile w = list.get(p, __builtin_ctzll(none));
+        uint8_t *c = static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * EL;
+        const int chunks = w.ncol * EL / 16;
+        for (int at = tid; at < w.nrow * chunks; at += threads) {
+            const int r = at / chunks;
+            *reinterpret_cast<u32x4 *>(c + r * p.K * EL + (at - r * chunks) * 16) = (u32x4){0u, 0u, 0u, 0u};
         }
     }
 }
 
-template <bool EXACT, bool ACCUMULATE>
+// bf16 results.  Columns of a wave's 128 in its 8 column subtiles: column 8 i + b of them is column i of subtile b, so that a
+// lane's results of a row are 16 bytes.  The chunks' places follow suit.
+__device__ __forceinline__ int cswz(int r) { return ((r >> 3) & 7) ^ ((r >> 6) & 1); }
+
+// Streaming stores: 64 gradients of 2048 x 7168 that nothing else delays (one block each) take 313 us with them (6.0 TB/s),
+// 432 without.
+constexpr int kNonTemporal = 2;
+// An offset past every tile's resource (256 rows of at most 2^22 bytes), also with a few rows added to it.
+constexpr int kFar = 0x60000000;
+
+// A lane holds, of row 4 (4 g + r) + a of a wave's 64, columns 8 i .. 8 i + 7: 16 lanes store 256 consecutive bytes.  kStores of
+// them whatever the tile's size (those past it are out of range): the waits for copies that are older than the stores count
+// on it.
+constexpr int kStores = 16;
+
+// Rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there.  The whole offset goes into
+// the lane's: behind a store with a scalar offset the compiler lets the next instruction overwrite the store's data registers,
+// and the store was seen to take the new value there.
+template <bool ACCUMULATE>
+__device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const WgradTile &w, int row, int col) {
+    const i32x4 rs = make_rsrc(static_cast<uint16_t *>(p.dw) + ((int64_t)w.e * p.N + w.n0) * p.K + w.k0,
+                               (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * 2));
+    const int pitch = (int)p.K * 2, at = col < w.ncol ? row * pitch + col * 2 : kFar;
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+        i32x4 old[4];
+        if constexpr (ACCUMULATE) {
+#pragma unroll
+            for (int a = 0; a < 4; a++) old[a] = fp8q_raw_buffer_load_b128(rs, at + (4 * r + a) * pitch, 0, 0);
+        }
+#pragma unroll
+        for (int a = 0; a < 4; a++) {
+            i32x4 o;
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                float x = acc[a][2 * c][r], y = acc[a][2 * c + 1][r];
+                if constexpr (ACCUMULATE) {
+                    x += bf16_lo((uint32_t)old[a][c]);
+                    y += bf16_hi((uint32_t)old[a][c]);
+                }
+                o[c] = (int)pack_bf16x2(x, y);
+            }
+            fp8q_raw_buffer_store_b128(o, rs, at + (4 * r + a) * pitch, 0, kNonTemporal);
+        }
+    }
+}
+
+template <bool ACCUMULATE>
 __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
     const int wm = wave & 3, wn = wave >> 2;
     const int i = lane & 15, g = lane >> 4;
-    const int row = wm * 64 + 16 * g, col = wn * 128 + (EXACT ? 4 : 8) * i;  // of the lane's results
+    const int row = wm * 64 + 16 * g, col = wn * 128 + 8 * i;  // of the lane's results
     const int64_t ld = p.M;
     WgradTiles list;
     const int blocks = list.init(p, blockIdx.x + gridDim.x * lane);
     const uint64_t work = __ballot(blocks > 0);
-    if constexpr (!ACCUMULATE) {  // tiles of no tokens: zeros
-        for (uint64_t none = __ballot(blocks == 0); none != 0; none &= none - 1) {
-            const WgradTile w = list.get(p, __builtin_ctzll(none));
-            constexpr int kEl = EXACT ? 4 : 2;
-            uint8_t *c = static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl;
-            const int chunks = w.ncol * kEl / 16;
-            for (int at = tid; at < w.nrow * chunks; at += 512) {
-                const int r = at / chunks;
-                *reinterpret_cast<u32x4 *>(c + r * p.K * kEl + (at - r * chunks) * 16) = (u32x4){0u, 0u, 0u, 0u};
-            }
-        }
-    }
+    if constexpr (!ACCUMULATE) wgrad_zero<2>(p, list, __ballot(blocks == 0), tid, 512);
     if (work == 0) return;
 
     // Copies: an instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, chunk l % 8, which holds logical chunk
@@ -388,7 +384,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     for (int j = 0; j < 4; j++) {
         const int r = wave * 32 + j * 8 + (lane >> 3);
         avoff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
-        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz<EXACT>(r)) << 4);
+        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz(r)) << 4);
     }
     // The stream's issue end: the block that is copied next.
     uint64_t ahead = work;  // tiles from its tile on
@@ -406,7 +402,11 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         const int a = wm * 64 + 4 * i;
         vsa = a < w.nrow ? a : kOutOfRange;
         vsb0 = col < w.ncol ? col : kOutOfRange;
-        vsb1 = EXACT ? (col + 64 < w.ncol ? col + 64 : kOutOfRange) : vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
+        vsb1 = vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
+        uniform(ra);
+        uniform(rb);
+        uniform(sra);
+        uniform(srb);
         ahead &= ahead - 1;
     };
     auto copy_a = [&](int j, int slot) __attribute__((always_inline)) {
@@ -422,8 +422,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     };
     // Chunk 2 g of the lane's row of a wave's first subtile; chunk 2 g + 1: ^ 16.
     const int chunk = ((2 * g) ^ (i & 7) ^ (i >> 3)) << 4;
-    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * (EXACT ? 512 : 1024) + chunk;
-    auto b_off = [](int b) { return EXACT ? (b / 4) * 8192 + (b & 3) * 128 : b * 128; };
+    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * 1024 + chunk;
     auto read8 = [&](int at0, int at1, int off) __attribute__((always_inline)) {  // 32 codes of a row: both chunks
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(lds + at0 + off);
         const u32x4 hi = *reinterpret_cast<const u32x4 *>(lds + at1 + off);
@@ -449,17 +448,30 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     int slot = 0;
     auto wrap = [](int s) { return s >= kSlots ? s - kSlots : s; };
     v4f acc[4][8];
+    bool stored = false;  // a tile's results were stored between this block and the one before
+    // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's stores, which need not have
+    // reached memory.  (The compiler would move matrix instructions before the branch behind it.)
+    auto next_block_is_there = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int b = 0; b < 5; b++) asm volatile("" : "+v"(acc[a][b]));
+        if (stored)
+            copies_barrier<7 + kStores>();
+        else
+            copies_barrier<7>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
     v8i fa[4], fb[4];
 #pragma unroll
     for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
 #pragma unroll
-    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b_off(b));
+    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 128);
     auto mfma = [&](const uint32_t (&s)[3], auto a_, auto b_) __attribute__((always_inline)) {
         constexpr int a = decltype(a_)::value, b = decltype(b_)::value;
         acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a], fb[b & 3], acc[a][b], 0, 0, a, (int)s[0], b & 3,
                                                                      (int)s[1 + b / 4]);
     };
-    bool stored = false;  // a tile's results were stored between this block and the one before
     // One block.  Phases 0 to 4: column subtile b by the 4 row subtiles, while subtile b + 3 is read.  Then everything of
     // the block is in registers: the barrier frees its slots, and subtiles 5 to 7 are taken row by row, each row's fragment
     // being replaced by the next block's when it is done.  (Every other phase runs backwards, so that one operand changes
@@ -475,7 +487,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         if (++ikb >= iKB) open_tile();  // (here, where no matrix instruction could be moved behind its branch)
         static_for<5>([&](auto b_) __attribute__((always_inline)) {
             constexpr int b = decltype(b_)::value;
-            fb[(b + 3) & 3] = read8(b0, b1, b_off(b + 3));
+            fb[(b + 3) & 3] = read8(b0, b1, (b + 3) * 128);
             if constexpr (b < 4) copy_a(b, last);
             static_for<4>([&](auto a_) __attribute__((always_inline)) {
                 mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
@@ -485,18 +497,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
             __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
             __builtin_amdgcn_sched_barrier(0);
         });
-        // (the compiler would move the phases above behind the branch)
-#pragma unroll
-        for (int a = 0; a < 4; a++)
-#pragma unroll
-            for (int b = 0; b < 5; b++) asm volatile("" : "+v"(acc[a][b]));
-        // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's stores, which need
-        // not have reached memory.
-        if (stored)
-            copies_barrier<7 + kStores<EXACT>>();
-        else
-            copies_barrier<7>();
-        __builtin_amdgcn_sched_barrier(0);
+        next_block_is_there();
         fb[0] = read8(nb0, nb1, 0);
         static_for<4>([&](auto a_) __attribute__((always_inline)) {
             constexpr int a = decltype(a_)::value;
@@ -508,8 +509,8 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
             fa[a] = read8(na0, na1, a * 128);
             __builtin_amdgcn_sched_barrier(0);
         });
-        fb[1] = read8(nb0, nb1, b_off(1));
-        fb[2] = read8(nb0, nb1, b_off(2));
+        fb[1] = read8(nb0, nb1, 128);
+        fb[2] = read8(nb0, nb1, 256);
         slot = nA;
         stored = false;
     };
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #define FP8Q_WGRAD_STEP(TURN)                                                                                  \
     block(Index<TURN>{});                                                                                      \
     if (--left == 0) {                                                                                         \
-        wgrad_store<EXACT, ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
+        wgrad_store<ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
         todo &= todo - 1;                                                                                      \
         if (todo == 0) break;                                                                                  \
         left = list.get(p, __builtin_ctzll(todo)).KB;                                      \
@@ -545,7 +546,7 @@ hipError_t launch_wgrad(WgradArgs p, hipStream_t stream) {
         p.n_tiles = tiles(p.N, 256);
         p.k_tiles = tiles(p.K, 256);
         const int64_t n = p.E * p.n_tiles * p.k_tiles, wgs = (n + 256 * kMostTiles - 1) / (256 * kMostTiles) * 256;
-        wgrad_stream_kernel<EXACT, ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
+        wgrad_stream_kernel<ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
     } else if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count()) {
         using S = WgradShape<4, 2, 2>;
         p.n_tiles = tiles(p.N, S::BM);

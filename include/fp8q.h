@@ -495,8 +495,8 @@ int fp8q_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t 
                                  int w_dtype, float eps, int pow2, int64_t M, int64_t K, uint16_t *h, uint16_t *y,
                                  uint8_t *q, float *s, float *rstd, void *stream);
 
-/* Bytes of device workspace for fp8q_rmsnorm_backward (never more for fewer
- * tokens of the same K).  Returns -1 for invalid sizes. */
+/* Bytes of device workspace for fp8q_rmsnorm_backward: 0 up to 128 tokens (never
+ * more for fewer tokens of the same K).  Returns -1 for invalid sizes. */
 int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
 
 /* The norm's gradients (the quantization is passed straight through):
@@ -511,7 +511,7 @@ int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
  *   gw   : fp32 [K] (output, or NULL, and then no workspace is needed); 0 when M is 0
  *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, its contents
  *          on entry do not matter (calls that share one must not overlap)
- * Requires K % 128 == 0, K <= 20480, ldg and ldh >= K and multiples of 8, M < 2^22.
+ * Requires K % 128 == 0, K <= 24576, ldg and ldh >= K and multiples of 8, M < 2^22.
  * fp32 arithmetic, sums in a fixed order.  Two launches at most. */
 int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w, int w_dtype,
                           const float *rstd, const uint16_t *gres, int64_t M, int64_t K, uint16_t *gx, float *gw,
@@ -541,8 +541,8 @@ int fp8q_quant_act_128x1(const uint16_t *x, int64_t ld, int64_t T, int64_t K, co
  *        fl32(amax / 448)
  *   gqt : E4M3 [2F, Mp], get : uint8 [Mp/128][2F]   (outputs) their backward copy
  *   hqt : E4M3 [F, Mp], het : uint8 [Mp/128][F]     (outputs) that of h
- * Requires F % 128 == 0, ldg >= F, ldg % 8 == 0, fewer than 2^23 tiles of 128 x 128;
- * s, gs 4-byte aligned, the rest to 16 bytes.  One launch. */
+ * Requires F % 128 == 0, F <= 2^20, F <= ldg <= 2^23, ldg % 8 == 0, fewer than 2^23 tiles of
+ * 128 x 128; s, gs 4-byte aligned, the rest to 16 bytes.  One launch. */
 int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t *gh, int64_t ldg, int64_t M, int64_t F,
                                uint8_t *gq, float *gs, uint8_t *gqt, uint8_t *get, uint8_t *hqt, uint8_t *het,
                                void *stream);

@@ -147,8 +147,8 @@ def check_grad(gx, gw, gy, h, w, rstd, gres):
 
 
 @pytest.mark.parametrize("w_dtype,residual", [(torch.bfloat16, True), (torch.float32, False)])
-@pytest.mark.parametrize("M,K", [(1, 128), (1, 7168), (37, 2048), (130, 2176), (700, 4096), (1500, 7168), (33, 8192), (40, 8320),
-                                 (5, 18432), (3, 20480)])
+@pytest.mark.parametrize("M,K", [(1, 128), (1, 7168), (37, 2048), (130, 2176), (128, 384), (129, 256), (700, 4096), (1500, 7168),
+                                 (33, 8192), (140, 8320), (5, 18432), (150, 24576), (3, 24576)])
 def test_norm_gradient(M, K, w_dtype, residual):
     h, gres, w = inputs(M, K, w_dtype, 3)
     gy = (1e-3 * torch.randn((M, K), device="cuda")).bfloat16()
