@@ -897,7 +897,7 @@ def fp8q_rmsnorm_backward(gy, h, w, rstd, gres=None, gx=None, gw=None, workspace
     """Gradients of the norm (the quantization is passed straight through).  ``gy`` and ``h`` bf16 [M, K] (rows may be
     strided), ``w`` bf16 or float32 [K], ``rstd`` float32 [M] (the forward call's), ``gres`` bf16 [M, K], the gradient that
     reaches ``h`` past the norm, or None -> ``(gx bf16 [M, K], gw float32 [K])``; ``gx`` is the gradient of ``x`` and of the
-    residual alike, and may be ``gres`` or ``gy``.  ``workspace``
+    residual alike, and may be ``gres`` (but not ``gy`` or ``h``).  ``workspace``
     (``fp8q_rmsnorm_backward_workspace_bytes(M, K)`` bytes) is allocated when not given."""
     dev = _GET_DEVICE()
     ldg = _here(gy, "gy", (torch.bfloat16,), 2, dev)

@@ -519,7 +519,8 @@ int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, in
     if (!aligned16(gy) || !aligned16(h) || !aligned16(w) || !aligned4(rstd) || !aligned16(gres) || !aligned16(gx) ||
         !aligned16(gw) || !aligned16(workspace))
         return FP8Q_ERR_ALIGN;
-    if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;  // (need may be 0)
+    if (M > 0 && (gx == gy || gx == h)) return FP8Q_ERR_OPTION;  // other workgroups may still read them
+    if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_rmsnorm_backward(gy, ldg, h, ldh, w, w_dtype == FP8Q_OUT_BF16, rstd, gres, M, K, gx, gw,

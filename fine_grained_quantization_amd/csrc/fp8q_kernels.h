@@ -92,7 +92,7 @@ hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const 
                                           uint16_t *h, uint16_t *y, uint8_t *q, float *s, float *rstd,
                                           hipStream_t stream);
 int64_t rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
-constexpr int64_t kMaxNormGradK = 24576;
+constexpr int64_t kMaxNormGradK = 20480;
 hipError_t launch_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w,
                                    bool w_bf16, const float *rstd, const uint16_t *gres, int64_t M, int64_t K,
                                    uint16_t *gx, float *gw, float *workspace, hipStream_t stream);

@@ -15,7 +15,26 @@ __device__ __forceinline__ float elem(const u32x4 &v, int i) {
     return i & 1 ? bf16_hi(d) : bf16_lo(d);
 }
 
-// 8 weights from element k on.
+// 8 weights from element k on, as they are (bf16) or widened to fp32.
+template <bool W_BF16>
+struct W8 {
+    u32x4 v[W_BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const void *w, int64_t k) {
+        if constexpr (W_BF16) {
+            v[0] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(w) + k);
+        } else {
+            v[0] = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(w) + k);
+            v[1] = *reinterpret_cast<const u32x4 *>(static_cast<const float *>(w) + k + 4);
+        }
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[W_BF16 ? 0 : 1] = (u32x4){0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (W_BF16) return elem(v[0], i);
+        const u32x4 &u = v[i < 4 ? 0 : 1];
+        return __uint_as_float((i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w);
+    }
+};
+
 template <bool W_BF16>
 __device__ __forceinline__ void load_w8(const void *w, int64_t k, float *f) {
     if constexpr (W_BF16) {
@@ -226,7 +245,8 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
         return;
     }
     const int64_t chunks = p.K >> 3;
-    float gw[CH][8], w[CH][8];
+    float gw[CH][8];
+    W8<W_BF16> w[CH];
     u32x4 g[CH], h[CH], a[CH];
     auto load = [&](int64_t m) __attribute__((always_inline)) {
 #pragma unroll
@@ -238,19 +258,18 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             a[j] = in && p.gres != nullptr ? *reinterpret_cast<const u32x4 *>(p.gres + m * p.K + c * 8) : (u32x4){0u, 0u, 0u, 0u};
         }
     };
-    constexpr bool kAhead = CH == 1;  // (more chunks a thread: their registers would not suffice for two rows)
-    if constexpr (kAhead) load(blockIdx.x);
+    load(blockIdx.x);
 #pragma unroll
     for (int j = 0; j < CH; j++) {
         const int64_t c = t + THREADS * j;
 #pragma unroll
-        for (int i = 0; i < 8; i++) gw[j][i] = w[j][i] = 0.f;
-        if (c < chunks) load_w8<W_BF16>(p.w, c * 8, w[j]);
+        for (int i = 0; i < 8; i++) gw[j][i] = 0.f;
+        w[j].zero();
+        if (c < chunks) w[j].load(p.w, c * 8);
     }
     int flip = 0;
     for (int64_t m = blockIdx.x; m < p.M; m += p.G, flip ^= 1) {
         const float r = p.rstd[m];
-        if constexpr (!kAhead) load(m);
         u32x4 g0[CH], h0[CH], a0[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) {
@@ -258,7 +277,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             h0[j] = h[j];
             a0[j] = a[j];
         }
-        if constexpr (kAhead) load(m + p.G);
+        load(m + p.G);
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < CH; j++)
@@ -266,7 +285,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             for (int i = 0; i < 8; i++) {
                 const float gh = elem(g0[j], i) * elem(h0[j], i);
                 gw[j][i] = __builtin_fmaf(gh, r, gw[j][i]);
-                dot = __builtin_fmaf(gh, w[j][i], dot);
+                dot = __builtin_fmaf(gh, w[j].at(i), dot);
             }
         // (two buffers in turn: a wave may reach the next row's sum while others still read this one)
         const float sum = block_sum<THREADS>(dot, part[flip]);
@@ -278,7 +297,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                o[i] = elem(a0[j], i) + r * (elem(g0[j], i) * w[j][i] - elem(h0[j], i) * f);
+                o[i] = elem(a0[j], i) + r * (elem(g0[j], i) * w[j].at(i) - elem(h0[j], i) * f);
             const u32x4 v = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
                              pack_bf16x2(o[6], o[7])};
             *reinterpret_cast<u32x4 *>(p.gx + m * p.K + c * 8) = v;
@@ -304,6 +323,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_gw_kernel(const float *__restric
     const int64_t k = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int slice = threadIdx.x >> 5;
     float s = 0.f;
+#pragma unroll 8
     for (int64_t g = slice; g < G; g += 32) s += part[g * K + k];
     sum[slice][threadIdx.x & 31] = s;
     __syncthreads();
@@ -313,9 +333,9 @@ __global__ __launch_bounds__(1024) void rmsnorm_gw_kernel(const float *__restric
     }
 }
 
-// Two workgroups of 1024 threads to a CU, or eight of 256.
+// As many workgroups as the CUs hold at once: four of 256 threads, two of 1024, or one of 512 with five chunks a thread.
 int64_t norm_groups(int64_t M, int64_t K) {
-    const int64_t most = (K <= 2048 ? 8 : 2) * cu_count();
+    const int64_t most = (K <= 2048 ? 4 : K <= 8192 ? 2 : 1) * cu_count();
     return M < most ? M : most;
 }
 
@@ -324,7 +344,7 @@ void launch_norm_backward(const NormGradArgs &p, hipStream_t stream) {
     const dim3 grid((unsigned)(p.G + (p.gw != nullptr ? p.K / 64 : 0)));
     if (p.K <= 2048) rmsnorm_backward_kernel<W_BF16, 256, 1><<<grid, 256, 0, stream>>>(p);
     else if (p.K <= 8192) rmsnorm_backward_kernel<W_BF16, 1024, 1><<<grid, 1024, 0, stream>>>(p);
-    else rmsnorm_backward_kernel<W_BF16, 1024, 3><<<grid, 1024, 0, stream>>>(p);
+    else rmsnorm_backward_kernel<W_BF16, 512, 5><<<grid, 512, 0, stream>>>(p);
 }
 
 }  // namespace

@@ -507,11 +507,11 @@ int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
  *   rstd : fp32 [M] as the forward call gave it
  *   gres : bf16 [M, K], contiguous, or NULL: the gradient that reaches h past the norm
  *   gx   : bf16 [M, K] (output), the gradient of x and of the residual alike; it may
- *          be gres, or gy when that is contiguous
+ *          be gres, and must overlap neither gy nor h (FP8Q_ERR_OPTION if it is one)
  *   gw   : fp32 [K] (output, or NULL, and then no workspace is needed); 0 when M is 0
  *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, its contents
  *          on entry do not matter (calls that share one must not overlap)
- * Requires K % 128 == 0, K <= 24576, ldg and ldh >= K and multiples of 8, M < 2^22.
+ * Requires K % 128 == 0, K <= 20480, ldg and ldh >= K and multiples of 8, M < 2^22.
  * fp32 arithmetic, sums in a fixed order.  Two launches at most. */
 int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, int64_t ldh, const void *w, int w_dtype,
                           const float *rstd, const uint16_t *gres, int64_t M, int64_t K, uint16_t *gx, float *gw,
