@@ -200,7 +200,7 @@ hipError_t launch_norm(const NormArgs &p, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------------------------------------
-// Gradients.  A workgroup takes rows b, b + G, ..., the next row on the way while one is summed up, and keeps its columns'
+// Gradients.  A workgroup takes rows b, b + G, ..., the next row on the way while one is summed up (K up to 8192), and keeps its columns'
 // weights and parts of gw in registers; the parts [G][K] meet in the workspace and a second launch adds them in order.
 // Up to kFewRows rows gw needs no parts: in the same launch further workgroups read g and h again (from the caches) and sum
 // up 64 columns each.
@@ -258,7 +258,8 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             a[j] = in && p.gres != nullptr ? *reinterpret_cast<const u32x4 *>(p.gres + m * p.K + c * 8) : (u32x4){0u, 0u, 0u, 0u};
         }
     };
-    load(blockIdx.x);
+    constexpr bool kAhead = CH == 1;  // (else the registers would not suffice for two rows)
+    if constexpr (kAhead) load(blockIdx.x);
 #pragma unroll
     for (int j = 0; j < CH; j++) {
         const int64_t c = t + THREADS * j;
@@ -270,6 +271,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
     int flip = 0;
     for (int64_t m = blockIdx.x; m < p.M; m += p.G, flip ^= 1) {
         const float r = p.rstd[m];
+        if constexpr (!kAhead) load(m);
         u32x4 g0[CH], h0[CH], a0[CH];
 #pragma unroll
         for (int j = 0; j < CH; j++) {
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             h0[j] = h[j];
             a0[j] = a[j];
         }
-        load(m + p.G);
+        if constexpr (kAhead) load(m + p.G);
         float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < CH; j++)
@@ -294,6 +296,8 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
         for (int j = 0; j < CH; j++) {
             const int64_t c = t + THREADS * j;
             if (c >= chunks) continue;
+            // (not to be kept in fp32 since the sum: those registers would be missing)
+            asm volatile("" : "+v"(g0[j]), "+v"(h0[j]));
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -333,7 +337,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_gw_kernel(const float *__restric
     }
 }
 
-// As many workgroups as the CUs hold at once: four of 256 threads, two of 1024, or one of 512 with five chunks a thread.
+// As many workgroups as the CUs hold at once: four of 256 threads, two of 1024, or one of those with three chunks a thread.
 int64_t norm_groups(int64_t M, int64_t K) {
     const int64_t most = (K <= 2048 ? 4 : K <= 8192 ? 2 : 1) * cu_count();
     return M < most ? M : most;
@@ -344,7 +348,7 @@ void launch_norm_backward(const NormGradArgs &p, hipStream_t stream) {
     const dim3 grid((unsigned)(p.G + (p.gw != nullptr ? p.K / 64 : 0)));
     if (p.K <= 2048) rmsnorm_backward_kernel<W_BF16, 256, 1><<<grid, 256, 0, stream>>>(p);
     else if (p.K <= 8192) rmsnorm_backward_kernel<W_BF16, 1024, 1><<<grid, 1024, 0, stream>>>(p);
-    else rmsnorm_backward_kernel<W_BF16, 512, 5><<<grid, 512, 0, stream>>>(p);
+    else rmsnorm_backward_kernel<W_BF16, 1024, 3><<<grid, 1024, 0, stream>>>(p);
 }
 
 }  // namespace
