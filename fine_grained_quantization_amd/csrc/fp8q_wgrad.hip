@@ -17,6 +17,7 @@ namespace fp8q {
 namespace {
 
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 template <int I>
@@ -64,6 +65,15 @@ __device__ __forceinline__ v8bf to_bf16(int d0, int d1, float s) {
     r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1]; r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
     return r;
 }
+
+// 16 codes times a power of two, in bf16.
+__device__ __forceinline__ void widen16(const v4i &d, float s, v8bf (&o)[2]) {
+    o[0] = to_bf16(d[0], d[1], s);
+    o[1] = to_bf16(d[2], d[3], s);
+}
+
+// The power of two of byte j of a scale dword.  (Byte 0, which stands for 2^-127, becomes 0: its group is all zeros.)
+__device__ __forceinline__ float power_of(uint32_t s, int j) { return __uint_as_float(((s >> (8 * j)) & 255u) << 23); }
 
 template <int WM, int WN, int CG>
 struct WgradShape {
@@ -315,9 +325,12 @@ __device__ __forceinline__ void wgrad_zero(const WgradArgs &p, const WgradTiles 
     }
 }
 
-// bf16 results.  Columns of a wave's 128 in its 8 column subtiles: column 8 i + b of them is column i of subtile b, so that a
-// lane's results of a row are 16 bytes.  The chunks' places follow suit.
-__device__ __forceinline__ int cswz(int r) { return ((r >> 3) & 7) ^ ((r >> 6) & 1); }
+// Columns of a wave's 128 in its 8 column subtiles, so that a lane's results of a row come 16 bytes at a time: column i of
+// subtile b is column 8 i + b of them (bf16), or 64 (b / 4) + 4 i + b % 4 (fp32).  The chunks' places follow suit.
+template <bool EXACT>
+__device__ __forceinline__ int cswz(int r) {
+    return EXACT ? wswz(r) : ((r >> 3) & 7) ^ ((r >> 6) & 1);
+}
 
 // Streaming stores: 64 gradients of 2048 x 7168 that nothing else delays (one block each) take 313 us with them (6.0 TB/s),
 // 432 without.
@@ -325,56 +338,72 @@ constexpr int kNonTemporal = 2;
 // An offset past every tile's resource (256 rows of at most 2^22 bytes), also with a few rows added to it.
 constexpr int kFar = 0x60000000;
 
-// A lane holds, of row 4 (4 g + r) + a of a wave's 64, columns 8 i .. 8 i + 7: 16 lanes store 256 consecutive bytes.  kStores of
-// them whatever the tile's size (those past it are out of range): the waits for copies that are older than the stores count
-// on it.
-constexpr int kStores = 16;
+// A lane holds, of row 4 (4 g + r) + a of a wave's 64, columns 8 i .. 8 i + 7, or 4 i .. 4 i + 3 of either half: 16 lanes store
+// 256 consecutive bytes.  kStores of them whatever the tile's size (those past it are out of range): the waits for copies that
+// are older than the stores count on it.
+template <bool EXACT>
+constexpr int kStores = EXACT ? 32 : 16;
 
 // Rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there.  The whole offset goes into
 // the lane's: behind a store with a scalar offset the compiler lets the next instruction overwrite the store's data registers,
 // and the store was seen to take the new value there.
-template <bool ACCUMULATE>
+template <bool EXACT, bool ACCUMULATE>
 __device__ __forceinline__ void wgrad_store(const WgradArgs &p, const v4f (&acc)[4][8], const WgradTile &w, int row, int col) {
-    const i32x4 rs = make_rsrc(static_cast<uint16_t *>(p.dw) + ((int64_t)w.e * p.N + w.n0) * p.K + w.k0,
-                               (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * 2));
-    const int pitch = (int)p.K * 2, at = col < w.ncol ? row * pitch + col * 2 : kFar;
+    constexpr int kEl = EXACT ? 4 : 2;
+    const i32x4 rs = make_rsrc(static_cast<uint8_t *>(p.dw) + (((int64_t)w.e * p.N + w.n0) * p.K + w.k0) * kEl,
+                               (uint64_t)(((w.nrow - 1) * p.K + w.ncol) * kEl));
+    const int pitch = (int)p.K * kEl, at = row * pitch + col * kEl;
+    const int at0 = col < w.ncol ? at : kFar, at1 = col + 64 < w.ncol ? at + 64 * kEl : kFar;
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-        i32x4 old[4];
+        i32x4 old[4][2];
         if constexpr (ACCUMULATE) {
 #pragma unroll
-            for (int a = 0; a < 4; a++) old[a] = fp8q_raw_buffer_load_b128(rs, at + (4 * r + a) * pitch, 0, 0);
+            for (int a = 0; a < 4; a++) {
+                old[a][0] = fp8q_raw_buffer_load_b128(rs, at0 + (4 * r + a) * pitch, 0, 0);
+                if constexpr (EXACT) old[a][1] = fp8q_raw_buffer_load_b128(rs, at1 + (4 * r + a) * pitch, 0, 0);
+            }
         }
 #pragma unroll
         for (int a = 0; a < 4; a++) {
-            i32x4 o;
+            if constexpr (EXACT) {
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                float x = acc[a][2 * c][r], y = acc[a][2 * c + 1][r];
-                if constexpr (ACCUMULATE) {
-                    x += bf16_lo((uint32_t)old[a][c]);
-                    y += bf16_hi((uint32_t)old[a][c]);
+                for (int c = 0; c < 2; c++) {
+                    v4f v = {acc[a][4 * c][r], acc[a][4 * c + 1][r], acc[a][4 * c + 2][r], acc[a][4 * c + 3][r]};
+                    if constexpr (ACCUMULATE) v += __builtin_bit_cast(v4f, old[a][c]);
+                    fp8q_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), rs, (c ? at1 : at0) + (4 * r + a) * pitch, 0,
+                                               kNonTemporal);
                 }
-                o[c] = (int)pack_bf16x2(x, y);
+            } else {
+                i32x4 o;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    float x = acc[a][2 * c][r], y = acc[a][2 * c + 1][r];
+                    if constexpr (ACCUMULATE) {
+                        x += bf16_lo((uint32_t)old[a][0][c]);
+                        y += bf16_hi((uint32_t)old[a][0][c]);
+                    }
+                    o[c] = (int)pack_bf16x2(x, y);
+                }
+                fp8q_raw_buffer_store_b128(o, rs, at0 + (4 * r + a) * pitch, 0, kNonTemporal);
             }
-            fp8q_raw_buffer_store_b128(o, rs, at + (4 * r + a) * pitch, 0, kNonTemporal);
         }
     }
 }
 
-template <bool ACCUMULATE>
+template <bool EXACT, bool ACCUMULATE>
 __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kSlots * kSlot];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
     const int wm = wave & 3, wn = wave >> 2;
     const int i = lane & 15, g = lane >> 4;
-    const int row = wm * 64 + 16 * g, col = wn * 128 + 8 * i;  // of the lane's results
+    const int row = wm * 64 + 16 * g, col = wn * 128 + (EXACT ? 4 : 8) * i;  // of the lane's results
     const int64_t ld = p.M;
     WgradTiles list;
     const int blocks = list.init(p, blockIdx.x + gridDim.x * lane);
     const uint64_t work = __ballot(blocks > 0);
-    if constexpr (!ACCUMULATE) wgrad_zero<2>(p, list, __ballot(blocks == 0), tid, 512);
+    if constexpr (!ACCUMULATE) wgrad_zero<EXACT ? 4 : 2>(p, list, __ballot(blocks == 0), tid, 512);
     if (work == 0) return;
 
     // Copies: an instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, chunk l % 8, which holds logical chunk
@@ -384,7 +413,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     for (int j = 0; j < 4; j++) {
         const int r = wave * 32 + j * 8 + (lane >> 3);
         avoff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
-        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz(r)) << 4);
+        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz<EXACT>(r)) << 4);
     }
     // The stream's issue end: the block that is copied next.
     uint64_t ahead = work;  // tiles from its tile on
@@ -402,7 +431,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         const int a = wm * 64 + 4 * i;
         vsa = a < w.nrow ? a : kOutOfRange;
         vsb0 = col < w.ncol ? col : kOutOfRange;
-        vsb1 = vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
+        vsb1 = EXACT ? (col + 64 < w.ncol ? col + 64 : kOutOfRange) : vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
         uniform(ra);
         uniform(rb);
         uniform(sra);
@@ -422,7 +451,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     };
     // Chunk 2 g of the lane's row of a wave's first subtile; chunk 2 g + 1: ^ 16.
     const int chunk = ((2 * g) ^ (i & 7) ^ (i >> 3)) << 4;
-    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * 1024 + chunk;
+    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * (EXACT ? 512 : 1024) + chunk;
     auto read8 = [&](int at0, int at1, int off) __attribute__((always_inline)) {  // 32 codes of a row: both chunks
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(lds + at0 + off);
         const u32x4 hi = *reinterpret_cast<const u32x4 *>(lds + at1 + off);
@@ -431,6 +460,11 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         f[4] = (int)hi[0]; f[5] = (int)hi[1]; f[6] = (int)hi[2]; f[7] = (int)hi[3];
         return f;
     };
+
+    auto read4 = [&](int at, int off) __attribute__((always_inline)) {  // 16 codes of a row: a chunk
+        return *reinterpret_cast<const v4i *>(lds + at + off);
+    };
+    auto b_off = [](int b) { return EXACT ? (b / 4) * 8192 + (b & 3) * 128 : b * 128; };
 
     uint32_t sc[2][3];  // block s's are in sc[s % 2]
     open_tile();
@@ -455,18 +489,29 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #pragma unroll
         for (int a = 0; a < 4; a++)
 #pragma unroll
-            for (int b = 0; b < 5; b++) asm volatile("" : "+v"(acc[a][b]));
+            for (int b = 0; b < (EXACT ? 6 : 5); b++) asm volatile("" : "+v"(acc[a][b]));
         if (stored)
-            copies_barrier<7 + kStores>();
+            copies_barrier<7 + kStores<EXACT>>();
         else
             copies_barrier<7>();
         __builtin_amdgcn_sched_barrier(0);
     };
-    v8i fa[4], fb[4];
+    // Fragments that are alive between blocks: for bf16 the codes of 4 rows (32 of each) and of up to 4 columns; for fp32
+    // the 4 rows widened (16 codes of each) and the codes of up to 3 columns.
+    v8i fa[EXACT ? 1 : 4], fb[EXACT ? 1 : 4];
+    v8bf wide[EXACT ? 4 : 1][2];
+    v4i raw[EXACT ? 3 : 1];
+    if constexpr (!EXACT) {
 #pragma unroll
-    for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
+        for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
 #pragma unroll
-    for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 128);
+        for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b_off(b));
+    } else {
+#pragma unroll
+        for (int b = 0; b < 2; b++) raw[b] = read4(kSlot + fb_at, b_off(b));
+#pragma unroll
+        for (int a = 0; a < 4; a++) widen16(read4(fa_at, a * 128), power_of(sc[0][0], a), wide[a]);
+    }
     auto mfma = [&](const uint32_t (&s)[3], auto a_, auto b_) __attribute__((always_inline)) {
         constexpr int a = decltype(a_)::value, b = decltype(b_)::value;
         acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa[a], fb[b & 3], acc[a][b], 0, 0, a, (int)s[0], b & 3,
@@ -485,32 +530,80 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         const int na0 = nA * kSlot + fa_at, na1 = na0 ^ 16;
         scales(sc[turn ^ 1]);
         if (++ikb >= iKB) open_tile();  // (here, where no matrix instruction could be moved behind its branch)
-        static_for<5>([&](auto b_) __attribute__((always_inline)) {
-            constexpr int b = decltype(b_)::value;
-            fb[(b + 3) & 3] = read8(b0, b1, (b + 3) * 128);
-            if constexpr (b < 4) copy_a(b, last);
+        if constexpr (!EXACT) {
+            static_for<5>([&](auto b_) __attribute__((always_inline)) {
+                constexpr int b = decltype(b_)::value;
+                fb[(b + 3) & 3] = read8(b0, b1, b_off(b + 3));
+                if constexpr (b < 4) copy_a(b, last);
+                static_for<4>([&](auto a_) __attribute__((always_inline)) {
+                    mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
+                });
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                if constexpr (b < 4) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            next_block_is_there();
+            fb[0] = read8(nb0, nb1, 0);
             static_for<4>([&](auto a_) __attribute__((always_inline)) {
-                mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
+                constexpr int a = decltype(a_)::value;
+                copy_b(a, slot);
+                static_for<3>([&](auto c_) __attribute__((always_inline)) {
+                    constexpr int c = decltype(c_)::value;
+                    mfma(s, a_, Index<5 + ((a & 1) ? 2 - c : c)>{});
+                });
+                fa[a] = read8(na0, na1, a * 128);
+                __builtin_amdgcn_sched_barrier(0);
             });
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            if constexpr (b < 4) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        });
-        next_block_is_there();
-        fb[0] = read8(nb0, nb1, 0);
-        static_for<4>([&](auto a_) __attribute__((always_inline)) {
-            constexpr int a = decltype(a_)::value;
-            copy_b(a, slot);
-            static_for<3>([&](auto c_) __attribute__((always_inline)) {
-                constexpr int c = decltype(c_)::value;
-                mfma(s, a_, Index<5 + ((a & 1) ? 2 - c : c)>{});
+            fb[1] = read8(nb0, nb1, b_off(1));
+            fb[2] = read8(nb0, nb1, b_off(2));
+        } else {
+            const int a1 = (slot * kSlot + fa_at) ^ 16;
+            static_for<2>([&](auto half_) __attribute__((always_inline)) {
+                constexpr int half = decltype(half_)::value;
+                // (the compiler is not to keep the powers of one half for the other: their registers would be missing)
+                asm volatile("" : "+v"(s[0]), "+v"(s[1]), "+v"(s[2]));
+                v4i rows[4];
+                v8bf cols[2][2];
+                widen16(raw[0], power_of(s[1], 0), cols[0]);
+                static_for<6>([&](auto b_) __attribute__((always_inline)) {
+                    constexpr int b = decltype(b_)::value;
+                    raw[(b + 2) % 3] = read4(half ? b1 : b0, b_off(b + 2));
+                    if constexpr (half == 0 && b < 4) copy_a(b, last);
+                    if constexpr (half == 0 && b > 3) rows[b - 4] = read4(a1, (b - 4) * 128);
+                    // (the next column's codes are widened beside this one's products)
+                    widen16(raw[(b + 1) % 3], power_of(s[1 + (b + 1) / 4], (b + 1) & 3), cols[(b + 1) & 1]);
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+#pragma unroll
+                        for (int a = 0; a < 4; a++)
+                            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[a][h], cols[b & 1][h], acc[a][b], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                if constexpr (half == 1) {
+                    next_block_is_there();
+#pragma unroll
+                    for (int a = 0; a < 2; a++) rows[a] = read4(na0, a * 128);
+                }
+                widen16(raw[7 % 3], power_of(s[2], 3), cols[1]);  // columns 6 and 7
+#pragma unroll
+                for (int b = 0; b < 2; b++) raw[b] = read4(half ? nb0 : b1, b_off(b));
+                __builtin_amdgcn_sched_barrier(0);
+                static_for<4>([&](auto a_) __attribute__((always_inline)) {
+                    constexpr int a = decltype(a_)::value;
+                    if constexpr (half == 1) copy_b(a, slot);
+                    if constexpr (a < 2) rows[a + 2] = read4(half ? na0 : a1, (a + 2) * 128);
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++)
+                            acc[a][6 + c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[a][h], cols[c][h], acc[a][6 + c], 0, 0, 0);
+                    widen16(rows[a], power_of(half ? sc[turn ^ 1][0] : s[0], a), wide[a]);
+                    if constexpr (half == 1) asm volatile("" : "+v"(wide[a][0]), "+v"(wide[a][1]));  // (not behind the branch)
+                    __builtin_amdgcn_sched_barrier(0);
+                });
             });
-            fa[a] = read8(na0, na1, a * 128);
-            __builtin_amdgcn_sched_barrier(0);
-        });
-        fb[1] = read8(nb0, nb1, 128);
-        fb[2] = read8(nb0, nb1, 256);
+        }
         slot = nA;
         stored = false;
     };
@@ -525,7 +618,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #define FP8Q_WGRAD_STEP(TURN)                                                                                  \
     block(Index<TURN>{});                                                                                      \
     if (--left == 0) {                                                                                         \
-        wgrad_store<ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
+        wgrad_store<EXACT, ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
         todo &= todo - 1;                                                                                      \
         if (todo == 0) break;                                                                                  \
         left = list.get(p, __builtin_ctzll(todo)).KB;                                      \
@@ -542,11 +635,11 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 template <bool EXACT, bool ACCUMULATE>
 hipError_t launch_wgrad(WgradArgs p, hipStream_t stream) {
     auto tiles = [](int64_t n, int64_t t) { return (n + t - 1) / t; };
-    if (!EXACT && p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count() / 2) {
+    if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count() / 2) {
         p.n_tiles = tiles(p.N, 256);
         p.k_tiles = tiles(p.K, 256);
         const int64_t n = p.E * p.n_tiles * p.k_tiles, wgs = (n + 256 * kMostTiles - 1) / (256 * kMostTiles) * 256;
-        wgrad_stream_kernel<ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
+        wgrad_stream_kernel<EXACT, ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
     } else if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count()) {
         using S = WgradShape<4, 2, 2>;
         p.n_tiles = tiles(p.N, S::BM);
