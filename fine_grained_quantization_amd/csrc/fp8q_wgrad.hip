@@ -38,6 +38,8 @@ struct WgradArgs {
     const int32_t *off;  // null: one product over all M columns
     int64_t M, N, K, E;
     int64_t n_tiles, k_tiles;
+    float *sums;  // [parts][N][K]
+    int64_t parts;
 };
 
 // Rows in groups of 64: row 4 i + j of a group is row i of the group's 16-row subtile j.  So a lane's scale bytes of the 4
@@ -75,38 +77,65 @@ __device__ __forceinline__ void widen16(const v4i &d, float s, v8bf (&o)[2]) {
 // The power of two of byte j of a scale dword.  (Byte 0, which stands for 2^-127, becomes 0: its group is all zeros.)
 __device__ __forceinline__ float power_of(uint32_t s, int j) { return __uint_as_float(((s >> (8 * j)) & 255u) << 23); }
 
-template <int WM, int WN, int CG>
-struct WgradShape {
-    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-    static constexpr int BM = 64 * WM, BN = 64 * CG * WN;
-    static constexpr int kScale = (BM + BN) * 128;           // scale bytes behind the codes: rows, then columns
-    static constexpr int kStage = kScale + 1024;
-    static constexpr int kCopyA = BM / 8 / kWaves, kCopyB = BN / 8 / kWaves;
+// 4 results as they are in memory, and in fp32.
+template <bool BF16>
+struct Four {
+    uint2 lo, hi;
+    __device__ __forceinline__ void load(const void *c, int64_t idx) {
+        const uint2 *at = reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(c) + idx * (BF16 ? 2 : 4));
+        lo = at[0];
+        if constexpr (!BF16) hi = at[1];
+    }
+    __device__ __forceinline__ v4f value() const {
+        if constexpr (BF16) return (v4f){bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
+        return (v4f){__uint_as_float(lo.x), __uint_as_float(lo.y), __uint_as_float(hi.x), __uint_as_float(hi.y)};
+    }
 };
 
-// One tile of BM rows (n) x BN columns (k) by WM x WN waves of 64 x 64 CG.
-template <bool EXACT, bool ACCUMULATE, int WM, int WN, int CG>
-__global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(WgradArgs p) {
-    using S = WgradShape<WM, WN, CG>;
-    __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStage];
-    __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStage];
+template <bool BF16>
+__device__ __forceinline__ v4f load4(const void *c, int64_t idx) {
+    Four<BF16> f;
+    f.load(c, idx);
+    return f.value();
+}
+
+// ---------------------------------------------------------------------------------------------------------
+// Small results: 128 x 128 tiles by 4 waves of 64 x 64, two workgroups to a CU, blocks of 128 tokens through two LDS stages.
+// PARTS: the blocks are dealt to several workgroups a tile, whose sums go to the workspace [parts][N][K] in fp32 and are added
+// in order by a second launch.
+// ---------------------------------------------------------------------------------------------------------
+
+constexpr int kTile = 128;
+constexpr int kScaleAt = 2 * kTile * 128, kStage = kScaleAt + 1024;  // a stage: rows, columns, and the scale bytes of both
+
+enum Store { kStoreBf16, kStoreF32, kAddBf16, kAddF32, kParts };
+
+template <bool EXACT, int STORE>
+__global__ __launch_bounds__(256, 2) void wgrad_small_kernel(WgradArgs p) {
+    __shared__ __attribute__((aligned(1024))) uint8_t stage0[kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage1[kStage];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wn = wave / WM;
+    const int wm = wave & 1, wn = wave >> 1;
     const int i = lane & 15, g = lane >> 4;
     const int64_t per = p.n_tiles * p.k_tiles;
-    // (dense: the XCD order spreads the tiles over all workgroups of a round, so blockIdx may be past the number of tiles)
-    const int64_t e = p.off == nullptr ? 0 : blockIdx.x / per;
-    int64_t nt, kt;
-    if (p.off == nullptr) {
+    int64_t e = 0, part = 0, nt, kt;
+    if constexpr (STORE == kParts) {  // a tile's parts are far apart, neighbours share an operand
+        part = blockIdx.x / per;
+        const int64_t r = blockIdx.x - part * per;
+        nt = r / p.k_tiles;
+        kt = r % p.k_tiles;
+    } else if (p.off == nullptr) {
+        // (the XCD order spreads the tiles over all workgroups of a round, so blockIdx may be past the number of tiles)
         if (!dense_tile_at(xcd_order(blockIdx.x), p.n_tiles, p.k_tiles, nt, kt)) return;
     } else {
+        e = blockIdx.x / per;
         if (e >= p.E) return;
         const int64_t r = blockIdx.x - e * per;
         nt = r / p.k_tiles;
         kt = r % p.k_tiles;
     }
-    const int64_t n0 = nt * S::BM, k0 = kt * S::BN;
+    const int64_t n0 = nt * kTile, k0 = kt * kTile;
     // the segment, cut to [0, M) and to whole blocks
     int64_t lo = 0, hi = p.M;
     if (p.off != nullptr) {
@@ -115,22 +144,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(WgradArgs p) {
         lo = lo < 0 ? 0 : (lo > p.M ? p.M : lo & ~127);
         hi = hi < lo ? lo : (hi > p.M ? p.M : hi & ~127);
     }
+    if constexpr (STORE == kParts) {
+        const int64_t each = (p.M / 128 + p.parts - 1) / p.parts * 128;
+        lo = part * each < p.M ? part * each : p.M;
+        hi = lo + each < p.M ? lo + each : p.M;
+    }
     const int b0 = __builtin_amdgcn_readfirstlane((int)(lo >> 7));
     const int KB = __builtin_amdgcn_readfirstlane((int)((hi - lo) >> 7));
     const int64_t ld = p.M;
-    const int64_t nrow = p.N - n0 < S::BM ? p.N - n0 : S::BM, ncol = p.K - k0 < S::BN ? p.K - k0 : S::BN;
+    const int64_t nrow = p.N - n0 < kTile ? p.N - n0 : kTile, ncol = p.K - k0 < kTile ? p.K - k0 : kTile;
     const i32x4 ra = make_rsrc(p.gt + n0 * ld + (int64_t)b0 * 128, (uint64_t)((nrow - 1) * ld + (int64_t)KB * 128));
     const i32x4 rb = make_rsrc(p.xt + k0 * ld + (int64_t)b0 * 128, (uint64_t)((ncol - 1) * ld + (int64_t)KB * 128));
-    int av[S::kCopyA], bv[S::kCopyB];
+    int av[4], bv[4];
 #pragma unroll
-    for (int j = 0; j < S::kCopyA; j++) {
-        const int r = (wave * S::kCopyA + j) * 8 + (lane >> 3);
-        av[j] = r < nrow ? (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4) : kOutOfRange;
-    }
-#pragma unroll
-    for (int j = 0; j < S::kCopyB; j++) {
-        const int r = (wave * S::kCopyB + j) * 8 + (lane >> 3);
-        bv[j] = r < ncol ? (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4) : kOutOfRange;
+    for (int j = 0; j < 4; j++) {
+        const int r = (wave * 4 + j) * 8 + (lane >> 3);
+        const int at = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
+        av[j] = r < nrow ? at : kOutOfRange;
+        bv[j] = r < ncol ? at : kOutOfRange;
     }
     // Block kb's codes and scale bytes into a stage; past the last block nothing is read (zeros land).
     auto issue = [&](uint8_t *st, int kb) __attribute__((always_inline)) {
@@ -142,94 +173,96 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void wgrad_kernel(WgradArgs p) {
             const int64_t n = rows ? nrow : ncol;
             const i32x4 rs = make_rsrc((rows ? p.eg + (int64_t)(b0 + kb) * p.N + n0 : p.ex + (int64_t)(b0 + kb) * p.K + k0),
                                        in ? (uint64_t)n : 0);
-            fp8q_raw_buffer_load_lds(rs, (lds_ptr)(st + S::kScale + wave * 512), 4, lane * 4, 0, 0, 0);
+            fp8q_raw_buffer_load_lds(rs, (lds_ptr)(st + kScaleAt + wave * 512), 4, lane * 4, 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < S::kCopyA; j++)
-            fp8q_raw_buffer_load_lds(ta, (lds_ptr)(st + (wave * S::kCopyA + j) * 1024), 16, av[j], so, 0, 0);
+        for (int j = 0; j < 4; j++) fp8q_raw_buffer_load_lds(ta, (lds_ptr)(st + (wave * 4 + j) * 1024), 16, av[j], so, 0, 0);
 #pragma unroll
-        for (int j = 0; j < S::kCopyB; j++)
-            fp8q_raw_buffer_load_lds(tb, (lds_ptr)(st + S::BM * 128 + (wave * S::kCopyB + j) * 1024), 16, bv[j], so, 0, 0);
+        for (int j = 0; j < 4; j++)
+            fp8q_raw_buffer_load_lds(tb, (lds_ptr)(st + kTile * 128 + (wave * 4 + j) * 1024), 16, bv[j], so, 0, 0);
     };
-    v4f acc[4][CG * 4];
+    v4f acc[4][4];
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
-        for (int b = 0; b < CG * 4; b++) acc[a][b] = (v4f){0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < 4; b++) acc[a][b] = (v4f){0.f, 0.f, 0.f, 0.f};
     issue(stage0, 0);
+    // A lane holds, of row 4 (4 g + r) + a of the wave's 64, columns 4 i .. 4 i + 3: 16 lanes store 64 consecutive columns.
+    constexpr bool kBf16 = STORE == kStoreBf16 || STORE == kAddBf16, kAdd = STORE == kAddBf16 || STORE == kAddF32;
+    const int64_t k = k0 + wn * 64 + 4 * i;
+    void *out = STORE == kParts ? static_cast<void *>(p.sums) : p.dw;
+    auto there = [&](int a, int r) { return k < p.K && n0 + wm * 64 + 4 * (4 * g + r) + a < p.N; };
+    auto place = [&](int a, int r) {  // (one of e and part is 0)
+        return ((e + part) * p.N + n0 + wm * 64 + 4 * (4 * g + r) + a) * p.K + k;
+    };
+    Four<kBf16> old[4][4];  // on the way while the blocks are multiplied
+    if constexpr (kAdd) {
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                old[a][r].lo = old[a][r].hi = (uint2){0u, 0u};
+                if (there(a, r)) old[a][r].load(out, place(a, r));
+            }
+    }
     for (int kb = 0; kb < KB; kb++) {
         uint8_t *cur = (kb & 1) ? stage1 : stage0, *nxt = (kb & 1) ? stage0 : stage1;
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
         issue(nxt, kb + 1);
-        const uint8_t *tB = cur + S::BM * 128;
-        const uint32_t sa = *reinterpret_cast<const uint32_t *>(cur + S::kScale + wm * 64 + 4 * i);
+        const uint32_t sa = *reinterpret_cast<const uint32_t *>(cur + kScaleAt + wm * 64 + 4 * i);
+        const uint32_t sb = *reinterpret_cast<const uint32_t *>(cur + kScaleAt + 512 + wn * 64 + 4 * i);
         v8i af[4];
         v8bf ab[EXACT ? 4 : 1][4];
 #pragma unroll
         for (int a = 0; a < 4; a++) af[a] = wfrag(cur, wm * 64 + 4 * i + a, g);
         if constexpr (EXACT) {
 #pragma unroll
-            for (int a = 0; a < 4; a++) {
-                const float s = __uint_as_float(((sa >> (8 * a)) & 255u) << 23);
+            for (int a = 0; a < 4; a++)
 #pragma unroll
-                for (int q = 0; q < 4; q++) ab[a][q] = to_bf16(af[a][2 * q], af[a][2 * q + 1], s);
-            }
+                for (int q = 0; q < 4; q++) ab[a][q] = to_bf16(af[a][2 * q], af[a][2 * q + 1], power_of(sa, a));
         }
-        static_for<CG>([&](auto cg_) __attribute__((always_inline)) {
-            constexpr int cg = decltype(cg_)::value;
-            const int c0 = (wn * CG + cg) * 64 + 4 * i;
-            const uint32_t sb = *reinterpret_cast<const uint32_t *>(cur + S::kScale + 512 + c0);
-            static_for<4>([&](auto b_) __attribute__((always_inline)) {
-                constexpr int b = decltype(b_)::value;
-                const v8i bf = wfrag(tB, c0 + b, g);
-                if constexpr (EXACT) {
-                    const float s = __uint_as_float(((sb >> (8 * b)) & 255u) << 23);
+        static_for<4>([&](auto b_) __attribute__((always_inline)) {
+            constexpr int b = decltype(b_)::value;
+            const v8i bf = wfrag(cur + kTile * 128, wn * 64 + 4 * i + b, g);
+            if constexpr (EXACT) {
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const v8bf bb = to_bf16(bf[2 * q], bf[2 * q + 1], s);
+                for (int q = 0; q < 4; q++) {
+                    const v8bf bb = to_bf16(bf[2 * q], bf[2 * q + 1], power_of(sb, b));
 #pragma unroll
-                        for (int a = 0; a < 4; a++)
-                            acc[a][cg * 4 + b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ab[a][q], bb, acc[a][cg * 4 + b], 0, 0, 0);
-                    }
-                } else {
-                    static_for<4>([&](auto a_) __attribute__((always_inline)) {
-                        constexpr int a = decltype(a_)::value;
-                        acc[a][cg * 4 + b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            af[a], bf, acc[a][cg * 4 + b], 0, 0, a, (int)sa, b, (int)sb);
-                    });
+                    for (int a = 0; a < 4; a++)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ab[a][q], bb, acc[a][b], 0, 0, 0);
                 }
-            });
+            } else {
+                static_for<4>([&](auto a_) __attribute__((always_inline)) {
+                    constexpr int a = decltype(a_)::value;
+                    acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[a], bf, acc[a][b], 0, 0, a, (int)sa, b,
+                                                                                (int)sb);
+                });
+            }
         });
     }
-    // A lane holds, of row 4 (4 g + r) + a of the wave's 64, columns 4 i .. 4 i + 3 of each column group: 16 lanes store 64
-    // consecutive columns.
-    constexpr bool kBf16 = !EXACT;
-    const int64_t base = e * p.N * p.K;
 #pragma unroll
     for (int a = 0; a < 4; a++)
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-            const int64_t n = n0 + wm * 64 + 4 * (4 * g + r) + a;
-            if (n >= p.N) continue;
-#pragma unroll
-            for (int cg = 0; cg < CG; cg++) {
-                const int64_t k = k0 + (wn * CG + cg) * 64 + 4 * i;
-                if (k >= p.K) continue;
-                const int64_t at = base + n * p.K + k;
-                v4f v = {acc[a][cg * 4][r], acc[a][cg * 4 + 1][r], acc[a][cg * 4 + 2][r], acc[a][cg * 4 + 3][r]};
-                if constexpr (ACCUMULATE) {
-                    if constexpr (kBf16) {
-                        const uint2 o = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.dw) + at);
-                        v[0] += bf16_lo(o.x); v[1] += bf16_hi(o.x); v[2] += bf16_lo(o.y); v[3] += bf16_hi(o.y);
-                    } else {
-                        const float4 o = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.dw) + at);
-                        v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
-                    }
-                }
-                store4<kBf16>(p.dw, at, v);
-            }
+            v4f v = {acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r]};
+            if constexpr (kAdd) v += old[a][r].value();
+            if (there(a, r)) store4<kBf16>(out, place(a, r), v);
         }
+}
+
+// The parts' sums, in order, 4 results a thread.
+template <int STORE>
+__global__ __launch_bounds__(256) void wgrad_parts_kernel(WgradArgs p) {
+    constexpr bool kBf16 = STORE == kStoreBf16 || STORE == kAddBf16;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, size = p.N * p.K;
+    if (at >= size) return;
+    v4f v = load4<false>(p.sums, at);
+#pragma unroll 4
+    for (int64_t s = 1; s < p.parts; s++) v += load4<false>(p.sums, s * size + at);
+    if constexpr (STORE == kAddBf16 || STORE == kAddF32) v += load4<kBf16>(p.dw, at);
+    store4<kBf16>(p.dw, at, v);
 }
 
 // ---------------------------------------------------------------------------------------------------------
@@ -632,44 +665,75 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     }
 }
 
+int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// Where 256 x 256 tiles would leave more than half of the CUs without one, 128 x 128 tiles.  (bf16, 4096 tokens: 576 x 7168, 84
+// large tiles, 31 us by small ones; 2048 x 2048 from 2048 tokens, 64, 14.6.)
+bool large_tiles(int64_t E, int64_t N, int64_t K) { return E * tiles_of(N, 256) * tiles_of(K, 256) >= cu_count() / 2; }
+
+// Parts of a tile's blocks (small tiles, one product), by estimated time in us: a block of a tile takes 0.6 with one
+// workgroup to a CU and 1.0 with two (fp32: 0.95 and 1.6), a second launch 4, and every part a write and a read of N K sums
+// at 5 TB/s.
+int64_t wgrad_parts(int64_t M, int64_t N, int64_t K, bool out_bf16) {
+    if (large_tiles(1, N, K)) return 1;
+    const int64_t blocks = M / 128, tiles = tiles_of(N, kTile) * tiles_of(K, kTile), cu = cu_count();
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t parts = 1; parts <= 64 && parts <= blocks; parts++) {
+        const int64_t each = tiles_of(blocks, parts), wgs = tiles * parts;
+        if (parts > 1 && wgs > 2 * cu) break;
+        if (each * (parts - 1) >= blocks) continue;  // the last would have none
+        const double block = (out_bf16 ? 1.0 : 1.6) * (wgs <= cu ? 0.6 : (double)tiles_of(wgs, 2 * cu));
+        const double t = (double)each * block + (parts > 1 ? 4.0 + (double)parts * (double)(N * K) * 8.0 / 5e6 : 0.0);
+        if (parts == 1 || t < least) {
+            least = t;
+            best = parts;
+        }
+    }
+    return best;
+}
+
 template <bool EXACT, bool ACCUMULATE>
 hipError_t launch_wgrad(WgradArgs p, hipStream_t stream) {
-    auto tiles = [](int64_t n, int64_t t) { return (n + t - 1) / t; };
-    if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count() / 2) {
-        p.n_tiles = tiles(p.N, 256);
-        p.k_tiles = tiles(p.K, 256);
-        const int64_t n = p.E * p.n_tiles * p.k_tiles, wgs = (n + 256 * kMostTiles - 1) / (256 * kMostTiles) * 256;
+    constexpr int kHow = EXACT ? (ACCUMULATE ? kAddF32 : kStoreF32) : (ACCUMULATE ? kAddBf16 : kStoreBf16);
+    if (large_tiles(p.E, p.N, p.K)) {
+        p.n_tiles = tiles_of(p.N, 256);
+        p.k_tiles = tiles_of(p.K, 256);
+        const int64_t wgs = tiles_of(p.E * p.n_tiles * p.k_tiles, 256 * kMostTiles) * 256;
         wgrad_stream_kernel<EXACT, ACCUMULATE><<<dim3((unsigned)wgs), 512, 0, stream>>>(p);
-    } else if (p.E * tiles(p.N, 256) * tiles(p.K, 256) >= cu_count()) {
-        using S = WgradShape<4, 2, 2>;
-        p.n_tiles = tiles(p.N, S::BM);
-        p.k_tiles = tiles(p.K, S::BN);
-        const dim3 grid((unsigned)((p.E * p.n_tiles * p.k_tiles + 255) / 256 * 256));
-        wgrad_kernel<EXACT, ACCUMULATE, 4, 2, 2><<<grid, S::kThreads, 0, stream>>>(p);
-    } else {
-        using S = WgradShape<2, 2, 1>;
-        p.n_tiles = tiles(p.N, S::BM);
-        p.k_tiles = tiles(p.K, S::BN);
-        const dim3 grid((unsigned)((p.E * p.n_tiles * p.k_tiles + 255) / 256 * 256));
-        wgrad_kernel<EXACT, ACCUMULATE, 2, 2, 1><<<grid, S::kThreads, 0, stream>>>(p);
+        return hipGetLastError();
     }
+    p.n_tiles = tiles_of(p.N, kTile);
+    p.k_tiles = tiles_of(p.K, kTile);
+    if (p.parts > 1) {
+        wgrad_small_kernel<EXACT, kParts><<<dim3((unsigned)(p.parts * p.n_tiles * p.k_tiles)), 256, 0, stream>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        wgrad_parts_kernel<kHow><<<dim3((unsigned)tiles_of(p.N * p.K, 1024)), 256, 0, stream>>>(p);
+        return hipGetLastError();
+    }
+    const int64_t wgs = tiles_of(p.E * p.n_tiles * p.k_tiles, 256) * 256;
+    wgrad_small_kernel<EXACT, kHow><<<dim3((unsigned)wgs), 256, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gemm_wgrad_workspace_bytes(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, bool out_bf16) {
+    const int64_t parts = N > 0 && K > 0 ? wgrad_parts(M, N, K, out_bf16) : 1;
+    return parts > 1 ? parts * N * K * 4 : 0;
+}
 
 int64_t gemm_wgrad_blocks(int64_t N, int64_t K, int64_t E) {
-    const int64_t per = ((N + 127) / 128) * ((K + 127) / 128);
+    const int64_t per = tiles_of(N, kTile) * tiles_of(K, kTile);
     if (per > 0 && E > (int64_t(1) << 40) / per) return -1;
     return per * E + 256;
 }
 
 hipError_t launch_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw,
                              bool out_bf16, bool accumulate, const int32_t *off, int64_t E, int64_t M, int64_t N,
-                             int64_t K, float *, hipStream_t stream) {
-    const WgradArgs p = {gt, eg, xt, ex, dw, off, M, N, K, E, 0, 0};
+                             int64_t K, float *workspace, hipStream_t stream) {
+    const WgradArgs p = {gt, eg, xt, ex, dw, off, M, N, K, E, 0, 0, workspace, off == nullptr ? wgrad_parts(M, N, K, out_bf16) : 1};
     if (out_bf16) return accumulate ? launch_wgrad<false, true>(p, stream) : launch_wgrad<false, false>(p, stream);
     return accumulate ? launch_wgrad<true, true>(p, stream) : launch_wgrad<true, false>(p, stream);
 }
