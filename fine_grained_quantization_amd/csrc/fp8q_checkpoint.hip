@@ -204,17 +204,34 @@ struct SwigluArgs {
     uint8_t *gqt, *get, *hqt, *het;
 };
 
-// Codes of a token's 128 channels (the 16 lanes of a DPP row) and their scale.  (The reciprocal is within an ulp, and the
-// values themselves are within a few.)
+// 1 / (1 + e^-x): the hardware's exponential (an ulp, and |x| / 2 for its argument) and its reciprocal with a Newton step.  Up
+// to 2^126 the sum has a reciprocal that is a normal number; gates below -87 are as good as -87.
+__device__ __forceinline__ float sigmoid(float x) {
+    const float d = 1.0f + __builtin_amdgcn_exp2f(__builtin_fminf(x * -1.44269504088896340736f, 126.0f));
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+
+// Codes of a token's 128 channels (the 16 lanes of a DPP row) and their scale.
 __device__ __forceinline__ float row_codes(const float (&v)[8], uint8_t *q) {
     float a = __builtin_fabsf(v[0]);
 #pragma unroll
     for (int i = 1; i < 8; i++) a = __builtin_fmaxf(a, __builtin_fabsf(v[i]));
     const float top = __uint_as_float(row16_max(__float_as_uint(a)));
-    const float inv = top > 0.0f ? 448.0f * __builtin_amdgcn_rcpf(top) : 0.0f;
-    uint2 o;
-    o.x = encode4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    o.y = encode4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    uint2 o = {0u, 0u};
+    if (top > 0x1p-110f && top < 0x1p110f) {  // 448 / top with a Newton step, far from where reciprocals are no normal numbers
+        const float r = __builtin_amdgcn_rcpf(top), inv0 = 448.0f * r;
+        const float inv = __builtin_fmaf(__builtin_fmaf(-top, inv0, 448.0f), r, inv0);
+        o.x = encode4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        o.y = encode4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    } else if (top > 0.0f) {
+        const double inv = 448.0 / (double)top;
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = (float)((double)v[i] * inv);
+        o.x = encode4(w[0], w[1], w[2], w[3]);
+        o.y = encode4(w[4], w[5], w[6], w[7]);
+    }
     *reinterpret_cast<uint2 *>(q) = o;
     return group_scale(top);
 }
@@ -277,8 +294,7 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs
             widen8(g0[j], gr);
 #pragma unroll
             for (int c = 0; c < 8; c++) {
-                const float e = __builtin_amdgcn_exp2f(x[c] * -1.44269504088896340736f);
-                const float sg = __builtin_amdgcn_rcpf(1.0f + e);  // 0 where e is infinite
+                const float sg = sigmoid(x[c]);
                 const float silu = x[c] * sg;
                 v[1][j][c] = gr[c] * silu;
                 v[2][j][c] = silu * u[c];

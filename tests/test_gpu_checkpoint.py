@@ -188,6 +188,23 @@ def test_swiglu_gradient_of_large_and_small_gates():
     check_swiglu(fq.fp8q_swiglu_backward_quant(q, s, gh), q, s, gh)
 
 
+@pytest.mark.parametrize("size", [3e-34, 1e35])
+def test_swiglu_gradient_of_extreme_gradients(size):
+    """Groups whose maximum's reciprocal is beyond fp32's normal numbers, or near it.  Every value is within E4M3's half step,
+    2^-4, of its own or, below E4M3's normal range, 2^-10 of the scale; scales here are at least 2^-126 / 2^4, kept to 2^-20."""
+    M, F = 130, 128
+    q, s = checkpoint(M, 2 * F, 7)
+    s = torch.full_like(s, 0.01)
+    gh = (size * torch.randn((M, F), device="cuda")).bfloat16()
+    gq, gs = fq.fp8q_swiglu_backward_quant(q, s, gh)[:2]
+    x, u = decode(q, s).chunk(2, 1)
+    dx, du, _ = swiglu_grad64(x, u, gh)
+    want = torch.cat([dx, du], 1)
+    sc = gs.t().double().repeat_interleave(128, 1)
+    got = gq.view(torch.float8_e4m3fn).double() * sc
+    assert bool(((got - want).abs() <= (2.0 ** -4 + 2.0 ** -18) * want.abs() + 2.0 ** -10 * sc * (1 + 2.0 ** -18)).all())
+
+
 def test_swiglu_gradient_against_differences():
     """Central differences (step 1e-5, error 1e-10) of sum(gh * silu(x) u) in float64 against the decoded gradients: within
     E4M3's half step."""
