@@ -44,13 +44,14 @@ struct WgradArgs {
 
 // Rows in groups of 64: row 4 i + j of a group is row i of the group's 16-row subtile j.  So a lane's scale bytes of the 4
 // subtiles are one dword (the instruction picks the byte), and in the result the 4 subtiles of a column group are 4
-// consecutive columns.  A tile row (128 codes, 8 chunks of 16) holds logical chunk c at c ^ wswz(row): a fragment read
-// touches rows 4 i + j of 16 i at one chunk, and the chunks of 8 neighbouring i are all different.
-__device__ __forceinline__ int wswz(int r) { return ((r >> 2) & 7) ^ ((r >> 5) & 1); }
+// consecutive columns.  In LDS the subtiles lie one behind the other, place 16 j + i, 128 codes (8 chunks of 16) each, chunk c
+// at c ^ swzf(place): a fragment read touches 16 neighbouring places at one chunk, all banks alike.  (With row 4 i + j at that
+// place, every row of a fragment starts in the same half of the 64 banks, and half of the reads' cycles were conflicts.)
+__device__ __forceinline__ int row_at(int place) { return (place & ~63) + 4 * (place & 15) + ((place >> 4) & 3); }
 
-__device__ __forceinline__ v8i wfrag(const uint8_t *tile, int r, int g) {
-    const u32x4 lo = *reinterpret_cast<const u32x4 *>(tile + r * 128 + (((2 * g) ^ wswz(r)) << 4));
-    const u32x4 hi = *reinterpret_cast<const u32x4 *>(tile + r * 128 + (((2 * g + 1) ^ wswz(r)) << 4));
+__device__ __forceinline__ v8i wfrag(const uint8_t *tile, int place, int g) {
+    const u32x4 lo = *reinterpret_cast<const u32x4 *>(tile + swz(place, 2 * g));
+    const u32x4 hi = *reinterpret_cast<const u32x4 *>(tile + swz(place, 2 * g + 1));
     v8i f;
     f[0] = (int)lo[0]; f[1] = (int)lo[1]; f[2] = (int)lo[2]; f[3] = (int)lo[3];
     f[4] = (int)hi[0]; f[5] = (int)hi[1]; f[6] = (int)hi[2]; f[7] = (int)hi[3];
@@ -158,8 +159,8 @@ __global__ __launch_bounds__(256, 2) void wgrad_small_kernel(WgradArgs p) {
     int av[4], bv[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const int r = (wave * 4 + j) * 8 + (lane >> 3);
-        const int at = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
+        const int place = (wave * 4 + j) * 8 + (lane >> 3), r = row_at(place);
+        const int at = (int)(r * ld) + (((lane & 7) ^ swzf(place)) << 4);
         av[j] = r < nrow ? at : kOutOfRange;
         bv[j] = r < ncol ? at : kOutOfRange;
     }
@@ -215,7 +216,7 @@ __global__ __launch_bounds__(256, 2) void wgrad_small_kernel(WgradArgs p) {
         v8i af[4];
         v8bf ab[EXACT ? 4 : 1][4];
 #pragma unroll
-        for (int a = 0; a < 4; a++) af[a] = wfrag(cur, wm * 64 + 4 * i + a, g);
+        for (int a = 0; a < 4; a++) af[a] = wfrag(cur, wm * 64 + 16 * a + i, g);
         if constexpr (EXACT) {
 #pragma unroll
             for (int a = 0; a < 4; a++)
@@ -224,7 +225,7 @@ __global__ __launch_bounds__(256, 2) void wgrad_small_kernel(WgradArgs p) {
         }
         static_for<4>([&](auto b_) __attribute__((always_inline)) {
             constexpr int b = decltype(b_)::value;
-            const v8i bf = wfrag(cur + kTile * 128, wn * 64 + 4 * i + b, g);
+            const v8i bf = wfrag(cur + kTile * 128, wn * 64 + 16 * b + i, g);
             if constexpr (EXACT) {
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
@@ -359,10 +360,10 @@ __device__ __forceinline__ void wgrad_zero(const WgradArgs &p, const WgradTiles 
 }
 
 // Columns of a wave's 128 in its 8 column subtiles, so that a lane's results of a row come 16 bytes at a time: column i of
-// subtile b is column 8 i + b of them (bf16), or 64 (b / 4) + 4 i + b % 4 (fp32).  The chunks' places follow suit.
+// subtile b is column 8 i + b of them (bf16), or 64 (b / 4) + 4 i + b % 4 (fp32).  Its place in LDS is 16 b + i.
 template <bool EXACT>
-__device__ __forceinline__ int cswz(int r) {
-    return EXACT ? wswz(r) : ((r >> 3) & 7) ^ ((r >> 6) & 1);
+__device__ __forceinline__ int col_at(int place) {
+    return EXACT ? row_at(place) : (place & ~127) + 8 * (place & 15) + ((place >> 4) & 7);
 }
 
 // Streaming stores: 64 gradients of 2048 x 7168 that nothing else delays (one block each) take 313 us with them (6.0 TB/s),
@@ -439,14 +440,14 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     if constexpr (!ACCUMULATE) wgrad_zero<EXACT ? 4 : 2>(p, list, __ballot(blocks == 0), tid, 512);
     if (work == 0) return;
 
-    // Copies: an instruction moves 8 rows (1 KB); lane l lands in row l / 8 of them, chunk l % 8, which holds logical chunk
-    // (l % 8) ^ wswz(row) (cswz for columns).  Rows past the operand are past its resource: their offset is at least nrow * ld.
+    // Copies: an instruction moves 8 places (1 KB); lane l lands in place l / 8 of them, chunk l % 8, which holds logical chunk
+    // (l % 8) ^ swzf(place).  Rows past the operand are past its resource: their offset is at least nrow * ld.
     int avoff[4], bvoff[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const int r = wave * 32 + j * 8 + (lane >> 3);
-        avoff[j] = (int)(r * ld) + (((lane & 7) ^ wswz(r)) << 4);
-        bvoff[j] = (int)(r * ld) + (((lane & 7) ^ cswz<EXACT>(r)) << 4);
+        const int place = wave * 32 + j * 8 + (lane >> 3), chunk = ((lane & 7) ^ swzf(place)) << 4;
+        avoff[j] = (int)(row_at(place) * ld) + chunk;
+        bvoff[j] = (int)(col_at<EXACT>(place) * ld) + chunk;
     }
     // The stream's issue end: the block that is copied next.
     uint64_t ahead = work;  // tiles from its tile on
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     };
     // Chunk 2 g of the lane's row of a wave's first subtile; chunk 2 g + 1: ^ 16.
     const int chunk = ((2 * g) ^ (i & 7) ^ (i >> 3)) << 4;
-    const int fa_at = wm * 8192 + i * 512 + chunk, fb_at = wn * 16384 + i * (EXACT ? 512 : 1024) + chunk;
+    const int fa_at = wm * 8192 + i * 128 + chunk, fb_at = wn * 16384 + i * 128 + chunk;
     auto read8 = [&](int at0, int at1, int off) __attribute__((always_inline)) {  // 32 codes of a row: both chunks
         const u32x4 lo = *reinterpret_cast<const u32x4 *>(lds + at0 + off);
         const u32x4 hi = *reinterpret_cast<const u32x4 *>(lds + at1 + off);
@@ -497,7 +498,6 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     auto read4 = [&](int at, int off) __attribute__((always_inline)) {  // 16 codes of a row: a chunk
         return *reinterpret_cast<const v4i *>(lds + at + off);
     };
-    auto b_off = [](int b) { return EXACT ? (b / 4) * 8192 + (b & 3) * 128 : b * 128; };
 
     uint32_t sc[2][3];  // block s's are in sc[s % 2]
     open_tile();
@@ -536,14 +536,14 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     v4i raw[EXACT ? 3 : 1];
     if constexpr (!EXACT) {
 #pragma unroll
-        for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 128);
+        for (int a = 0; a < 4; a++) fa[a] = read8(fa_at, fa_at ^ 16, a * 2048);
 #pragma unroll
-        for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b_off(b));
+        for (int b = 0; b < 3; b++) fb[b] = read8(kSlot + fb_at, kSlot + (fb_at ^ 16), b * 2048);
     } else {
 #pragma unroll
-        for (int b = 0; b < 2; b++) raw[b] = read4(kSlot + fb_at, b_off(b));
+        for (int b = 0; b < 2; b++) raw[b] = read4(kSlot + fb_at, b * 2048);
 #pragma unroll
-        for (int a = 0; a < 4; a++) widen16(read4(fa_at, a * 128), power_of(sc[0][0], a), wide[a]);
+        for (int a = 0; a < 4; a++) widen16(read4(fa_at, a * 2048), power_of(sc[0][0], a), wide[a]);
     }
     auto mfma = [&](const uint32_t (&s)[3], auto a_, auto b_) __attribute__((always_inline)) {
         constexpr int a = decltype(a_)::value, b = decltype(b_)::value;
@@ -566,7 +566,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         if constexpr (!EXACT) {
             static_for<5>([&](auto b_) __attribute__((always_inline)) {
                 constexpr int b = decltype(b_)::value;
-                fb[(b + 3) & 3] = read8(b0, b1, b_off(b + 3));
+                fb[(b + 3) & 3] = read8(b0, b1, (b + 3) * 2048);
                 if constexpr (b < 4) copy_a(b, last);
                 static_for<4>([&](auto a_) __attribute__((always_inline)) {
                     mfma(s, Index<(b & 1) ? 3 - decltype(a_)::value : decltype(a_)::value>{}, b_);
@@ -585,11 +585,11 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
                     constexpr int c = decltype(c_)::value;
                     mfma(s, a_, Index<5 + ((a & 1) ? 2 - c : c)>{});
                 });
-                fa[a] = read8(na0, na1, a * 128);
+                fa[a] = read8(na0, na1, a * 2048);
                 __builtin_amdgcn_sched_barrier(0);
             });
-            fb[1] = read8(nb0, nb1, b_off(1));
-            fb[2] = read8(nb0, nb1, b_off(2));
+            fb[1] = read8(nb0, nb1, 2048);
+            fb[2] = read8(nb0, nb1, 2 * 2048);
         } else {
             const int a1 = (slot * kSlot + fa_at) ^ 16;
             static_for<2>([&](auto half_) __attribute__((always_inline)) {
@@ -601,9 +601,9 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
                 widen16(raw[0], power_of(s[1], 0), cols[0]);
                 static_for<6>([&](auto b_) __attribute__((always_inline)) {
                     constexpr int b = decltype(b_)::value;
-                    raw[(b + 2) % 3] = read4(half ? b1 : b0, b_off(b + 2));
+                    raw[(b + 2) % 3] = read4(half ? b1 : b0, (b + 2) * 2048);
                     if constexpr (half == 0 && b < 4) copy_a(b, last);
-                    if constexpr (half == 0 && b > 3) rows[b - 4] = read4(a1, (b - 4) * 128);
+                    if constexpr (half == 0 && b > 3) rows[b - 4] = read4(a1, (b - 4) * 2048);
                     // (the next column's codes are widened beside this one's products)
                     widen16(raw[(b + 1) % 3], power_of(s[1 + (b + 1) / 4], (b + 1) & 3), cols[(b + 1) & 1]);
 #pragma unroll
@@ -616,16 +616,16 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
                 if constexpr (half == 1) {
                     next_block_is_there();
 #pragma unroll
-                    for (int a = 0; a < 2; a++) rows[a] = read4(na0, a * 128);
+                    for (int a = 0; a < 2; a++) rows[a] = read4(na0, a * 2048);
                 }
                 widen16(raw[7 % 3], power_of(s[2], 3), cols[1]);  // columns 6 and 7
 #pragma unroll
-                for (int b = 0; b < 2; b++) raw[b] = read4(half ? nb0 : b1, b_off(b));
+                for (int b = 0; b < 2; b++) raw[b] = read4(half ? nb0 : b1, b * 2048);
                 __builtin_amdgcn_sched_barrier(0);
                 static_for<4>([&](auto a_) __attribute__((always_inline)) {
                     constexpr int a = decltype(a_)::value;
                     if constexpr (half == 1) copy_b(a, slot);
-                    if constexpr (a < 2) rows[a + 2] = read4(half ? na0 : a1, (a + 2) * 128);
+                    if constexpr (a < 2) rows[a + 2] = read4(half ? na0 : a1, (a + 2) * 2048);
 #pragma unroll
                     for (int h = 0; h < 2; h++)
 #pragma unroll
