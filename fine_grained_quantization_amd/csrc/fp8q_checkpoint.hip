@@ -243,13 +243,22 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs
     __shared__ __align__(16) uint32_t tile[3][128 * 32];
     __shared__ __align__(16) uint32_t top[3][128];  // the channels' bytes, as in column_bytes
     const int t = threadIdx.x, lane = t & 63, chunk = t & 15, g = t >> 4;
-    const uint32_t FB = (uint32_t)(p.F >> 7), tiles = FB * (uint32_t)(p.cols >> 7);  // (fewer than 2^23)
+    const uint32_t FB = (uint32_t)(p.F >> 7), MB = (uint32_t)(p.cols >> 7), tiles = FB * MB;  // (fewer than 2^23)
+    // The tiles under way are neighbours along the shorter side first, so that both the rows' and the columns' pieces that
+    // are written together are long: 4096 x 18432 takes 170 us along the tokens and 184 along the channels, 8192 x 2048 41.2
+    // and 39.9.
+    auto place = [&](uint32_t i, int64_t &fb, int64_t &mb) __attribute__((always_inline)) {
+        const uint32_t n = MB < FB ? MB : FB, far = i / n, near = i % n;
+        fb = MB < FB ? far : near;
+        mb = MB < FB ? near : far;
+    };
     const int ldq = (int)(2 * p.F), ldg = (int)p.ldg;  // (offsets within a tile's 128 rows are 32 bits)
     uint2 xq[4], uq[4];
     u32x4 gq[4];
     float sx[4], su[4];
     auto load = [&](uint32_t i) __attribute__((always_inline)) {
-        const int64_t fb = i % FB, mb = i / FB;
+        int64_t fb, mb;
+        place(i, fb, mb);
         const int rows = (int)(p.M - mb * 128 < 128 ? p.M - mb * 128 : 128);
         const uint8_t *q0 = p.q + mb * 128 * 2 * p.F + fb * 128;
         const uint16_t *g0 = p.gh + mb * 128 * p.ldg + fb * 128;
@@ -266,7 +275,8 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs
     };
     load(blockIdx.x);
     for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
-        const int64_t fb = i % FB, mb = i / FB;
+        int64_t fb, mb;
+        place(i, fb, mb);
         const int rows = (int)(p.M - mb * 128 < 128 ? p.M - mb * 128 : 128);
         uint8_t *oq = p.gq + mb * 128 * 2 * p.F + fb * 128;
         float *osx = p.gs + fb * p.M + mb * 128, *osu = osx + FB * p.M;

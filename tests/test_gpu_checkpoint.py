@@ -158,7 +158,7 @@ def check_swiglu(out, q, s, gh):
     assert float((both - cols).norm() / d.norm().clamp(min=1e-300)) < 2 * 2.0 ** -4
 
 
-@pytest.mark.parametrize("M,F", [(1, 128), (127, 256), (128, 128), (200, 1152), (1030, 2048)])
+@pytest.mark.parametrize("M,F", [(1, 128), (127, 256), (128, 128), (200, 1152), (1030, 2048), (900, 5120), (4200, 1152)])
 def test_swiglu_gradient(M, F):
     q, s = checkpoint(M, 2 * F, 3)
     g = torch.Generator(device="cuda").manual_seed(M)
