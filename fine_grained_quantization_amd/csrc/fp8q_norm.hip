@@ -58,16 +58,23 @@ __device__ __forceinline__ u32x4 add8(const u32x4 &a, const u32x4 &b) {
     return o;
 }
 
-// Sum over the workgroup's threads; every thread gets it.  The order is fixed.
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float *part) {
+// Sum over the workgroup's threads; every thread gets it.  The order is fixed.  T: the type in which the waves' sums are added.
+template <int THREADS, typename T = float>
+__device__ __forceinline__ T block_sum(float v, float *part) {
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    float s = 0.f;
+    T s = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 64; i++) s += part[i];
     return s;
+}
+
+// 1 / sqrt(a): the hardware's fp32 result and a Newton step in double, where a and the result are normal numbers by far.
+__device__ __forceinline__ double inverse_root(double a) {
+    if (!(a > 0x1p-100 && a < 0x1p120)) return 1.0f / sqrtf((float)a);
+    const double r = __builtin_amdgcn_rsqf((float)a);
+    return fma(r * 0.5, fma(-a * r, r, 1.0), r);
 }
 
 struct NormArgs {
@@ -75,6 +82,7 @@ struct NormArgs {
     int64_t ldx, ldr, K;
     const void *w;
     float eps;
+    double inv_k;
     uint16_t *h, *y;
     uint8_t *q;
     float *s, *rstd;
@@ -174,8 +182,7 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_quant_kernel(NormArgs p) {
 #pragma unroll
         for (int i = 0; i < 8; i++) ss = __builtin_fmaf(elem(a, i), elem(a, i), ss);
     }
-    ss = block_sum<THREADS>(ss, part);
-    const float r = 1.0f / sqrtf(ss / (float)p.K + p.eps);
+    const float r = (float)inverse_root(block_sum<THREADS, double>(ss, part) * p.inv_k + (double)p.eps);
     if (t == 0 && p.rstd != nullptr) p.rstd[m] = r;
     if (p.q == nullptr && p.y == nullptr) return;
 #pragma unroll
@@ -359,7 +366,7 @@ hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const 
                                           const void *w, bool w_bf16, float eps, bool pow2, int64_t M, int64_t K,
                                           uint16_t *h, uint16_t *y, uint8_t *q, float *s, float *rstd,
                                           hipStream_t stream) {
-    const NormArgs p = {x, residual, ldx, ldr, K, w, eps, h, y, q, s, rstd, M};
+    const NormArgs p = {x, residual, ldx, ldr, K, w, eps, K > 0 ? 1.0 / (double)K : 0.0, h, y, q, s, rstd, M};
     if (w_bf16) return pow2 ? launch_norm<true, true>(p, stream) : launch_norm<true, false>(p, stream);
     return pow2 ? launch_norm<false, true>(p, stream) : launch_norm<false, false>(p, stream);
 }
