@@ -541,7 +541,7 @@ static int transpose_128x1(const void *x, const float *s, bool codes, int64_t ld
         return FP8Q_ERR_SHAPE;
     if (rows == 0 || K == 0) return FP8Q_OK;
     if ((T > 0 && (!x || (codes && !s))) || !qt || !et) return FP8Q_ERR_NULL;
-    if (!aligned16(x) || !aligned4(s) || !aligned4(row_token) || !aligned16(qt)) return FP8Q_ERR_ALIGN;
+    if (!aligned16(x) || !aligned4(s) || !aligned4(row_token) || !aligned16(qt) || !aligned16(et)) return FP8Q_ERR_ALIGN;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_transpose_128x1(x, s, codes, ld, T, K, row_token, rows, qt, et,

@@ -165,23 +165,21 @@ __global__ __launch_bounds__(256, 2) void wgrad_small_kernel(WgradArgs p) {
         av[j] = r < nrow ? at : kOutOfRange;
         bv[j] = r < ncol ? at : kOutOfRange;
     }
-    // Block kb's codes and scale bytes into a stage; past the last block nothing is read (zeros land).
+    // Block kb's codes and scale bytes into a stage.
     auto issue = [&](uint8_t *st, int kb) __attribute__((always_inline)) {
-        const bool in = kb < KB;
-        const i32x4 ta = in ? ra : empty_rsrc(ra), tb = in ? rb : empty_rsrc(rb);
-        const int so = in ? kb * 128 : 0;
+        if (kb >= KB) return;  // (no copy is on its way into LDS when the workgroup ends)
         if (wave < 2) {  // 4 scale bytes a lane: wave 0 the rows', wave 1 the columns'
             const bool rows = wave == 0;
             const int64_t n = rows ? nrow : ncol;
             const i32x4 rs = make_rsrc((rows ? p.eg + (int64_t)(b0 + kb) * p.N + n0 : p.ex + (int64_t)(b0 + kb) * p.K + k0),
-                                       in ? (uint64_t)n : 0);
+                                       (uint64_t)n);
             fp8q_raw_buffer_load_lds(rs, (lds_ptr)(st + kScaleAt + wave * 512), 4, lane * 4, 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < 4; j++) fp8q_raw_buffer_load_lds(ta, (lds_ptr)(st + (wave * 4 + j) * 1024), 16, av[j], so, 0, 0);
+        for (int j = 0; j < 4; j++) fp8q_raw_buffer_load_lds(ra, (lds_ptr)(st + (wave * 4 + j) * 1024), 16, av[j], kb * 128, 0, 0);
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            fp8q_raw_buffer_load_lds(tb, (lds_ptr)(st + kTile * 128 + (wave * 4 + j) * 1024), 16, bv[j], so, 0, 0);
+            fp8q_raw_buffer_load_lds(rb, (lds_ptr)(st + kTile * 128 + (wave * 4 + j) * 1024), 16, bv[j], kb * 128, 0, 0);
     };
     v4f acc[4][4];
 #pragma unroll
@@ -668,6 +666,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #undef FP8Q_WGRAD_STEP
 #undef FP8Q_WGRAD_ZERO
     }
+    __builtin_amdgcn_s_waitcnt(0);  // the last (zero-byte) copies have retired before the workgroup ends
 }
 
 int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }

@@ -524,7 +524,7 @@ int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, in
  *       outside [0, T): zeros), or NULL: row r is token r, and rows must be T (or 0)
  *   qt : E4M3 [K, Mp], et : uint8 [Mp/128][K] with Mp = rows rounded up to 128
  * Requires T, rows < 2^31, K % 128 == 0, ld >= K, ld % 8 == 0, fewer than 2^23 tiles of
- * 128 x 128; q, x and qt 16-byte aligned, s and row_token 4-byte.  q, s and x may be
+ * 128 x 128; q, x, qt and et 16-byte aligned, s and row_token 4-byte.  q, s and x may be
  * NULL when T is 0.  One launch. */
 int fp8q_transpose_act_128x1(const uint8_t *q, const float *s, int64_t T, int64_t K, const int32_t *row_token,
                              int64_t rows, uint8_t *qt, uint8_t *et, void *stream);

@@ -72,7 +72,7 @@ TRANS = dict(q=A, s=A, T=4, K=256, row_token=None, rows=4, qt=B, et=B, stream=No
     (dict(row_token=A, rows=1 << 31), SHAPE), (dict(row_token=A, rows=1 << 30, K=256), SHAPE), (dict(K=1 << 40), SHAPE),
     (dict(T=0, rows=0, q=None), OK), (dict(rows=0, qt=None), OK), (dict(K=0), OK), (dict(q=None), NULL), (dict(s=None), NULL),
     (dict(qt=None), NULL), (dict(et=None), NULL), (dict(q=MIS8), ALIGN), (dict(s=MIS), ALIGN), (dict(row_token=MIS), ALIGN),
-    (dict(qt=MIS8), ALIGN),
+    (dict(qt=MIS8), ALIGN), (dict(et=MIS8), ALIGN),
 ])
 def test_transpose(lib, change, want):
     assert set(change) <= set(TRANS)

@@ -46,7 +46,8 @@ def build(T, H, F, E, k, seed=0):
 
 
 def off_by(got, want):
-    return float((got.double() - want.detach()).norm() / want.detach().norm())
+    got, want = got.detach().double(), want.detach()
+    return float((got - want).norm() / want.norm())
 
 
 @pytest.mark.parametrize("T,H,F,E,k", [(1, 256, 128, 4, 2), (60, 512, 256, 16, 4), (900, 1024, 640, 8, 3)])
