@@ -575,8 +575,13 @@ int fp8q_swiglu_backward_quant(const uint8_t *q, const float *s, const uint16_t 
                                                      static_cast<hipStream_t>(stream)));
 }
 
+static bool wgrad_sizes(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || M % 128 || M > kMaxK || N < 0 || N > kMaxWgrad || N % 16 || K < 0 || K > kMaxWgrad || K % 16) return false;
+    return M / 128 * (N > K ? N : K) <= int64_t(1) << 30;  // scale bytes are addressed with 32-bit offsets
+}
+
 int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out_dtype) {
-    if (M < 0 || M % 128 || M > kMaxK || N < 0 || N > kMaxWgrad || N % 16 || K < 0 || K > kMaxWgrad || K % 16) return -1;
+    if (!wgrad_sizes(M, N, K)) return -1;
     if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_F32) return -1;
     const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, 1);
     if (blocks < 0 || blocks > kMaxGrid512) return -1;
@@ -586,9 +591,7 @@ int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out
 static int wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
                  int accumulate, bool grouped, const int32_t *off, int64_t E, int64_t M, int64_t N, int64_t K,
                  void *workspace, int64_t workspace_bytes, void *stream) {
-    if (E < 1 || E > 0x7FFFFFFF || M < 0 || M % 128 || M > kMaxK || N < 0 || N > kMaxWgrad || N % 16 || K < 0 ||
-        K > kMaxWgrad || K % 16)
-        return FP8Q_ERR_SHAPE;
+    if (E < 1 || E > 0x7FFFFFFF || !wgrad_sizes(M, N, K)) return FP8Q_ERR_SHAPE;
     const int64_t blocks = fp8q::gemm_wgrad_blocks(N, K, E);
     if (blocks < 0 || blocks > kMaxGrid512) return FP8Q_ERR_SHAPE;
     if (out_dtype != FP8Q_OUT_BF16 && out_dtype != FP8Q_OUT_F32) return FP8Q_ERR_DTYPE;

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 typedef int fp8q_i32x4 __attribute__((ext_vector_type(4)));
+typedef int fp8q_i32x2 __attribute__((ext_vector_type(2)));
 
 // LLVM's raw buffer load into LDS (buffer_load_dwordx4 ... lds): per-lane byte offset `voffset`, scalar
 // byte offset `soffset`; the `size` bytes of lane l land at the wave's LDS address + size * l.  Reads at
@@ -13,9 +14,11 @@ __device__ void fp8q_raw_buffer_load_lds(fp8q_i32x4 rsrc, __attribute__((address
                                          int voffset, int soffset, int offset,
                                          int aux) __asm("llvm.amdgcn.raw.buffer.load.lds");
 
-// LLVM's raw buffer loads into registers (16 bytes / 4 bytes per lane); out-of-range reads return 0.
+// LLVM's raw buffer loads into registers (16, 8 or 4 bytes per lane); out-of-range reads return 0.
 __device__ fp8q_i32x4 fp8q_raw_buffer_load_b128(fp8q_i32x4 rsrc, int voffset, int soffset,
                                                 int aux) __asm("llvm.amdgcn.raw.buffer.load.v4i32");
+__device__ fp8q_i32x2 fp8q_raw_buffer_load_b64(fp8q_i32x4 rsrc, int voffset, int soffset,
+                                               int aux) __asm("llvm.amdgcn.raw.buffer.load.v2i32");
 __device__ float fp8q_raw_buffer_load_f32(fp8q_i32x4 rsrc, int voffset, int soffset,
                                           int aux) __asm("llvm.amdgcn.raw.buffer.load.f32");
 

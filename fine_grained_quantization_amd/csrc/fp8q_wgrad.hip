@@ -380,6 +380,10 @@ constexpr int kFar = 0x60000000;
 // are older than the stores count on it.
 template <bool EXACT>
 constexpr int kStores = EXACT ? 32 : 16;
+// Loads of a block's scale bytes; the waits count on these too.  (They are written as the instructions that they become: two
+// loads of neighbouring dwords would be merged, and a wait too short.)
+template <bool EXACT>
+constexpr int kScaleLoads = EXACT ? 3 : 2;
 
 // Rows past the tile are past the resource, from nrow * pitch on; columns past it are sent there.  The whole offset goes into
 // the lane's: behind a store with a scalar offset the compiler lets the next instruction overwrite the store's data registers,
@@ -435,7 +439,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 7;
     const int wm = wave & 3, wn = wave >> 2;
     const int i = lane & 15, g = lane >> 4;
-    const int row = wm * 64 + 16 * g, col = wn * 128 + (EXACT ? 4 : 8) * i;  // of the lane's results
+    const int col = wn * 128 + (EXACT ? 4 : 8) * i;  // of the lane's results
     const int64_t ld = p.M;
     WgradTiles list;
     const int blocks = list.init(p, blockIdx.x + gridDim.x * lane);
@@ -445,9 +449,10 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 
     // Copies: an instruction moves 8 places (1 KB); lane l lands in place l / 8 of them, chunk l % 8, which holds logical chunk
     // (l % 8) ^ swzf(place).  Rows past the operand are past its resource: their offset is at least nrow * ld.
-    int avoff[4], bvoff[4];
+    // (Places j + 2 hold the rows after those of places j: the scalar offset takes that.)
+    int avoff[2], bvoff[2];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < 2; j++) {
         const int place = wave * 32 + j * 8 + (lane >> 3), chunk = ((lane & 7) ^ swzf(place)) << 4;
         avoff[j] = (int)(row_at(place) * ld) + chunk;
         bvoff[j] = (int)(col_at<EXACT>(place) * ld) + chunk;
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     // The stream's issue end: the block that is copied next.
     uint64_t ahead = work;  // tiles from its tile on
     i32x4 ra, rb, sra, srb;
-    int ikb = 0, iKB = 0, vsa = 0, vsb0 = 0, vsb1 = 0;
+    int ikb = 0, iKB = 0, vsa = 0, vsb = 0;
     auto open_tile = [&]() __attribute__((always_inline)) {  // the first of `ahead`; none: nothing is read
         const WgradTile w = list.get(p, ahead ? __builtin_ctzll(ahead) : 0);
         ikb = 0;
@@ -467,8 +472,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         srb = make_rsrc(p.ex + (int64_t)w.b0 * p.K + w.k0, ahead ? (uint64_t)((w.KB - 1) * p.K + w.ncol) : 0);
         const int a = wm * 64 + 4 * i;
         vsa = a < w.nrow ? a : kOutOfRange;
-        vsb0 = col < w.ncol ? col : kOutOfRange;
-        vsb1 = EXACT ? (col + 64 < w.ncol ? col + 64 : kOutOfRange) : vsb0 + 4;  // (kOutOfRange + 4 is out of range too)
+        vsb = col < w.ncol ? col : kOutOfRange;
         uniform(ra);
         uniform(rb);
         uniform(sra);
@@ -476,15 +480,25 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         ahead &= ahead - 1;
     };
     auto copy_a = [&](int j, int slot) __attribute__((always_inline)) {
-        fp8q_raw_buffer_load_lds(ra, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, avoff[j], ikb * 128, 0, 0);
+        fp8q_raw_buffer_load_lds(ra, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, avoff[j & 1],
+                                 ikb * 128 + (j >> 1) * (int)ld, 0, 0);
     };
     auto copy_b = [&](int j, int slot) __attribute__((always_inline)) {
-        fp8q_raw_buffer_load_lds(rb, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, bvoff[j], ikb * 128, 0, 0);
+        fp8q_raw_buffer_load_lds(rb, (lds_ptr)(lds + slot * kSlot + (wave * 4 + j) * 1024), 16, bvoff[j & 1],
+                                 ikb * 128 + (j >> 1) * (int)ld, 0, 0);
     };
     auto scales = [&](uint32_t (&s)[3]) __attribute__((always_inline)) {
         s[0] = __float_as_uint(fp8q_raw_buffer_load_f32(sra, vsa, ikb * (int)p.N, 0));
-        s[1] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb0, ikb * (int)p.K, 0));
-        s[2] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb1, ikb * (int)p.K, 0));
+        if constexpr (EXACT) {
+            s[1] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, vsb, ikb * (int)p.K, 0));
+            // (Past the tile's columns these are other columns' bytes, or zeros: they meet codes of zero, and no result is
+            // stored.)
+            s[2] = __float_as_uint(fp8q_raw_buffer_load_f32(srb, (int)((uint32_t)vsb + 64u), ikb * (int)p.K, 0));
+        } else {
+            const fp8q_i32x2 both = fp8q_raw_buffer_load_b64(srb, vsb, ikb * (int)p.K, 0);
+            s[1] = (uint32_t)both[0];
+            s[2] = (uint32_t)both[1];
+        }
     };
     // Chunk 2 g of the lane's row of a wave's first subtile; chunk 2 g + 1: ^ 16.
     const int chunk = ((2 * g) ^ (i & 7) ^ (i >> 3)) << 4;
@@ -502,6 +516,13 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
         return *reinterpret_cast<const v4i *>(lds + at + off);
     };
 
+    // The lane, so that the compiler does not form the stores' addresses before the loop: 5 to 11 registers of the fp32 form
+    // spilled then, and a reload waits for all copies before it.
+    auto lane_again = []() __attribute__((always_inline)) {
+        int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        asm volatile("" : "+v"(l));
+        return l;
+    };
     uint32_t sc[2][3];  // block s's are in sc[s % 2]
     open_tile();
     scales(sc[0]);
@@ -519,7 +540,7 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
     auto wrap = [](int s) { return s >= kSlots ? s - kSlots : s; };
     v4f acc[4][8];
     bool stored = false;  // a tile's results were stored between this block and the one before
-    // Block s + 1 is there: younger are this block's 4 copies and 3 scales, and a finished tile's stores, which need not have
+    // Block s + 1 is there: younger are this block's 4 copies and its scales' loads, and a finished tile's stores, which need not have
     // reached memory.  (The compiler would move matrix instructions before the branch behind it.)
     auto next_block_is_there = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -527,9 +548,9 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #pragma unroll
             for (int b = 0; b < (EXACT ? 6 : 5); b++) asm volatile("" : "+v"(acc[a][b]));
         if (stored)
-            copies_barrier<7 + kStores<EXACT>>();
+            copies_barrier<4 + kScaleLoads<EXACT> + kStores<EXACT>>();
         else
-            copies_barrier<7>();
+            copies_barrier<4 + kScaleLoads<EXACT>>();
         __builtin_amdgcn_sched_barrier(0);
     };
     // Fragments that are alive between blocks: for bf16 the codes of 4 rows (32 of each) and of up to 4 columns; for fp32
@@ -654,10 +675,12 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 #define FP8Q_WGRAD_STEP(TURN)                                                                                  \
     block(Index<TURN>{});                                                                                      \
     if (--left == 0) {                                                                                         \
-        wgrad_store<EXACT, ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)), row, col);                  \
+        wgrad_store<EXACT, ACCUMULATE>(p, acc, list.get(p, __builtin_ctzll(todo)),                             \
+                                       wm * 64 + 16 * (lane_again() >> 4),                                     \
+                                       wn * 128 + (EXACT ? 4 : 8) * (lane_again() & 15));                      \
         todo &= todo - 1;                                                                                      \
         if (todo == 0) break;                                                                                  \
-        left = list.get(p, __builtin_ctzll(todo)).KB;                                      \
+        left = list.get(p, __builtin_ctzll(todo)).KB;                                                          \
         stored = true;                                                                                         \
         FP8Q_WGRAD_ZERO()                                                                                      \
     }

@@ -561,8 +561,8 @@ int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out
  *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, contents on
  *          entry do not matter (calls that share one must not overlap); NULL will do
  *          when 0 bytes are needed
- * Requires M % 128 == 0, M <= 2^23, N and K multiples of 16 up to 2^20; all pointers
- * 16-byte aligned.  With M 0, dw becomes 0 (or stays). */
+ * Requires M % 128 == 0, M <= 2^23, N and K multiples of 16 up to 2^20, M/128 * N and
+ * M/128 * K up to 2^30; all pointers 16-byte aligned.  With M 0, dw becomes 0 (or stays). */
 int fp8q_gemm_wgrad(const uint8_t *gt, const uint8_t *eg, const uint8_t *xt, const uint8_t *ex, void *dw, int out_dtype,
                     int accumulate, int64_t M, int64_t N, int64_t K, void *workspace, int64_t workspace_bytes,
                     void *stream);

@@ -83,6 +83,14 @@ def test_transpose(lib, change, want):
                                         None) == want
 
 
+def test_weight_gradients_with_too_many_scale_bytes(lib):
+    need = lib.fp8q_gemm_wgrad_workspace_bytes
+    assert need(1 << 23, 16384, 16, 1) >= 0 and need(1 << 23, 16400, 16, 1) == -1 and need(1 << 23, 16, 16400, 1) == -1
+    c = {**WG, "M": 1 << 23, "N": 16, "K": 16400}
+    assert lib.fp8q_gemm_wgrad(*c.values()) == SHAPE
+    assert lib.fp8q_grouped_gemm_wgrad(*{**GWG, "M": 1 << 23, "N": 16400, "K": 16}.values()) == SHAPE
+
+
 def test_bf16_rows(lib):
     f = lib.fp8q_quant_act_128x1
     assert f(A, 255, 4, 256, None, 4, B, B, None) == SHAPE and f(A, 260, 4, 256, None, 4, B, B, None) == SHAPE
