@@ -123,56 +123,65 @@ struct TransposeArgs {
 // between the maxima and the codes, which go through LDS to leave as rows of 128 bytes.  8192 x 7168: 22 us from codes (5.35
 // TB/s), 29 from bf16 (6.0).  Routed to 64 experts (73,000 rows of 7168): 149-160 us for 523 MB written; 490 vector
 // instructions a wave keep the SIMDs busy for two thirds of that.
-template <bool CODES>
+template <bool CODES, bool ROUTED>
 __global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs p) {
     __shared__ __align__(16) uint32_t tile[256 * 32];
     __shared__ u32x4 all[8][32];
     const int t = threadIdx.x, lane = t & 63, chunk = t & 31, g = t >> 5;
     // Rows in place: neighbours share rows.  Routed rows: each XCD (workgroups b with the same b % 8) takes an eighth of all
     // tiles, channels by channels, so that a token's 256 channels come from its L2 after the first of the token's rows.
-    const int64_t KQ = (p.K + 255) >> 8, MB = p.cols >> 7;
-    int64_t kq, mb;
-    if (p.row_token == nullptr) {
+    const uint32_t KQ = (uint32_t)((p.K + 255) >> 8), MB = (uint32_t)(p.cols >> 7), tiles = KQ * MB;  // (fewer than 2^23)
+    uint32_t kq, mb32;
+    if constexpr (!ROUTED) {
+        if (blockIdx.x >= tiles) return;
         kq = blockIdx.x % KQ;
-        mb = blockIdx.x / KQ;
-        if (mb >= MB) return;
+        mb32 = blockIdx.x / KQ;
     } else {
-        const int64_t t8 = (KQ * MB + 7) / 8, i = (blockIdx.x % 8) * t8 + blockIdx.x / 8;
-        if (i >= KQ * MB) return;
+        const uint32_t i = (blockIdx.x % 8) * ((tiles + 7) / 8) + blockIdx.x / 8;
+        if (i >= tiles) return;
         kq = i / MB;
-        mb = i % MB;
+        mb32 = i % MB;
     }
-    const int64_t k0 = kq * 256;
+    const int64_t k0 = kq * 256, mb = mb32;
     const bool in = k0 + chunk * 8 < p.K;
-    int64_t tok[8];
+    const int c0 = (in ? chunk : chunk & 15) * 8;
+    // Rows without a token, and channels past the last, read token 0 and are made zeros: no branch stands between the loads.
+    int tok[8];
     const int64_t m0 = mb * 128 + g * 8;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        tok[j] = m0 + j < p.rows && in ? m0 + j : -1;
-        if (p.row_token != nullptr && tok[j] >= 0) tok[j] = p.row_token[m0 + j];
-        if (tok[j] >= p.T) tok[j] = -1;
+        const bool there = m0 + j < p.rows;
+        tok[j] = ROUTED ? p.row_token[there ? m0 + j : 0] : (int)(m0 + j);
+        if (!(there && in && (uint32_t)tok[j] < (uint32_t)p.T)) tok[j] = -1;
     }
     float v[8][8];
     if constexpr (CODES) {
-        const uint8_t *x = static_cast<const uint8_t *>(p.x) + k0 + chunk * 8;
-        const float *s = p.s + (k0 / 128 + (chunk >> 4)) * p.T;
+        const uint8_t *x = static_cast<const uint8_t *>(p.x) + k0 + c0;
+        const float *s = p.s + (k0 / 128 + (c0 >> 7)) * p.T;
         uint2 d[8];
         float sc[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            d[j] = tok[j] >= 0 ? *reinterpret_cast<const uint2 *>(x + tok[j] * p.K) : (uint2){0u, 0u};
-            sc[j] = tok[j] >= 0 ? s[tok[j]] : 0.0f;
+            const uint32_t r = max(tok[j], 0);
+            d[j] = *reinterpret_cast<const uint2 *>(x + r * (uint64_t)(uint32_t)p.K);
+            sc[j] = s[r];
         }
 #pragma unroll
-        for (int j = 0; j < 8; j++) decode8(d[j], sc[j], v[j]);
+        for (int j = 0; j < 8; j++) {
+            if (tok[j] < 0) d[j] = (uint2){0u, 0u};
+            if (tok[j] < 0) sc[j] = 0.0f;
+            decode8(d[j], sc[j], v[j]);
+        }
     } else {
-        const uint16_t *x = static_cast<const uint16_t *>(p.x) + k0 + chunk * 8;
+        const uint16_t *x = static_cast<const uint16_t *>(p.x) + k0 + c0;
         u32x4 d[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            d[j] = tok[j] >= 0 ? *reinterpret_cast<const u32x4 *>(x + tok[j] * p.ld) : (u32x4){0u, 0u, 0u, 0u};
+        for (int j = 0; j < 8; j++) d[j] = *reinterpret_cast<const u32x4 *>(x + (int64_t)max(tok[j], 0) * p.ld);
 #pragma unroll
-        for (int j = 0; j < 8; j++) widen8(d[j], v[j]);
+        for (int j = 0; j < 8; j++) {
+            if (tok[j] < 0) d[j] = (u32x4){0u, 0u, 0u, 0u};
+            widen8(d[j], v[j]);
+        }
     }
     Bytes8 e;
     column_bytes(v, e);
@@ -364,12 +373,20 @@ hipError_t launch_transpose_128x1(const void *x, const float *s, bool codes, int
                                   const int32_t *row_token, int64_t rows, uint8_t *qt, uint8_t *et,
                                   hipStream_t stream) {
     const int64_t cols = (rows + 127) / 128 * 128;
+    if (T == 0) {  // (all rows are zeros; what they read does not matter, and the copy's first 128 rows are there)
+        x = qt;
+        s = reinterpret_cast<const float *>(qt);
+    }
     const TransposeArgs p = {x, s, ld, T, K, rows, cols, row_token, qt, et};
     const dim3 grid((unsigned)((cols / 128 * ((K + 255) / 256) + 7) / 8 * 8));
-    if (codes)
-        transpose_kernel<true><<<grid, kThreads, 0, stream>>>(p);
+    if (codes && row_token != nullptr)
+        transpose_kernel<true, true><<<grid, kThreads, 0, stream>>>(p);
+    else if (codes)
+        transpose_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
+    else if (row_token != nullptr)
+        transpose_kernel<false, true><<<grid, kThreads, 0, stream>>>(p);
     else
-        transpose_kernel<false><<<grid, kThreads, 0, stream>>>(p);
+        transpose_kernel<false, false><<<grid, kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
