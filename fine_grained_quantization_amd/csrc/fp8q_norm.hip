@@ -87,7 +87,26 @@ struct NormArgs {
     uint8_t *q;
     float *s, *rstd;
     int64_t M;
+    bool stream;
 };
+
+// A row's first chunks, CH a thread.
+template <int THREADS, int CH>
+__device__ __forceinline__ void load_row(const uint16_t *x, int64_t chunks, bool stream, u32x4 (&v)[CH]) {
+    if (stream) {
+#pragma unroll
+        for (int j = 0; j < CH; j++) {
+            const int64_t c = threadIdx.x + THREADS * j;
+            v[j] = c < chunks ? load_stream16(x + c * 8) : (u32x4){0u, 0u, 0u, 0u};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; j++) {
+            const int64_t c = threadIdx.x + THREADS * j;
+            v[j] = c < chunks ? *reinterpret_cast<const u32x4 *>(x + c * 8) : (u32x4){0u, 0u, 0u, 0u};
+        }
+    }
+}
 
 // Codes of one 8-element chunk of h: t = h w, exact in fp32 where w is bf16.  A group's 16 chunks lie in the 16 lanes of a
 // DPP row.  With scale amax / 448 the row's factor cancels, y / (amax_y / 448) = t 448 / amax_t; products of two bf16
@@ -140,7 +159,7 @@ __device__ __forceinline__ void norm_chunk(const NormArgs &p, const u32x4 &v, in
 // One workgroup per row, its first CH * THREADS chunks of 8 elements kept in registers between the sum and the codes; the
 // chunks past them are read again.  (x, residual and h may be one array: a thread reads its elements before it writes them.)
 // Threads by K, so that a row fits their registers: 256 x 1 chunk, 256 x 4, 1024 x 3.  Bound by memory: 4096 x 7168 with a
-// residual 44.5 us, 4.6 TB/s (a copy of that size 5.0); 8192 x 2048 21.7 us, 5.4.  One row 4.2 us: a load, the sum, a store.
+// residual 41 us, 5.0 TB/s (as a large copy); 8192 x 2048 21.5 us, 5.4.  One row 4.2 us: a load, the sum, a store.
 template <bool W_BF16, bool POW2, int THREADS, int CH>
 __global__ __launch_bounds__(THREADS) void rmsnorm_quant_kernel(NormArgs p) {
     __shared__ float part[THREADS / 64];
@@ -151,18 +170,10 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_quant_kernel(NormArgs p) {
     const uint16_t *res = p.res != nullptr ? p.res + m * p.ldr : nullptr;
     uint16_t *h = p.res != nullptr ? p.h + m * p.K : nullptr;
     u32x4 v[CH];
-#pragma unroll
-    for (int j = 0; j < CH; j++) {
-        const int64_t c = t + THREADS * j;
-        v[j] = c < chunks ? *reinterpret_cast<const u32x4 *>(x + c * 8) : (u32x4){0u, 0u, 0u, 0u};
-    }
+    load_row<THREADS>(x, chunks, p.stream, v);
     if (res != nullptr) {
         u32x4 u[CH];
-#pragma unroll
-        for (int j = 0; j < CH; j++) {
-            const int64_t c = t + THREADS * j;
-            u[j] = c < chunks ? *reinterpret_cast<const u32x4 *>(res + c * 8) : (u32x4){0u, 0u, 0u, 0u};
-        }
+        load_row<THREADS>(res, chunks, p.stream, u);
 #pragma unroll
         for (int j = 0; j < CH; j++) {
             const int64_t c = t + THREADS * j;
@@ -369,7 +380,13 @@ hipError_t launch_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const 
                                           const void *w, bool w_bf16, float eps, bool pow2, int64_t M, int64_t K,
                                           uint16_t *h, uint16_t *y, uint8_t *q, float *s, float *rstd,
                                           hipStream_t stream) {
-    const NormArgs p = {x, residual, ldx, ldr, K, w, eps, K > 0 ? 1.0 / (double)K : 0.0, h, y, q, s, rstd, M};
+    // Streaming loads for inputs of 96 to 256 MB, which the last cache cannot keep beside the outputs, but would try to.  us with
+    // them and without: 4096 x 4096 and a residual (67 MB) 24.9, 22.9; 4096 x 5120 (84 MB) 29.5, 29.2; 4096 x 7168 (117 MB) 41.2,
+    // 46.7; 8192 x 5120 (168 MB) 51.4, 57.1; 8192 x 7168 (235 MB) 78.0, 79.2, and 82, 85 where x has just been written;
+    // 16384 x 7168 149 both, and then 170, 150.
+    const int64_t in = M * K * (residual != nullptr ? 4 : 2);
+    const bool stream_loads = in > (int64_t(96) << 20) && in <= (int64_t(256) << 20);
+    const NormArgs p = {x, residual, ldx, ldr, K, w, eps, K > 0 ? 1.0 / (double)K : 0.0, h, y, q, s, rstd, M, stream_loads};
     if (w_bf16) return pow2 ? launch_norm<true, true>(p, stream) : launch_norm<true, false>(p, stream);
     return pow2 ? launch_norm<false, true>(p, stream) : launch_norm<false, false>(p, stream);
 }

@@ -90,6 +90,15 @@ def test_norm_in_place(which, K):
     check_norm(q, s, h, rstd, None, want, w, 1e-6, False)
 
 
+@pytest.mark.parametrize("M,K,residual", [(3700, 7168, True), (7200, 7296, False), (2100, 24704, False)])
+def test_norm_of_inputs_past_the_cache(M, K, residual):
+    """Inputs of 104 to 106 MB, which are read with streaming loads; the last rows are wider than the registers."""
+    x, r, w = inputs(M, K, torch.bfloat16, 3)
+    say(f"norm M={M} K={K} residual={residual}, streaming loads")
+    q, s, h, rstd = fq.fp8q_rmsnorm_quant_act_1x128(x, w, residual=r if residual else None)
+    check_norm(q, s, h, rstd, None, (x.float() + r.float()).bfloat16() if residual else x, w, 1e-6, False)
+
+
 def test_norm_of_extreme_rows():
     """Rows of zeros (codes 0 with the product's sign, scale 0), one value in a row, a group of zeros, small and large rows,
     a weight of zeros and negative weights."""
