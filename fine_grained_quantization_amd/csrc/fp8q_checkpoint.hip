@@ -121,8 +121,8 @@ struct TransposeArgs {
 
 // A workgroup takes 128 tokens x 256 channels (the last may have 128): a thread 8 tokens x 8 channels, 64 values in registers
 // between the maxima and the codes, which go through LDS to leave as rows of 128 bytes.  8192 x 7168: 22 us from codes (5.35
-// TB/s), 29 from bf16 (6.0).  Routed to 64 experts (73,000 rows of 7168): 149-160 us for 523 MB written; 490 vector
-// instructions a wave keep the SIMDs busy for two thirds of that.
+// TB/s), 28 from bf16 (6.3).  Routed to 64 experts (73,000 rows of 7168): 124-143 us for 523 MB written (with a branch around
+// each load 149-160); 470 vector instructions a wave keep the SIMDs busy for 0.86 of that.
 template <bool CODES, bool ROUTED>
 __global__ __launch_bounds__(kThreads) void transpose_kernel(TransposeArgs p) {
     __shared__ __align__(16) uint32_t tile[256 * 32];

@@ -104,7 +104,7 @@ __device__ __forceinline__ v4f load4(const void *c, int64_t idx) {
 // Small results: 128 x 128 tiles by 4 waves of 64 x 64, two workgroups to a CU, blocks of 128 tokens through two LDS stages.
 // kParts: the blocks are dealt to several workgroups a tile, whose sums go to the workspace [parts][N][K] in fp32 and are added
 // in order by a second launch.  Bound by the latency of a block's copies (0.6 us, nothing else is on the way): 300 x 576 x 2064
-// (3 blocks) 6.9 us; 16384 x 512 x 512 79 us by 16 workgroups, 15.7 by 256.
+// (3 blocks) 6.8 us; 16384 x 512 x 512 79 us by 16 workgroups, 15.7 by 256.
 // ---------------------------------------------------------------------------------------------------------
 
 constexpr int kTile = 128;
@@ -271,9 +271,9 @@ __global__ __launch_bounds__(256) void wgrad_parts_kernel(WgradArgs p) {
 // A ring of 5 LDS slots of one operand's block each (A0 B0 A1 B1 A2 ...): while block s is multiplied, s + 1 and A's s + 2
 // are on the way or there.  Block s has A in slot 2 s mod 5; A's s + 2 goes where B's s - 1 was, B's s + 2 where A's s was.
 // The scale bytes come straight into registers, a block ahead.
-// 4096 x 18432 x 7168: bf16 390-400 us, 2.7-2.8 PFLOP/s, at the power limit (304 us with zeros for codes); fp32 765-785 us,
-// 1.4 PFLOP/s, 865 where it adds to 528 MB of older results: the matrix cores are busy for 0.58 of the cycles at 1.84 GHz, the
-// conversions and addresses (two vector instructions to one of theirs) fill most of the rest.  64 experts of 1152 rows,
+// 4096 x 18432 x 7168: bf16 383-400 us, 2.7-2.8 PFLOP/s, at the power limit (304 us with zeros for codes); fp32 732-750 us,
+// 1.45 PFLOP/s, 817-842 where it adds to 528 MB of older results: the matrix cores are busy for 0.63 of the cycles at 1.76 GHz,
+// the conversions and addresses (two vector instructions to one of theirs) fill most of the rest.  64 experts of 1152 rows,
 // 2048 x 7168 in bf16: 1030 us, of which 1.9 GB of results cost 300 (722 without the stores).
 // ---------------------------------------------------------------------------------------------------------
 
