@@ -694,9 +694,10 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 
 int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
-// Where 256 x 256 tiles would leave more than half of the CUs without one, 128 x 128 tiles.  (bf16, 4096 tokens: 576 x 7168, 84
-// large tiles, 31 us by small ones; 2048 x 2048 from 2048 tokens, 64, 14.6.)
-bool large_tiles(int64_t E, int64_t N, int64_t K) { return E * tiles_of(N, 256) * tiles_of(K, 256) >= cu_count() / 2; }
+// 128 x 128 tiles where all of them are under way at once, two to a CU; 256 x 256 tiles else.  us by large and by small tiles,
+// 4096 tokens: 576 x 7168 (280 small tiles) bf16 47, 31, fp32 87, 54; 4096 x 2048 (512) 49, 34 and 94, 64; 2816 x 3584 (616)
+// 48, 51 and 94, 85; 4096 x 4096 (1024) 55, 64 and 100, 117.
+bool large_tiles(int64_t E, int64_t N, int64_t K) { return E * tiles_of(N, kTile) * tiles_of(K, kTile) > 2 * cu_count(); }
 
 // Parts of a tile's blocks (small tiles, one product), by estimated time in us: a block of a tile takes 0.6 with one
 // workgroup to a CU and 1.0 with two (fp32: 0.95 and 1.6), a second launch 4, and every part a write and a read of N K sums
