@@ -217,11 +217,17 @@ struct SwigluArgs {
 };
 
 // 1 / (1 + e^-x): the hardware's exponential (an ulp, and |x| / 2 for its argument) and its reciprocal with a Newton step.  Up
-// to 2^126 the sum has a reciprocal that is a normal number; gates below -87 are as good as -87.
+// to 2^126 the sum has a reciprocal that is a normal number; it is held there for gates below kFarGate, whose results still
+// lack far_factor.
+constexpr float kLog2e = 1.44269504088896340736f, kFarGate = -87.0f;
 __device__ __forceinline__ float sigmoid(float x) {
-    const float d = 1.0f + __builtin_amdgcn_exp2f(__builtin_fminf(x * -1.44269504088896340736f, 126.0f));
+    const float d = 1.0f + __builtin_amdgcn_exp2f(__builtin_fminf(x * -kLog2e, 126.0f));
     const float r = __builtin_amdgcn_rcpf(d);
     return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+}
+// e^x / 2^-126 for gates beyond that, which takes p through the subnormal numbers to zero; else exactly 1.
+__device__ __forceinline__ float far_factor(float x) {
+    return __builtin_amdgcn_exp2f(__builtin_fminf(126.0f + x * kLog2e, 0.0f));
 }
 
 // Codes of a token's 128 channels (the 16 lanes of a DPP row) and their scale.
@@ -315,9 +321,19 @@ __global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs
             decode8(x0[j], sx0[j], x);
             decode8(u0[j], su0[j], u);
             widen8(g0[j], gr);
+            float p1[8], least = x[0];
 #pragma unroll
             for (int c = 0; c < 8; c++) {
-                const float sg = sigmoid(x[c]);
+                p1[c] = sigmoid(x[c]);
+                least = __builtin_fminf(least, x[c]);
+            }
+            if (__any(least < kFarGate)) {  // (rare, and the same for the whole wave)
+#pragma unroll
+                for (int c = 0; c < 8; c++) p1[c] *= far_factor(x[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+                const float sg = p1[c];
                 const float silu = x[c] * sg;
                 v[1][j][c] = gr[c] * silu;
                 v[2][j][c] = silu * u[c];

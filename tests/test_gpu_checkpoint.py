@@ -188,6 +188,35 @@ def test_swiglu_gradient_of_large_and_small_gates():
     check_swiglu(fq.fp8q_swiglu_backward_quant(q, s, gh), q, s, gh)
 
 
+def test_swiglu_gradient_of_gates_that_vanish():
+    """Gates around and far below -87, where p = 1 / (1 + e^-x) leaves fp32's normal numbers and then all of them, with inputs
+    and gradients of 1e10 that keep the results normal: the relative bounds of check_swiglu, and what p and x p lose below
+    2^-126 (half a step of 2^-149 each, times |x| and the other factors).  From -110 on p is below 2^-158: zeros."""
+    gates = (80.0, 86.0, 87.2, 87.5, 88.0, 92.0, 97.0, 100.0, 103.0, 110.0, 150.0, 1000.0, 3e38)
+    M, F = 128 * len(gates), 256
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q = torch.full((M, 2 * F), 0x38, dtype=torch.uint8, device="cuda")
+    q[:, :F] = torch.where(torch.rand((M, F), device="cuda", generator=g) < 0.5, 0xB8, 0xB9).to(torch.uint8)  # -1, -1.125
+    s = torch.full((2 * F // 128, M), 1e10, device="cuda")
+    s[:F // 128] = torch.tensor(gates, device="cuda").repeat_interleave(128)
+    gh = (1e10 * torch.randn((M, F), device="cuda", generator=g)).bfloat16()
+    say("swiglu gradient, gates that vanish")
+    gq, gs, gqt, get, hqt, het = fq.fp8q_swiglu_backward_quant(q, s, gh)
+    x, u = decode(q, s).chunk(2, 1)
+    dx, du, h = swiglu_grad64(x, u, gh)
+    xa, ga, ua = x.double().abs(), gh.double().abs(), u.double().abs()
+    rel, least = 2 * (16 + 8 * xa) * U, 2.0 ** -149 * (2 + xa)
+    d = torch.cat([dx, du], 1)
+    t = torch.cat([rel * dx.abs() + least * ga * ua, rel * du.abs() + least * ga], 1)
+    check_rows(gq, gs, d, t)
+    check_copy(gqt, get, d, t)
+    check_copy(hqt, het, h, rel * h.abs() + least * ua)
+    gone = gates.index(110.0) * 128
+    assert float(decode(gq, gs)[gone:].abs().max()) == 0.0 and float(gs[:, gone:].max()) == 0.0
+    for code, byte in ((gqt, get), (hqt, het)):
+        assert int((code[:, gone:] & 0x7F).max()) == 0 and int(byte[gone // 128:].max()) == 0
+
+
 @pytest.mark.parametrize("size", [3e-34, 1e35])
 def test_swiglu_gradient_of_extreme_gradients(size):
     """Groups whose maximum's reciprocal is beyond fp32's normal numbers, or near it.  Every value is within E4M3's half step,
