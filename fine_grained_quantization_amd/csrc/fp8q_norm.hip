@@ -239,6 +239,7 @@ struct NormGradArgs {
 };
 
 constexpr int64_t kFewRows = 128;
+constexpr float kMaxF32 = 3.402823466e38f;
 
 template <bool W_BF16, int THREADS, int CH>
 __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs p) {
@@ -312,7 +313,8 @@ __global__ __launch_bounds__(THREADS) void rmsnorm_backward_kernel(NormGradArgs 
             }
         // (two buffers in turn: a wave may reach the next row's sum while others still read this one)
         const float sum = block_sum<THREADS>(dot, part[flip]);
-        const float f = r * r * sum / (float)p.K;
+        // (r is past 2^64, and its square past fp32, where eps is below 3e-39 and the row small: f itself need not be)
+        const float r2 = r * r, f = r2 <= kMaxF32 ? r2 * sum / (float)p.K : r * (r * (sum / (float)p.K));
 #pragma unroll
         for (int j = 0; j < CH; j++) {
             const int64_t c = t + THREADS * j;

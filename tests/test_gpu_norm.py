@@ -171,6 +171,23 @@ def test_norm_gradient(M, K, w_dtype, residual):
     assert torch.equal(again[0].view(torch.int16), gx.view(torch.int16)) and torch.equal(again[1], gw)
 
 
+@pytest.mark.parametrize("M,K", [(5, 256), (200, 384), (5, 8320)])
+@pytest.mark.parametrize("eps", [1e-37, 1e-40, 1e-44])
+def test_norm_gradient_of_small_rows_and_a_tiny_eps(M, K, eps):
+    """Rows of zeros and of 1e-20 (squares 1e-40): 1 / sqrt(eps) up to 1e22, whose square is no fp32 number.  The bounds are
+    check_grad's; squares of subnormal size do not enter the gradients, which take the returned rstd."""
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    h = (1e-20 * torch.randn((M, K), device="cuda", generator=g)).bfloat16()
+    h[1] = 0
+    w = (1 + 0.1 * torch.randn(K, device="cuda", generator=g)).bfloat16()
+    gy = (1e-12 * torch.randn((M, K), device="cuda", generator=g)).bfloat16()
+    say(f"norm gradient of small rows M={M} K={K} eps={eps}")
+    rstd = fq.fp8q_rmsnorm_quant_act_1x128(h, w, eps=eps)[3]
+    assert bool(torch.isfinite(rstd).all()) and float(rstd.max()) > (2.0 ** 64 if eps < 1e-39 else 1e18)
+    gx, gw = fq.fp8q_rmsnorm_backward(gy, h, w, rstd)
+    check_grad(gx, gw, gy, h, w, rstd, None)
+
+
 def test_norm_gradient_strided_and_in_place():
     h, gres, w = inputs(50, 4096, torch.bfloat16, 4)
     gy = (1e-3 * torch.randn((50, 4096), device="cuda")).bfloat16()
