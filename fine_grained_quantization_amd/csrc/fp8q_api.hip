@@ -481,6 +481,23 @@ int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, co
                                                  static_cast<hipStream_t>(stream)));
 }
 
+// Whether the bytes of `out`, contiguous rows, meet any of `in`'s rows: M of K 2-byte elements, ld elements apart.
+static bool meets_rows(const void *out, const void *in, int64_t ld, int64_t M, int64_t K) {
+    const int64_t o = (int64_t)reinterpret_cast<uintptr_t>(out), i = (int64_t)reinterpret_cast<uintptr_t>(in);
+    const int64_t pitch = ld < (int64_t(1) << 60) ? 2 * ld : int64_t(1) << 61, row = 2 * K, end = o + M * row;
+    if (i >= end) return false;
+    // the last row that begins before the end of `out` (a row that ends behind its beginning, or none does)
+    const int64_t last = (end - i - 1) / pitch < M - 1 ? (end - i - 1) / pitch : M - 1;
+    return i + last * pitch + row > o;
+}
+
+// Whether a kernel that reads rows of `in` and writes the same rows of `out`, a workgroup a row, would write over rows that others
+// still read: they share memory and are not one array.
+static bool writes_over(const void *out, const void *in, int64_t ld, int64_t M, int64_t K) {
+    if (out == in && (ld == K || M == 1)) return false;
+    return meets_rows(out, in, ld, M, K);
+}
+
 int fp8q_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr, const void *w,
                                  int w_dtype, float eps, int pow2, int64_t M, int64_t K, uint16_t *h, uint16_t *y,
                                  uint8_t *q, float *s, float *rstd, void *stream) {
@@ -495,6 +512,10 @@ int fp8q_rmsnorm_quant_act_1x128(const uint16_t *x, int64_t ldx, const uint16_t 
     if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
         !aligned4(s) || !aligned4(rstd))
         return FP8Q_ERR_ALIGN;
+    for (const uint16_t *out : {h, y})
+        if (out && (writes_over(out, x, ldx, M, K) || (residual && writes_over(out, residual, ldr, M, K))))
+            return FP8Q_ERR_OPTION;
+    if (h && y && meets_rows(y, h, K, M, K)) return FP8Q_ERR_OPTION;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_rmsnorm_quant_act_1x128(x, ldx, residual, ldr, w, w_dtype == FP8Q_OUT_BF16, eps,

@@ -484,8 +484,10 @@ int fp8q_grouped_gemm_int8_gather(const int8_t *q, const float *s, int64_t T, co
  *   residual : bf16 [M, K], rows ldr elements apart, or NULL
  *   w        : [K] in w_dtype (FP8Q_OUT_BF16 or FP8Q_OUT_F32)
  *   h        : bf16 [M, K] (output; with a residual only, and then required).  It may
- *              be x or residual itself when that array is contiguous.
- *   y        : bf16 [M, K] (output, or NULL) the normed rows rounded to bf16
+ *              be x or residual itself when that array is contiguous, and may not
+ *              share memory with their rows otherwise (FP8Q_ERR_OPTION).
+ *   y        : bf16 [M, K] (output, or NULL) the normed rows rounded to bf16; like h it
+ *              may not share memory with rows that it is not, nor with h
  *   q, s     : E4M3 [M, K], fp32 [K/128][M] (outputs, or both NULL)
  *   rstd     : fp32 [M] (output, or NULL), what fp8q_rmsnorm_backward takes
  * Requires K % 128 == 0, ldx and ldr >= K and multiples of 8, M < 2^22, a

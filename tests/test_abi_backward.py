@@ -39,6 +39,35 @@ def test_norm(lib, change, want):
     assert lib.fp8q_rmsnorm_quant_act_1x128(*{**NORM, **change}.values()) == want
 
 
+@pytest.mark.parametrize("out", ["h", "y"])
+@pytest.mark.parametrize("which", ["x", "res"])
+def test_norm_over_rows_that_others_read(lib, which, out):
+    """h or y in place of an array whose rows are further apart than theirs, or sharing part of its memory: each row's workgroup
+    would write over rows of others.  (4 rows of 256 elements: 2048 bytes of h or y from 1 << 20 on.)"""
+    base, ld = 1 << 20, "ldx" if which == "x" else "ldr"
+    other = "res" if which == "x" else "x"
+
+    def call(**change):
+        c = {**NORM, other: ctypes.c_void_p(1 << 30), "h": ctypes.c_void_p(1 << 31), out: ctypes.c_void_p(base), **change}
+        return lib.fp8q_rmsnorm_quant_act_1x128(*c.values())
+
+    for at, stride in ((base, 264), (base, 512), (base + 16, 256), (base - 16, 256), (base + 512, 256), (base - 512, 256),
+                       (base + 2032, 256), (base - 2032, 256), (base - 1536 * 2, 768 + 256), (base - 3 * 8192 + 2032, 4096)):
+        assert call(**{which: ctypes.c_void_p(at), ld: stride}) == OPTION, (at - base, stride)
+    # fine: the array itself, one row of any stride, memory before and behind, and between two rows; they pass to the next
+    # check (of the device), which a machine without one fails
+    if not torch.cuda.is_available():
+        for at, stride, M in ((base, 256, 4), (base, 512, 1), (base - 2048, 256, 4), (base + 2048, 256, 4), (base - 512, 2048, 4),
+                              (base + (1 << 25), 512, 4), (base - 4096, (1 << 63) - 8, 4)):
+            assert call(**{which: ctypes.c_void_p(at), ld: stride, "M": M}) not in (OK, NULL, SHAPE, ALIGN, OPTION), (at - base, stride)
+
+
+def test_norm_outputs_apart(lib):
+    for y in (8192, 8192 + 2032, 8192 - 2032):
+        c = {**NORM, "h": ctypes.c_void_p(8192), "y": ctypes.c_void_p(y), "x": ctypes.c_void_p(1 << 20), "res": ctypes.c_void_p(1 << 21)}
+        assert lib.fp8q_rmsnorm_quant_act_1x128(*c.values()) == OPTION
+
+
 GRAD = dict(gy=A, ldg=256, h=A, ldh=256, w=A, dtype=1, rstd=A, gres=None, M=200, K=256, gx=B, gw=B, ws=B, wsb=1 << 20, stream=None)
 
 
