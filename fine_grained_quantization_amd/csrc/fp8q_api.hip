@@ -542,6 +542,8 @@ int fp8q_rmsnorm_backward(const uint16_t *gy, int64_t ldg, const uint16_t *h, in
         return FP8Q_ERR_ALIGN;
     if (M > 0 && (gx == gy || gx == h)) return FP8Q_ERR_OPTION;  // other workgroups may still read them
     if (gw && workspace_bytes < need) return FP8Q_ERR_WORKSPACE;
+    if (M > 0 && (meets_rows(gx, gy, ldg, M, K) || meets_rows(gx, h, ldh, M, K) || (gres && writes_over(gx, gres, K, M, K))))
+        return FP8Q_ERR_OPTION;
     int rc = check_device();
     if (rc) return rc;
     return finish(fp8q::launch_rmsnorm_backward(gy, ldg, h, ldh, w, w_dtype == FP8Q_OUT_BF16, rstd, gres, M, K, gx, gw,

@@ -509,7 +509,8 @@ int64_t fp8q_rmsnorm_backward_workspace_bytes(int64_t M, int64_t K);
  *   rstd : fp32 [M] as the forward call gave it
  *   gres : bf16 [M, K], contiguous, or NULL: the gradient that reaches h past the norm
  *   gx   : bf16 [M, K] (output), the gradient of x and of the residual alike; it may
- *          be gres, and must overlap neither gy nor h (FP8Q_ERR_OPTION if it is one)
+ *          be gres, and shares no memory with gy's and h's rows, nor with gres
+ *          otherwise (FP8Q_ERR_OPTION)
  *   gw   : fp32 [K] (output, or NULL, and then no workspace is needed); 0 when M is 0
  *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, its contents
  *          on entry do not matter (calls that share one must not overlap)

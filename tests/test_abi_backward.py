@@ -84,6 +84,21 @@ def test_norm_gradient(lib, change, want):
     assert lib.fp8q_rmsnorm_backward(*{**GRAD, **change}.values()) == want
 
 
+@pytest.mark.parametrize("which,ld", [("gy", "ldg"), ("h", "ldh"), ("gres", None)])
+def test_norm_gradient_over_rows_that_others_read(lib, which, ld):
+    """gx sharing part of the memory of gy, h or gres (4 rows of 256 elements, 2048 bytes of gx)."""
+    base = 1 << 20
+    c = {**GRAD, "M": 4, "gy": ctypes.c_void_p(1 << 30), "h": ctypes.c_void_p(1 << 31), "gres": ctypes.c_void_p(1 << 32),
+         "gx": ctypes.c_void_p(base)}
+    for at, stride in ((16, 256), (-16, 256), (512, 256), (-512, 256), (2032, 256), (-2032, 256), (-3072, 1024), (0, 512)):
+        if ld is not None or (stride == 256):
+            change = {which: ctypes.c_void_p(base + at), **({ld: stride} if ld else {})}
+            assert lib.fp8q_rmsnorm_backward(*{**c, **change}.values()) == OPTION, (at, stride)
+    if not torch.cuda.is_available():  # fine, up to the check of the device
+        for at in (-2048, 2048) if ld else (-2048, 0, 2048):
+            assert lib.fp8q_rmsnorm_backward(*{**c, which: ctypes.c_void_p(base + at)}.values()) not in (OK, NULL, SHAPE, ALIGN, OPTION)
+
+
 def test_norm_gradient_workspace(lib):
     need = lib.fp8q_rmsnorm_backward_workspace_bytes
     assert need(0, 256) == 0 and need(128, 7168) == 0 and need(129, 256) == 129 * 256 * 4
