@@ -116,7 +116,7 @@ constexpr uint32_t kPow2Round = 0x1FFFFFu;
 __device__ __forceinline__ uint32_t pow2_byte(uint32_t amax) {
     return max((amax + kPow2Round) >> 23, 8u) - 8u;
 }
-// The power itself, and its reciprocal (both exact in fp32 for bytes up to 248, the largest of a finite group; 2^-127 is
+// The power itself, and its reciprocal (both exact in fp32 for bytes up to 247, the largest of a finite group; 2^-127 is
 // subnormal).
 __device__ __forceinline__ float pow2_value(uint32_t byte) {
     return __uint_as_float(byte > 0 ? byte << 23 : 0x00400000u);

@@ -7,8 +7,9 @@
 //  - bf16: v_mfma_scale_f32_16x16x128_f8f6f4, a block of 128 tokens per instruction, scales applied by it.  The E4M3 MFMAs
 //    line their 128 products up before adding them and cut what falls below: each result is 1.4e-5 (relative, rms, for codes
 //    of normal values) off the exact sum, at K = 128 as at K = 32768, without a bias.  That is 1/100 of bf16's own rounding.
-//  - fp32: the codes, times their scales, become bf16 (exactly: 4 significant bits and a power of two) in registers, and
-//    v_mfma_f32_16x16x32_bf16 adds them to 1e-7.  Half of the peak rate.
+//  - fp32: the codes, times their scales, become bf16 (exactly: 4 significant bits and a power of two; bytes 0 to 2 lose what is
+//    below bf16's least step, 2^-133) in registers, and v_mfma_f32_16x16x32_bf16, which takes subnormal numbers as they are,
+//    adds them to 1e-7.  Half of the peak rate.
 #include "fp8q_device.h"
 #include "fp8q_kernels.h"
 #include "fp8q_tiles.h"
@@ -75,7 +76,8 @@ __device__ __forceinline__ void widen16(const v4i &d, float s, v8bf (&o)[2]) {
     o[1] = to_bf16(d[2], d[3], s);
 }
 
-// The power of two of byte j of a scale dword.  (Byte 0, which stands for 2^-127, becomes 0: its group is all zeros.)
+// The power of two of byte j of a scale dword, for the conversions above.  (They read the exponent's bits only: the pattern 0 is
+// byte 0's 2^-127, which groups of zeros have and groups of values up to 448 2^-127.)
 __device__ __forceinline__ float power_of(uint32_t s, int j) { return __uint_as_float(((s >> (8 * j)) & 255u) << 23); }
 
 // 4 results as they are in memory, and in fp32.

@@ -558,9 +558,10 @@ int64_t fp8q_gemm_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int out
  *   dw[n,k] = sum_mb 2^(eg[mb][n] + ex[mb][k] - 254) sum_{m in mb} gt[n,m] xt[k,m]   (+ dw[n,k] if accumulate)
  *   gt : E4M3 [N, M], eg : uint8 [M/128][N];  xt : E4M3 [K, M], ex : uint8 [M/128][K]
  *   dw : [N, K] in out_dtype (output, and input if accumulate is 1)
- * fp32 out: bf16 matrix instructions on the exact values, fp32 sums.  bf16 out: FP8
- * matrix instructions, whose sums are about 1.4e-5 off (relative to a result's rms),
- * rounded once.
+ * fp32 out: bf16 matrix instructions on the values gt 2^(eg - 127) and xt 2^(ex - 127),
+ * which are exact in bf16 (bytes 0 to 2: to its least step, 2^-133; values of 2^128 and
+ * more, from byte 247 on, are infinite), fp32 sums.  bf16 out: FP8 matrix instructions,
+ * whose sums are about 1.4e-5 off (relative to a result's rms), rounded once.
  *   workspace : device memory of workspace_bytes bytes, 16-byte aligned, contents on
  *          entry do not matter (calls that share one must not overlap); NULL will do
  *          when 0 bytes are needed

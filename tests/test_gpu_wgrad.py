@@ -82,6 +82,32 @@ def test_scales_of_every_exponent():
             assert torch.equal(dw, want)
 
 
+@pytest.mark.parametrize("K", [16, 8208])
+@pytest.mark.parametrize("swapped", [False, True])
+def test_every_code_at_the_least_scales(K, swapped):
+    """Bytes 0 (2^-127, with codes that are not zero) to 7, every code, on either side, by both kernels.  One token is not zero, so
+    results are products: exact in the bf16 form but for its rounding; in fp32 from the operand's value in bf16, whose least
+    step is 2^-133 (half of it is lost at most, times the other operand's power)."""
+    M = 128
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], device="cuda").to(torch.uint8).repeat(8)
+    a, ea = torch.zeros((codes.numel(), M), dtype=torch.uint8, device="cuda"), torch.arange(8, device="cuda").repeat_interleave(254)
+    a[:, 9] = codes
+    b, eb = torch.zeros((K, M), dtype=torch.uint8, device="cuda"), 127 + 7 * (torch.arange(K, device="cuda") % 16)
+    b[:, 9] = 0x38  # 1
+    ea, eb = ea.to(torch.uint8).view(1, -1), eb.to(torch.uint8).view(1, -1)
+    values, powers = copy_values(a, ea)[:, 9], copy_values(b, eb)[:, 9]
+    say(f"wgrad of the least scales, K={K} swapped={swapped}")
+    for dtype in (torch.float32, torch.bfloat16):
+        dw = fq.fp8q_gemm_wgrad(b, eb, a, ea, out_dtype=dtype).t() if swapped else fq.fp8q_gemm_wgrad(a, ea, b, eb, out_dtype=dtype)
+        want = values[:, None] * powers
+        if dtype is torch.bfloat16:
+            assert torch.equal(dw, want.to(dtype))
+        else:
+            kept = torch.round(values * 2.0 ** 133) * 2.0 ** -133 == values  # (exact in float64)
+            assert int(kept.sum()) >= 254 * 5 and torch.equal(dw[kept].double(), want[kept])
+            assert bool(((dw.double() - want).abs() <= 2.0 ** -134 * powers).all())
+
+
 def layout(loads, pad_blocks, device="cuda"):
     off = [0]
     for n in loads:
