@@ -188,3 +188,47 @@ def test_gradients_past_4_gib():
     g, x = copy_values(gt, eg), copy_values(xt, ex)
     for e in (0, 17, 31, 32, 39):
         check(dw[e], g[:, 128 * e:128 * e + 128], x[:, 128 * e:128 * e + 128], torch.float32, None, True)
+
+
+# The kernel for large results takes the sizes below by a factor of two at least: they are 1539 and 1089 or more tiles of
+# 128 x 128, the other kernel's up to 512 (two to a CU).
+
+@pytest.mark.parametrize("side", ["rows", "columns"])
+def test_large_results_from_copies_past_2_gib(side):
+    """M * C past 2^31 in either operand of a result of many tiles."""
+    M, n, C = 32768, 272, 65552
+    small, es = copies(n, M, 11, True)
+    big = torch.zeros((C, M), dtype=torch.uint8, device="cuda")
+    eb = torch.full((M // 128, C), 127, dtype=torch.uint8, device="cuda")
+    spans = (0, 40000, 65520, 65536)  # (rows from 65536 on begin past 2^31 bytes)
+    for i, at in enumerate(spans):
+        big[at:at + 16], eb[:, at:at + 16] = copies(16, M, 12 + i, True)
+    some = torch.cat([torch.arange(at, at + 16, device="cuda") for at in spans])
+    want = copy_values(big[some], eb[:, some].contiguous()) @ copy_values(small, es).t()
+    say(f"wgrad of 272 x 65552, operand of 2.1 GB on the side of {side}")
+    for dtype in (torch.float32, torch.bfloat16):
+        if side == "rows":
+            dw = fq.fp8q_gemm_wgrad(big, eb, small, es, out_dtype=dtype)
+        else:
+            dw = fq.fp8q_gemm_wgrad(small, es, big, eb, out_dtype=dtype).t()
+        assert torch.equal(dw[some].double(), want.to(dtype).double())
+        assert int((dw != 0).any(1).sum()) == int((want != 0).any(1).sum())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_segments_of_large_results_that_break_the_rules(dtype, accumulate):
+    """As test_segments_that_break_the_rules, of gradients that have many tiles."""
+    M, N, K = 512, 4112, 4112
+    gt, eg = copies(N, M, 17, True)
+    xt, ex = copies(K, M, 18, True)
+    g, x = copy_values(gt, eg), copy_values(xt, ex)
+    for off, spans in (([-300, 200, 2 ** 31 - 1], [(0, 128), (128, 512)]), ([256, 128, 130, 700], [(0, 0), (128, 128), (128, 512)]),
+                       ([600, 900], [(0, 0)]), ([-2 ** 31, 384], [(0, 384)]), ([0, 512, 0, 512], [(0, 512), (0, 0), (0, 512)])):
+        say(f"wgrad of large results, offsets {off} {dtype} accumulate={accumulate}")
+        o, E = torch.tensor(off, dtype=torch.int32, device="cuda"), len(spans)
+        base = torch.randint(-9, 9, (E, N, K), device="cuda").to(dtype) if accumulate else None
+        dw = base.clone() if accumulate else torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
+        fq.fp8q_grouped_gemm_wgrad(gt, eg, xt, ex, o, out_dtype=dtype, accumulate=accumulate, dw=dw)
+        for e, (a, b) in enumerate(spans):
+            check(dw[e], g[:, a:b], x[:, a:b], dtype, base[e] if accumulate else None, True)
