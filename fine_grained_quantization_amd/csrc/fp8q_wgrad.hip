@@ -383,7 +383,8 @@ constexpr int kFar = 0x60000000;
 template <bool EXACT>
 constexpr int kStores = EXACT ? 32 : 16;
 // Loads of a block's scale bytes; the waits count on these too.  (They are written as the instructions that they become: two
-// loads of neighbouring dwords would be merged, and a wait too short.)
+// loads of neighbouring dwords would be merged, and a wait too short.  tests/test_wgrad_waits.py counts all of them in the
+// compiler's listing.)
 template <bool EXACT>
 constexpr int kScaleLoads = EXACT ? 3 : 2;
 
