@@ -257,7 +257,7 @@ __device__ __forceinline__ float row_codes(const float (&v)[8], uint8_t *q) {
 // Tiles of 128 tokens x 128 channels, a thread 4 tokens x 8 channels of each of the three results: 96 registers of them.  Two
 // workgroups to a CU would leave 128 registers and spill (235-268 us at 4096 x 18432), 1024 threads of 4 x 4 take 215; so one
 // walks tiles b, b + G, ..., with the next tile's inputs on the way (40 more registers) while it computes: 170 us, 4.1 TB/s.
-// What keeps it from a copy's 138: one tile at a time between three barriers, vector instructions for 0.45 of the time.
+// What keeps it from a copy's 138: one tile at a time between three barriers, vector instructions for 0.52 of the time.
 __global__ __launch_bounds__(kThreads, 2) void swiglu_backward_kernel(SwigluArgs p) {
     __shared__ __align__(16) uint32_t tile[3][128 * 32];
     __shared__ __align__(16) uint32_t top[3][128];  // the channels' bytes, as in column_bytes

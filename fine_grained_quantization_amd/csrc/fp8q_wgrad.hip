@@ -273,10 +273,11 @@ __global__ __launch_bounds__(256) void wgrad_parts_kernel(WgradArgs p) {
 // A ring of 5 LDS slots of one operand's block each (A0 B0 A1 B1 A2 ...): while block s is multiplied, s + 1 and A's s + 2
 // are on the way or there.  Block s has A in slot 2 s mod 5; A's s + 2 goes where B's s - 1 was, B's s + 2 where A's s was.
 // The scale bytes come straight into registers, a block ahead.
-// 4096 x 18432 x 7168: bf16 383-400 us, 2.7-2.8 PFLOP/s, at the power limit (304 us with zeros for codes); fp32 732-750 us,
-// 1.45 PFLOP/s, 817-842 where it adds to 528 MB of older results: the matrix cores are busy for 0.63 of the cycles at 1.76 GHz,
-// the conversions and addresses (two vector instructions to one of theirs) fill most of the rest.  64 experts of 1152 rows,
-// 2048 x 7168 in bf16: 1030 us, of which 1.9 GB of results cost 300 (722 without the stores).
+// 4096 x 18432 x 7168: bf16 376-400 us, 2.7-2.9 PFLOP/s, at the power limit (304 us with zeros for codes), 423 where it adds to
+// older results; fp32 732-750 us, 1.45 PFLOP/s, 817-842 where it adds to 528 MB of older results: the matrix cores are busy for
+// 0.69 of the cycles, 0.60 with the older results, at 2.1 GHz; the conversions and addresses (two vector instructions to one of
+// theirs) fill most of the rest.  64 experts of 1152 rows, 2048 x 7168 in bf16: 1030 us, of which 1.9 GB of results cost 300
+// (722 without the stores), 1233 added to older ones; in fp32 1770 and 2200.
 // ---------------------------------------------------------------------------------------------------------
 
 constexpr int kSlot = 256 * 128, kSlots = 5, kMostTiles = 64;
@@ -698,8 +699,9 @@ __global__ __launch_bounds__(512, 2) void wgrad_stream_kernel(WgradArgs p) {
 int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 // 128 x 128 tiles where all of them are under way at once, two to a CU; 256 x 256 tiles else.  us by large and by small tiles,
-// 4096 tokens: 576 x 7168 (280 small tiles) bf16 47, 31, fp32 87, 54; 4096 x 2048 (512) 49, 34 and 94, 64; 2816 x 3584 (616)
-// 48, 51 and 94, 85; 4096 x 4096 (1024) 55, 64 and 100, 117.
+// 4096 tokens: 576 x 7168 (280 small tiles) bf16 47, 29, fp32 87, 52; 4096 x 2048 (512) 50, 34 and 96, 65; 2816 x 3584 (616)
+// 50, 50 and 97, 84; 4096 x 4096 (1024) 51, 61 and 98, 112.  The rule is one for both types: fp32 results just past it lose by
+// it (2816 x 3584; 16 experts of 1024 x 1024, 1024 rows each: 49, 42), bf16 ones do not (27, 31).
 bool large_tiles(int64_t E, int64_t N, int64_t K) { return E * tiles_of(N, kTile) * tiles_of(K, kTile) > 2 * cu_count(); }
 
 // Parts of a tile's blocks (small tiles, one product), by estimated time in us: a block of a tile takes 0.6 with one
